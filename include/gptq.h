@@ -256,6 +256,162 @@ gptq_status gptq_dequant_matmul(const void* X, gptq_dtype x_dtype, int64_t n,
                                 float* Y, int64_t ldy, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The transposed dequantizing matmul: the gradient of gptq_dequant_matmul
+ * with respect to its activations, through the frozen packed weights.
+ *
+ *   dX[k][c] = sum_r dY[k][r] * W_hat[r][c]
+ *
+ * dY: bf16 [n, m], row stride lddy >= m (GPTQ_BF16 only); 0 <= n <= 524280.
+ * qweight .. signed_codes: the stored format, as in gptq_dequant_matmul.
+ * dX: bf16 [n, d], row stride lddx >= d; fully overwritten.
+ * W_hat is rounded to bf16 once (by at most 2^-8 of it, as dX itself is when
+ * stored); products are exact, sums fp32, rounded to bf16 at the end.
+ * ws: at least gptq_dequant_matmul_t_workspace_bytes(n, m, d) bytes.
+ * Errors: INVALID_ARG (bad sizes, m or d > 65535, dtype, bits, group_size,
+ *         NULL pointers when n > 0); WORKSPACE; HIP.
+ * ------------------------------------------------------------------------- */
+size_t gptq_dequant_matmul_t_workspace_bytes(int64_t n, int64_t m, int64_t d);
+gptq_status gptq_dequant_matmul_t(const void* dY, gptq_dtype dy_dtype, int64_t n,
+                                  int64_t m, int64_t lddy, const uint32_t* qweight,
+                                  const void* scales, gptq_dtype scale_dtype,
+                                  const uint8_t* zeros, const int32_t* g_idx,
+                                  int64_t d, int32_t bits, int32_t group_size,
+                                  int32_t signed_codes, void* dX, int64_t lddx,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters beside the packed weights, for activation rows of many
+ * requests at once: row k goes through the shared product and through the
+ * adapter a = row[k] of its own request,
+ *
+ *   H[k] = X[k] A_a^T                                    (rank values)
+ *   Y[k] = X[k] W_hat^T + alpha_a H[k] B_a^T
+ *
+ * A row whose id is outside [0, n_adapters) (for instance -1) has none: its
+ * H is 0 and its Y the shared product alone.  Rows may name adapters in any
+ * order; rows of one adapter that follow each other share its loads.
+ * Adapters of a smaller rank are stored with zeros up to `rank`.
+ *
+ * X: bf16 [n, d], row stride ldx >= d; 0 <= n <= 524280; qweight ..
+ * signed_codes: as in gptq_dequant_matmul; H: fp32 [n, rank] contiguous, or
+ * NULL (gptq_lora_backward needs it); Y: [n, m] of y_dtype GPTQ_F32 or
+ * GPTQ_BF16 (rounded once, at the end), row stride ldy >= m.  Both are fully
+ * overwritten.
+ * The shared product is gptq_dequant_matmul's: exact codes and activations,
+ * fp32 sums per group; H is summed and kept in fp32 and enters its product
+ * with B as three bf16 parts, i.e. exactly.
+ * ws: at least gptq_lora_workspace_bytes(n, m, d, rank) bytes.
+ * Errors: INVALID_ARG (bad sizes, m or d > 65535, rank outside 1 .. 128,
+ *         n_adapters outside 1 .. 65535, dtype, bits, group_size, NULL
+ *         pointers when n > 0); WORKSPACE; HIP.
+ * ------------------------------------------------------------------------- */
+typedef struct gptq_adapters {
+  const void* A;        /* DEVICE bf16 [n_adapters, rank, d] contiguous  */
+  const void* B;        /* DEVICE bf16 [n_adapters, m, rank] contiguous  */
+  const float* alpha;   /* DEVICE fp32 [n_adapters]                       */
+  const int32_t* row;   /* DEVICE int32 [n]: adapter of each row          */
+  int32_t n_adapters;
+  int32_t rank;
+} gptq_adapters;
+
+size_t gptq_lora_workspace_bytes(int64_t n, int64_t m, int64_t d, int32_t rank);
+gptq_status gptq_lora_matmul(const void* X, gptq_dtype x_dtype, int64_t n, int64_t d,
+                             int64_t ldx, const uint32_t* qweight, const void* scales,
+                             gptq_dtype scale_dtype, const uint8_t* zeros,
+                             const int32_t* g_idx, int64_t m, int32_t bits,
+                             int32_t group_size, int32_t signed_codes,
+                             const gptq_adapters* adapters /*[host]*/, float* H,
+                             void* Y, gptq_dtype y_dtype, int64_t ldy, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Gradients of gptq_lora_matmul, given dY = d loss / d Y.  With a = row[k],
+ *
+ *   G[k]  = alpha_a dY[k] B_a
+ *   dX[k] = dY[k] W_hat + G[k] A_a
+ *   dA_a  = sum over the rows k of a  G[k]^T X[k]
+ *   dB_a  = alpha_a sum over the rows k of a  dY[k]^T H[k]
+ *
+ * dY: bf16 [n, m], row stride lddy >= m; X: bf16 [n, d], row stride ldx >= d;
+ * H: fp32 [n, rank], as gptq_lora_matmul wrote it (read for dB only).
+ * dX: bf16 [n, d], row stride lddx >= d, or NULL; rounded as in
+ * gptq_dequant_matmul_t.  dA: fp32 [n_adapters, rank, d] or NULL; dB: fp32
+ * [n_adapters, m, rank] or NULL.  accumulate = 1 adds to dA and dB (gradients
+ * over several micro-batches) instead of overwriting them; adapters without a
+ * row get 0 (nothing added).  G and H enter as three bf16 parts, i.e. exactly;
+ * sums fp32, over rows in an order fixed by the sizes and ids alone.  With
+ * n = 0 the outputs are written (zeros, unless accumulating).
+ * ws: at least gptq_lora_backward_workspace_bytes(...) bytes.
+ * Errors: as gptq_lora_matmul (a pointer that only an output left NULL would
+ *         read may be NULL).
+ * ------------------------------------------------------------------------- */
+size_t gptq_lora_backward_workspace_bytes(int64_t n, int64_t m, int64_t d, int32_t rank,
+                                          int32_t n_adapters);
+gptq_status gptq_lora_backward(const void* dY, gptq_dtype dy_dtype, int64_t n, int64_t m,
+                               int64_t lddy, const void* X, int64_t ldx, const float* H,
+                               const uint32_t* qweight, const void* scales,
+                               gptq_dtype scale_dtype, const uint8_t* zeros,
+                               const int32_t* g_idx, int64_t d, int32_t bits,
+                               int32_t group_size, int32_t signed_codes,
+                               const gptq_adapters* adapters /*[host]*/, void* dX,
+                               int64_t lddx, float* dA, float* dB, int32_t accumulate,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Distillation from a teacher's top logits: how far a student's logits are
+ * from a teacher's of whom only the k largest logits of each row are known
+ * (the unquantized model's, kept once), and the gradient that trains the
+ * student's adapters towards it.  With z = logits / T, q = softmax(z) over the
+ * vocabulary, S the row's known ids and t their logits,
+ *
+ *   t_lse NULL:  p = softmax of t / T over S
+ *     loss = w T^2 sum_S p (log p - log q)
+ *     d loss / d logits_v = w T (q_v - p_v)
+ *   t_lse given (the teacher's log-sum-exp of its logits / T over the whole
+ *   vocabulary): p = exp(t / T - t_lse), and what is left, p_r = max(0, 1 -
+ *   sum_S p), is one more class against the student's q_r = 1 - sum_S q
+ *     loss = w T^2 [sum_S p (log p - log q) + p_r (log p_r - log q_r)]
+ *     d loss / d logits_v = w T (q_v - p_v) on S, w T q_v (1 - p_r / q_r)
+ *     elsewhere; without student mass outside S that class is left out.
+ *
+ * logits: [n, vocab] of dtype GPTQ_BF16, GPTQ_F16 or GPTQ_F32, row stride ldl
+ *   >= vocab; 1 <= vocab <= 262144; n <= 2097152.
+ * t_idx int32 [n, k], t_logits fp32 [n, k]: contiguous, 1 <= k <= 1024.  Ids
+ *   outside [0, vocab) are padding.  The known ids of a row are meant to be
+ *   distinct; one named twice counts both its entries' probabilities.  A row
+ *   without any known id has loss 0 and (t_lse NULL or p_r = 1) gradient 0.
+ * weight: fp32 [n] or NULL (1).  A row of weight 0 is not read: its loss,
+ *   stats and gradient are 0 whatever its logits hold.
+ * A logit of -inf has probability 0 (a masked token); one that the teacher
+ *   gives probability makes the loss +inf.  NaN, +inf and a row of nothing
+ *   but -inf give NaN.
+ * loss: fp32 [n].  stats: fp32 [n, 2] or NULL: the log-sum-exp of z over the
+ *   vocabulary and over the ids outside S (t_lse NULL: the same), for
+ *   gptq_distill_backward.  dlogits: d sum(loss) / d logits in the logits'
+ *   dtype, row stride ldd >= vocab, or NULL; it may be the logits' own buffer
+ *   (same pointer and stride).
+ * Cells are exponentiated and summed in fp32 (fp64 across threads), all that
+ * is per row or known id in fp64.  Allocates nothing; no workspace.
+ * Errors: INVALID_ARG (bad sizes, dtype, temperature not positive and finite,
+ *         NULL pointers when n > 0); HIP.
+ * ------------------------------------------------------------------------- */
+gptq_status gptq_distill_loss(const void* logits, gptq_dtype dtype, int64_t n,
+                              int64_t vocab, int64_t ldl, const int32_t* t_idx,
+                              const float* t_logits, int64_t k, float temperature,
+                              const float* t_lse, const float* weight, float* loss,
+                              float* stats, void* dlogits, int64_t ldd, void* stream);
+/* The gradient by itself, from the stats that gptq_distill_loss wrote for the
+ * same arguments: dlogits[k] = grad[k] d loss[k] / d logits[k], grad fp32 [n]
+ * = the derivative of the caller's scalar with respect to loss[k].  Arguments
+ * and errors otherwise as in gptq_distill_loss. */
+gptq_status gptq_distill_backward(const void* logits, gptq_dtype dtype, int64_t n,
+                                  int64_t vocab, int64_t ldl, const float* stats,
+                                  const int32_t* t_idx, const float* t_logits, int64_t k,
+                                  float temperature, const float* t_lse,
+                                  const float* weight, const float* grad, void* dlogits,
+                                  int64_t ldd, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Layer by layer ([derivation] 3.2 steps 1-2 and 10: capture each layer's
  * inputs, quantize it, verify its reconstruction error, go on to the next;
  * [teardown] "layer-wise quantization").

@@ -21,3 +21,4 @@ in ``gptq_ref``'s header.
 """
 
 from .gptq_ref import *  # noqa: F401,F403
+from .adapters_ref import *  # noqa: F401,F403

@@ -18,7 +18,10 @@ __all__ = [
     "GPTQError", "lib_path", "load_library", "gptq_hessian_accumulate",
     "gptq_cholesky_inverse", "gptq_quantize_layer", "gptq_workspace_bytes",
     "gptq_hessian_workspace_bytes", "gptq_factor_workspace_bytes",
-    "gptq_hessian_accumulate_noalloc", "gptq_dequant_matmul", "gptq_quantize_stack",
+    "gptq_hessian_accumulate_noalloc", "gptq_dequant_matmul", "gptq_dequant_matmul_t",
+    "gptq_lora_matmul", "gptq_lora_backward", "gptq_lora_workspace_bytes",
+    "gptq_lora_backward_workspace_bytes", "gptq_dequant_matmul_t_workspace_bytes",
+    "gptq_distill_loss", "gptq_distill_backward", "gptq_quantize_stack",
     "gptq_trace_enable", "gptq_trace_read", "TRACE_PHASES",
     "EXPORTED_SYMBOLS", "GRIDS", "ACTIVATIONS", "GPTQ_OK", "GPTQ_ERR_INVALID_ARG", "GPTQ_ERR_NOT_SPD",
     "GPTQ_ERR_WORKSPACE", "GPTQ_ERR_HIP",
@@ -34,7 +37,9 @@ EXPORTED_SYMBOLS = (
     "gptq_cholesky_inverse", "gptq_workspace_bytes", "gptq_quantize_layer",
     "gptq_hessian_accumulate_noalloc", "gptq_dequant_matmul",
     "gptq_stack_workspace_bytes", "gptq_quantize_stack", "gptq_trace_enable",
-    "gptq_trace_read",
+    "gptq_trace_read", "gptq_dequant_matmul_t_workspace_bytes", "gptq_dequant_matmul_t",
+    "gptq_lora_workspace_bytes", "gptq_lora_matmul", "gptq_lora_backward_workspace_bytes",
+    "gptq_lora_backward", "gptq_distill_loss", "gptq_distill_backward",
 )
 TRACE_PHASES = ("stats", "factor", "chain", "lazy", "other")
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2}
@@ -68,6 +73,12 @@ class _StackLayer(ctypes.Structure):
                 ("zeros", ctypes.c_void_p), ("g_idx", ctypes.c_void_p)]
 
 
+class _Adapters(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("alpha", ctypes.c_void_p),
+                ("row", ctypes.c_void_p), ("n_adapters", ctypes.c_int32),
+                ("rank", ctypes.c_int32)]
+
+
 def lib_path() -> str:
     return os.path.join(_HERE, "libgptq_hip.so")
 
@@ -96,6 +107,29 @@ def load_library():
     lib.gptq_dequant_matmul.restype = ctypes.c_int
     lib.gptq_dequant_matmul.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, ctypes.c_int,
                                         vp, vp, i64, i32, i32, i32, vp, i64, vp]
+    ap = ctypes.POINTER(_Adapters)
+    dt = ctypes.c_int
+    lib.gptq_dequant_matmul_t_workspace_bytes.restype = sz
+    lib.gptq_dequant_matmul_t_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.gptq_dequant_matmul_t.restype = ctypes.c_int
+    lib.gptq_dequant_matmul_t.argtypes = [vp, dt, i64, i64, i64, vp, vp, dt, vp, vp, i64, i32, i32,
+                                          i32, vp, i64, vp, sz, vp]
+    lib.gptq_lora_workspace_bytes.restype = sz
+    lib.gptq_lora_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.gptq_lora_matmul.restype = ctypes.c_int
+    lib.gptq_lora_matmul.argtypes = [vp, dt, i64, i64, i64, vp, vp, dt, vp, vp, i64, i32, i32, i32,
+                                     ap, vp, vp, dt, i64, vp, sz, vp]
+    lib.gptq_lora_backward_workspace_bytes.restype = sz
+    lib.gptq_lora_backward_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    lib.gptq_lora_backward.restype = ctypes.c_int
+    lib.gptq_lora_backward.argtypes = [vp, dt, i64, i64, i64, vp, i64, vp, vp, vp, dt, vp, vp, i64,
+                                       i32, i32, i32, ap, vp, i64, vp, vp, i32, vp, sz, vp]
+    lib.gptq_distill_loss.restype = ctypes.c_int
+    lib.gptq_distill_loss.argtypes = [vp, dt, i64, i64, i64, vp, vp, i64, f32, vp, vp, vp, vp, vp,
+                                      i64, vp]
+    lib.gptq_distill_backward.restype = ctypes.c_int
+    lib.gptq_distill_backward.argtypes = [vp, dt, i64, i64, i64, vp, vp, vp, i64, f32, vp, vp, vp,
+                                          vp, i64, vp]
     sp = ctypes.POINTER(_StackLayer)
     lib.gptq_stack_workspace_bytes.restype = sz
     lib.gptq_stack_workspace_bytes.argtypes = [sp, i32, i64]
@@ -374,6 +408,268 @@ def gptq_dequant_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
                                     _dev_ptr(Y), m, _stream(dev))
     _check(st, "gptq_dequant_matmul")
     return Y
+
+
+# ---------------------------------------------------------------------------
+# Adapters beside the packed weights, and the loss that trains them
+# ---------------------------------------------------------------------------
+
+_F32, _BF16 = torch.float32, torch.bfloat16
+
+
+def _gpu_rows(t, name, cols=None, dtypes=(_BF16,)):
+    """Checks a [rows, cols] tensor on the GPU; returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [rows, {'cols' if cols is None else cols}], "
+                         f"got {tuple(t.shape)}")
+    return _row_stride(t, name) if t.shape[0] else t.shape[1]
+
+
+def _gpu_device(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU (no host path exists)")
+    return t.device
+
+
+def _check_packed(qweight, scales, zeros, g_idx, bits, group_size, m, d, dev):
+    """Checks the stored format of an [m, d] layer; returns the scales' type code."""
+    if bits not in (2, 3, 4, 8) or not (group_size == -1 or group_size > 0):
+        raise GPTQError(GPTQ_ERR_INVALID_ARG, "bits / group_size")
+    ng = 1 if group_size == -1 else -(-d // group_size)
+    if qweight.dtype not in (torch.int32, torch.uint32):
+        raise TypeError("qweight must be int32/uint32")
+    _expect(qweight, "qweight", qweight.dtype, (m, -(-d * bits // 32)), dev)
+    if scales.dtype not in (_F32, torch.float16):
+        raise TypeError("scales must be float32 or float16")
+    _expect(scales, "scales", scales.dtype, (m, ng), dev)
+    _expect(zeros, "zeros", torch.uint8, (m, ng), dev)
+    _expect(g_idx, "g_idx", torch.int32, (d,), dev)
+    return GPTQ_F16 if scales.dtype == torch.float16 else GPTQ_F32
+
+
+def _check_adapters(A, B, adapter, alpha, n, m, d, dev):
+    """Checks a set of adapters; returns its descriptor."""
+    if A.dim() != 3 or A.shape[2] != d:
+        raise ValueError(f"A must be [n_adapters, rank, {d}], got {tuple(A.shape)}")
+    count, rank = A.shape[0], A.shape[1]
+    _expect(A, "A", _BF16, (count, rank, d), dev)
+    _expect(B, "B", _BF16, (count, m, rank), dev)
+    _expect(adapter, "adapter", torch.int32, (n,), dev)
+    _expect(alpha, "alpha", _F32, (count,), dev)
+    return _Adapters(A.data_ptr(), B.data_ptr(), alpha.data_ptr(), adapter.data_ptr(), count, rank)
+
+
+def _out(t, name, dtype, shape, dev):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _expect(t, name, dtype, shape, dev)
+    return t
+
+
+def _enough(ws, need, dev):
+    if ws is None or ws.numel() * ws.element_size() < need:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous() or ws.data_ptr() % 16:
+        raise ValueError(f"ws must be contiguous, 16-byte aligned, on {dev}")
+    return ws
+
+
+def _launch(dev, where, fn, *args):
+    """Calls a library function with the stream of `dev` last, `dev` being the
+    current device for the launch."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != GPTQ_OK:
+        raise GPTQError(st, where)
+
+
+def gptq_lora_workspace_bytes(n: int, m: int, d: int, rank: int) -> int:
+    return int(_lib().gptq_lora_workspace_bytes(n, m, d, rank))
+
+
+def gptq_lora_backward_workspace_bytes(n: int, m: int, d: int, rank: int, n_adapters: int) -> int:
+    return int(_lib().gptq_lora_backward_workspace_bytes(n, m, d, rank, n_adapters))
+
+
+def gptq_dequant_matmul_t_workspace_bytes(n: int, m: int, d: int) -> int:
+    return int(_lib().gptq_dequant_matmul_t_workspace_bytes(n, m, d))
+
+
+def gptq_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                     zeros: torch.Tensor, g_idx: torch.Tensor, bits: int, group_size: int,
+                     A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor,
+                     alpha: torch.Tensor, signed: bool = False, Y=None, H=None,
+                     want_h: bool = False, out_dtype=torch.float32, ws=None):
+    """Y [n, m] = X W_hat^T + alpha_a (X A_a^T) B_a^T, a = adapter[row].
+
+    X bf16 [n, d] and the stored format as in gptq_dequant_matmul; A bf16
+    [n_adapters, rank, d], B bf16 [n_adapters, m, rank], alpha fp32
+    [n_adapters], adapter int32 [n] (an id outside [0, n_adapters), e.g. -1:
+    the shared product alone).  Y is float32 or bfloat16 (out_dtype, or the
+    given Y's).  Returns Y, or (Y, H) with H = X A_a^T fp32 [n, rank] when
+    want_h is set or H is given (gptq_lora_backward needs it)."""
+    ldx = _gpu_rows(X, "X")
+    dev = _gpu_device(X)
+    n, d = X.shape
+    m = qweight.shape[0]
+    sdt = _check_packed(qweight, scales, zeros, g_idx, bits, group_size, m, d, dev)
+    ad = _check_adapters(A, B, adapter, alpha, n, m, d, dev)
+    if Y is not None:
+        out_dtype = Y.dtype
+    if out_dtype is not _F32 and out_dtype is not _BF16:
+        raise TypeError(f"Y must be float32 or bfloat16, got {out_dtype}")
+    lib = _lib()
+    need = lib.gptq_lora_workspace_bytes(n, m, d, ad.rank)
+    ws = _enough(ws, need, dev)
+    Y = _out(Y, "Y", out_dtype, (n, m), dev)
+    if want_h or H is not None:
+        H = _out(H, "H", _F32, (n, ad.rank), dev)
+    _launch(dev, "gptq_lora_matmul", lib.gptq_lora_matmul, X.data_ptr(), GPTQ_BF16, n, d, ldx,
+            qweight.data_ptr(), scales.data_ptr(), sdt, zeros.data_ptr(), g_idx.data_ptr(), m, bits,
+            group_size, 1 if signed else 0, ctypes.byref(ad), None if H is None else H.data_ptr(),
+            Y.data_ptr(), GPTQ_F32 if out_dtype is _F32 else GPTQ_BF16, m, ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    return Y if H is None else (Y, H)
+
+
+def gptq_lora_backward(dY: torch.Tensor, X: torch.Tensor, H, qweight: torch.Tensor,
+                       scales: torch.Tensor, zeros: torch.Tensor, g_idx: torch.Tensor, bits: int,
+                       group_size: int, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor,
+                       alpha: torch.Tensor, signed: bool = False, need_dx: bool = True,
+                       need_dab: bool = True, dX=None, dA=None, dB=None, accumulate: bool = False,
+                       ws=None):
+    """Gradients of gptq_lora_matmul from dY bf16 [n, m]: (dX bf16 [n, d], dA
+    fp32 like A, dB fp32 like B), None for those not needed.  H as the
+    forward call returned it (only read for dB).  accumulate adds to the given
+    dA and dB instead of overwriting them."""
+    ldy = _gpu_rows(dY, "dY")
+    dev = _gpu_device(dY)
+    n, m = dY.shape
+    d = A.shape[-1]
+    sdt = _check_packed(qweight, scales, zeros, g_idx, bits, group_size, m, d, dev)
+    ad = _check_adapters(A, B, adapter, alpha, n, m, d, dev)
+    ldx = d
+    if need_dab:
+        ldx = _gpu_rows(X, "X", d)
+        if X.shape[0] != n or X.device != dev:
+            raise ValueError(f"X must be [{n}, {d}] on {dev}")
+        _expect(H, "H", _F32, (n, ad.rank), dev)
+        if accumulate and (dA is None or dB is None):
+            raise ValueError("accumulate needs dA and dB")
+        dA = _out(dA, "dA", _F32, tuple(A.shape), dev)
+        dB = _out(dB, "dB", _F32, tuple(B.shape), dev)
+    else:
+        dA = dB = None
+    dX = _out(dX, "dX", _BF16, (n, d), dev) if need_dx else None
+    lib = _lib()
+    need = lib.gptq_lora_backward_workspace_bytes(n, m, d, ad.rank, ad.n_adapters)
+    ws = _enough(ws, need, dev)
+    _launch(dev, "gptq_lora_backward", lib.gptq_lora_backward, dY.data_ptr(), GPTQ_BF16, n, m, ldy,
+            X.data_ptr() if need_dab else None, ldx, H.data_ptr() if need_dab else None,
+            qweight.data_ptr(), scales.data_ptr(), sdt, zeros.data_ptr(), g_idx.data_ptr(), d, bits,
+            group_size, 1 if signed else 0, ctypes.byref(ad),
+            dX.data_ptr() if need_dx else None, d, dA.data_ptr() if need_dab else None,
+            dB.data_ptr() if need_dab else None, 1 if accumulate else 0, ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    return dX, dA, dB
+
+
+def gptq_dequant_matmul_t(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                          zeros: torch.Tensor, g_idx: torch.Tensor, bits: int, group_size: int,
+                          signed: bool = False, dX=None, ws=None) -> torch.Tensor:
+    """dX bf16 [n, d] = dY W_hat for dY bf16 [n, m]: the gradient of
+    gptq_dequant_matmul with respect to its activations."""
+    ldy = _gpu_rows(dY, "dY")
+    dev = _gpu_device(dY)
+    n, m = dY.shape
+    d = g_idx.shape[0]
+    sdt = _check_packed(qweight, scales, zeros, g_idx, bits, group_size, m, d, dev)
+    lib = _lib()
+    ws = _enough(ws, lib.gptq_dequant_matmul_t_workspace_bytes(n, m, d), dev)
+    dX = _out(dX, "dX", _BF16, (n, d), dev)
+    _launch(dev, "gptq_dequant_matmul_t", lib.gptq_dequant_matmul_t, dY.data_ptr(), GPTQ_BF16, n, m,
+            ldy, qweight.data_ptr(), scales.data_ptr(), sdt, zeros.data_ptr(), g_idx.data_ptr(), d,
+            bits, group_size, 1 if signed else 0, dX.data_ptr(), d, ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    return dX
+
+
+_LOGITS = {torch.bfloat16: GPTQ_BF16, torch.float16: GPTQ_F16, torch.float32: GPTQ_F32}
+
+
+def _check_distill(logits, t_idx, t_logits, t_lse, weight):
+    ldl = _gpu_rows(logits, "logits", None, tuple(_LOGITS))
+    dev = _gpu_device(logits)
+    n = logits.shape[0]
+    if t_idx.dim() != 2:
+        raise ValueError("t_idx must be [n, k]")
+    k = t_idx.shape[1]
+    _expect(t_idx, "t_idx", torch.int32, (n, k), dev)
+    _expect(t_logits, "t_logits", _F32, (n, k), dev)
+    if t_lse is not None:
+        _expect(t_lse, "t_lse", _F32, (n,), dev)
+    if weight is not None:
+        _expect(weight, "weight", _F32, (n,), dev)
+    return ldl, dev, n, k
+
+
+def _dlogits(t, logits, dev):
+    """The gradient's tensor (the logits' own is allowed) and its row stride."""
+    if t is None:
+        t = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    ldd = _gpu_rows(t, "dlogits", logits.shape[1], (logits.dtype,))
+    if t.shape != logits.shape or t.device != dev:
+        raise ValueError(f"dlogits must be {tuple(logits.shape)} on {dev}")
+    return t, ldd
+
+
+def gptq_distill_loss(logits: torch.Tensor, t_idx: torch.Tensor, t_logits: torch.Tensor,
+                      temperature: float = 1.0, t_lse=None, weight=None, want_grad: bool = False,
+                      dlogits=None) -> dict:
+    """Divergence of the student's logits [n, vocab] (bfloat16, float16 or
+    float32) from a teacher known by the logits t_logits fp32 [n, k] at the ids
+    t_idx int32 [n, k] (outside [0, vocab): padding), per row, times weight and
+    temperature^2.  t_lse fp32 [n], the teacher's log-sum-exp of its logits /
+    temperature, makes what the known ids leave one more class; without it
+    the known ids are renormalised.  Returns {"loss": fp32 [n], "stats": fp32
+    [n, 2] (for gptq_distill_backward), "dlogits": the gradient of
+    sum(loss), or None}; dlogits may be the logits' own tensor."""
+    ldl, dev, n, k = _check_distill(logits, t_idx, t_logits, t_lse, weight)
+    ldd = 0
+    if want_grad or dlogits is not None:
+        dlogits, ldd = _dlogits(dlogits, logits, dev)
+    loss = torch.empty(n, dtype=_F32, device=dev)
+    stats = torch.empty(n, 2, dtype=_F32, device=dev)
+    _launch(dev, "gptq_distill_loss", _lib().gptq_distill_loss, logits.data_ptr(),
+            _LOGITS[logits.dtype], n, logits.shape[1], ldl, t_idx.data_ptr(), t_logits.data_ptr(), k,
+            temperature, None if t_lse is None else t_lse.data_ptr(),
+            None if weight is None else weight.data_ptr(), loss.data_ptr(), stats.data_ptr(),
+            None if dlogits is None else dlogits.data_ptr(), ldd)
+    return dict(loss=loss, stats=stats, dlogits=dlogits)
+
+
+def gptq_distill_backward(logits: torch.Tensor, stats: torch.Tensor, t_idx: torch.Tensor,
+                          t_logits: torch.Tensor, grad: torch.Tensor, temperature: float = 1.0,
+                          t_lse=None, weight=None, dlogits=None) -> torch.Tensor:
+    """dlogits = grad[row] d loss[row] / d logits from the stats of
+    gptq_distill_loss on the same arguments; grad fp32 [n]."""
+    ldl, dev, n, k = _check_distill(logits, t_idx, t_logits, t_lse, weight)
+    _expect(stats, "stats", _F32, (n, 2), dev)
+    _expect(grad, "grad", _F32, (n,), dev)
+    dlogits, ldd = _dlogits(dlogits, logits, dev)
+    _launch(dev, "gptq_distill_backward", _lib().gptq_distill_backward, logits.data_ptr(),
+            _LOGITS[logits.dtype], n, logits.shape[1], ldl, stats.data_ptr(), t_idx.data_ptr(),
+            t_logits.data_ptr(), k, temperature, None if t_lse is None else t_lse.data_ptr(),
+            None if weight is None else weight.data_ptr(), grad.data_ptr(), dlogits.data_ptr(), ldd)
+    return dlogits
 
 
 def gptq_quantize_stack(Ws, X: torch.Tensor, params, activation: str = "none",

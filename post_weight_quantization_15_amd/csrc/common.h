@@ -173,6 +173,41 @@ gptq_status launch_dequant_matmul(const uint16_t* X, int64_t ldx, int64_t n,
                                   int64_t ldy, int out_bf16, int act,
                                   hipStream_t st);
 
+// The packed format a product reads (qweight [m][words], scales / zeros
+// [m][ng], g_idx [d]).
+struct Packed {
+  const uint32_t* qw;
+  const void* scales;
+  const uint8_t* zeros;
+  const int32_t* g_idx;
+  int64_t m, d, ng;
+  int bits, group, scale_f16, sgn;
+};
+constexpr int64_t kMaxRows = int64_t(65535) * 8;   // activation rows of a product
+constexpr int kMaxRank = 128;
+
+// Y = X W_hat^T + alpha H B^T, H = X A^T (k_lora.hip); H may be NULL.
+size_t lora_ws_bytes(int64_t n, int64_t m, int64_t d, int rank);
+gptq_status launch_lora(const uint16_t* X, int64_t ldx, int64_t n, const Packed& w,
+                        const gptq_adapters& ad, float* H, void* Y, int out_bf16, int64_t ldy,
+                        void* ws, hipStream_t st);
+// dX = dY W_hat (+ G A with adapters), dA, dB; any of the three may be NULL.
+size_t lora_backward_ws_bytes(int64_t n, int64_t m, int64_t d, int rank, int n_adapters);
+gptq_status launch_lora_backward(const uint16_t* dY, int64_t lddy, int64_t n, const uint16_t* X,
+                                 int64_t ldx, const float* H, const Packed& w,
+                                 const gptq_adapters* ad, uint16_t* dX, int64_t lddx, float* dA,
+                                 float* dB, int accumulate, void* ws, hipStream_t st);
+
+// The distillation loss and its gradient (k_distill.hip): the loss, with the
+// gradient where dlogits is given; with grad the gradient alone from stats.
+constexpr int kDistillMaxK = 1024;
+constexpr int64_t kDistillMaxVocab = 262144;
+gptq_status launch_distill(const void* logits, gptq_dtype dt, int64_t n, int64_t vocab,
+                           int64_t ldl, const int32_t* t_idx, const float* t_logits, int64_t k,
+                           float temp, const float* t_lse, const float* weight,
+                           const float* grad, float* loss, float* stats, void* dlogits,
+                           int64_t ldd, hipStream_t st);
+
 // Tracing (trace.hip): per-phase event pairs on the caller's stream while
 // enabled.  trace_begin returns a token (-1 when off) for trace_end.
 constexpr int kTracePhases = GPTQ_TRACE_PHASES;

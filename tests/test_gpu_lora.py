@@ -1,0 +1,450 @@
+"""The adapter products against the oracle's float64 products on the same
+stored bytes: Y = X W_hat^T + alpha_a (X A_a^T) B_a^T, its gradients, and the
+transposed dequantizing product.
+
+Tolerances count roundings, entrywise, u = 2^-24 for fp32 and 2^-8 for bf16
+(half a step of it).  Products of bf16 numbers, and of an activation and a
+code, are exact in fp32; what is rounded are sums, steps times sums, and the
+outputs:
+  shared part   (d + 16) u sum |x| Delta (|code| + |zero|), as for the
+                dequantizing matmul (16 covers the per-group fold)
+  H             (d + 16) u sum |x| |A|, a sum of d exact products
+  adapter part  its inputs' error carried through B, and (r + 16) u of
+                alpha sum |H| |B| (H enters as three bf16 parts: 2^-24)
+  dX            W_hat is rounded to bf16: 2^-8 sum |dY| |W_hat|, its sums
+                (m + 16) u of the same, the adapter part as above, and the
+                output's own 2^-8 |dX|
+  dA, dB        sums over the adapter's rows: (rows + 16) u of the sum of
+                magnitudes, plus G's own error in dA
+All with a factor (1 + 2^-7) for the roundings of the roundings, and 1e-30.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+import post_weight_quantization_15_amd as gq
+
+pytestmark = pytest.mark.gpu
+
+U, UB = 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    gq.load_library()
+    return torch.device("cuda:0")
+
+
+class Layer:
+    """A random stored layer and what the oracle makes of it."""
+
+    def __init__(self, m, d, bits, group, order="natural", signed=False, f16=False, seed=0):
+        rng = np.random.default_rng([seed, m, d, bits])
+        ng = 1 if group == -1 else -(-d // group)
+        self.m, self.d, self.bits, self.group, self.signed = m, d, bits, group, signed
+        codes = rng.integers(0, 2 ** bits, size=(m, d))
+        self.packed = orc.pack_codes(codes, bits)
+        scales = rng.uniform(0.001, 0.05, size=(m, ng)).astype(np.float32)
+        self.scales = scales.astype(np.float16) if f16 else scales
+        self.zeros = np.zeros((m, ng), int) if signed else rng.integers(0, 2 ** bits, size=(m, ng))
+        g = np.zeros(d, int) if group == -1 else np.arange(d) // group
+        if order == "act":            # groups gather columns from everywhere, as act-order does
+            g = g[np.argsort(rng.permutation(d))]
+        elif order == "any":          # any ids at all
+            g = rng.integers(0, ng, size=d)
+        self.g_idx = g
+        if signed:
+            codes = np.where(codes >= 2 ** (bits - 1), codes - 2 ** bits, codes)
+        s = self.scales.astype(np.float64)[:, g]
+        z = self.zeros[:, g]
+        self.W = s * (codes - z)
+        self.mag = s * (np.abs(codes) + np.abs(z))
+
+    def on(self, dev):
+        return (torch.from_numpy(self.packed.view(np.int32)).to(dev),
+                torch.from_numpy(self.scales).to(dev),
+                torch.from_numpy(self.zeros.astype(np.uint8)).to(dev),
+                torch.from_numpy(self.g_idx.astype(np.int32)).to(dev), self.bits, self.group)
+
+
+def bf16(rng, *shape, scale=1.0):
+    return torch.from_numpy((rng.normal(size=shape) * scale).astype(np.float32)).to(torch.bfloat16)
+
+
+def adapters(rng, L, r, m, d):
+    A = bf16(rng, L, r, d, scale=d ** -0.5)
+    B = bf16(rng, L, m, r, scale=0.5)
+    alpha = torch.from_numpy(rng.uniform(0.5, 2.0, L).astype(np.float32))
+    return A, B, alpha
+
+
+def owners(rng, kind, n, L):
+    if kind == "none":
+        return np.full(n, -1)
+    if kind == "one":
+        return np.full(n, L - 1)
+    if kind == "runs":                # a few runs of rows, some without an adapter
+        ids = rng.integers(-1, L, size=7)
+        return ids[np.sort(rng.integers(0, 7, size=n))]
+    if kind == "each":
+        return np.arange(n) % L
+    ids = rng.integers(-1, L, size=n)
+    ids[rng.random(n) < 0.1] = L      # out of range: no adapter
+    ids[rng.random(n) < 0.05] = 2 ** 31 - 1
+    ids[rng.random(n) < 0.05] = -2 ** 31
+    return ids
+
+
+def near(got, want, bound, what):
+    err = np.abs(got.cpu().double().numpy() - want)
+    bound = bound * (1 + 2.0 ** -7) + 1e-30
+    assert np.isfinite(err).all(), f"{what}: not finite"
+    assert (err <= bound).all(), f"{what}: {float((err / bound).max()):.3g} of the bound"
+
+
+def lora_bounds(lay, x, A, B, al, ids, hidden):
+    """(bound of Y in fp32, bound of H)"""
+    n, (L, r, d) = x.shape[0], A.shape
+    shared = (d + 16) * U * (np.abs(x) @ lay.mag.T)
+    hb, part = np.zeros((n, r)), np.zeros((n, lay.m))
+    for a in range(L):
+        rows = np.nonzero(ids == a)[0]
+        hb[rows] = (d + 16) * U * (np.abs(x[rows]) @ np.abs(A[a]).T)
+        part[rows] = al[a] * ((hb[rows] + (r + 16) * U * np.abs(hidden[rows])) @ np.abs(B[a]).T)
+    return shared + part, hb
+
+
+def check_lora(dev, lay, n, L, r, kind, seed=0, out=torch.float32, pad=0, shift=0, want_h=True):
+    rng = np.random.default_rng([seed, n, L, r])
+    m, d = lay.m, lay.d
+    wide = torch.zeros(n, d + pad + shift, dtype=torch.bfloat16)
+    wide[:, shift:shift + d] = bf16(rng, n, d)
+    X = wide.to(dev)[:, shift:shift + d]
+    A, B, alpha = adapters(rng, L, r, m, d)
+    ids = owners(rng, kind, n, L)
+    got = gq.gptq_lora_matmul(X, *lay.on(dev), A.to(dev), B.to(dev),
+                              torch.from_numpy(ids.astype(np.int32)).to(dev), alpha.to(dev),
+                              signed=lay.signed, out_dtype=out, want_h=want_h)
+    torch.cuda.synchronize()
+    Y, Hg = got if want_h else (got, None)
+    x, a64, b64, al = X.cpu().double().numpy(), A.double().numpy(), B.double().numpy(), alpha.double().numpy()
+    Yo, Ho = orc.lora_matmul(x, lay.W, a64, b64, al, ids)
+    yb, hb = lora_bounds(lay, x, a64, b64, al, ids, Ho)
+    if out is torch.bfloat16:
+        yb = yb + UB * (np.abs(Yo) + yb)
+    near(Y, Yo, yb, "Y")
+    assert Y.dtype is out
+    if want_h:
+        near(Hg, Ho, hb, "H")
+
+
+SHAPES = [
+    # n, m, d, bits, group, order, adapters, rank, owners
+    (1, 64, 128, 4, 64, "natural", 3, 16, "one"),
+    (1, 130, 777, 4, 128, "natural", 1, 8, "one"),
+    (1, 70, 300, 3, 128, "act", 2, 5, "one"),
+    (2, 33, 96, 8, 32, "natural", 4, 4, "each"),
+    (7, 200, 520, 2, 64, "natural", 9, 16, "each"),
+    (16, 260, 1000, 4, 128, "natural", 16, 13, "each"),
+    (16, 96, 2112, 3, 96, "natural", 2, 1, "random"),
+    (17, 129, 640, 4, 128, "natural", 17, 16, "each"),
+    (33, 100, 257, 4, -1, "natural", 3, 32, "random"),
+    (64, 256, 512, 4, 128, "act", 5, 16, "runs"),
+    (65, 65, 65, 2, 8, "natural", 4, 33, "random"),
+    (100, 515, 390, 8, 40, "natural", 8, 64, "runs"),
+    (130, 300, 1030, 4, 128, "any", 6, 128, "random"),
+    (300, 260, 320, 4, 32, "natural", 1, 16, "none"),
+    (513, 300, 448, 3, 64, "natural", 40, 20, "runs"),
+    (700, 520, 1100, 4, 128, "natural", 3, 16, "random"),
+    (1030, 1100, 256, 4, 64, "natural", 2, 64, "runs"),
+    (3, 1, 1, 4, -1, "natural", 2, 2, "each"),
+    (40, 3, 5, 2, 2, "natural", 2, 3, "random"),
+]
+
+
+@pytest.mark.parametrize("case", SHAPES, ids=lambda c: "n%d_m%d_d%d_b%d_g%d_%s_L%d_r%d_%s" % c)
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_lora_matches_oracle(dev, case, out):
+    n, m, d, bits, group, order, L, r, kind = case
+    check_lora(dev, Layer(m, d, bits, group, order), n, L, r, kind, out=out)
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+@pytest.mark.parametrize("n", [1, 5, 48, 270])
+def test_lora_signed_codes_and_fp16_steps(dev, bits, n):
+    check_lora(dev, Layer(150, 416, bits, 32, signed=True), n, 3, 16, "random", want_h=False)
+    check_lora(dev, Layer(150, 416, bits, 32, f16=True), n, 3, 16, "random")
+
+
+@pytest.mark.parametrize("n", [1, 12, 40, 300])
+@pytest.mark.parametrize("pad,shift", [(8, 0), (3, 0), (0, 1), (5, 8)])
+def test_lora_strided_activations(dev, n, pad, shift):
+    check_lora(dev, Layer(130, 384, 4, 128), n, 4, 16, "runs", pad=pad, shift=shift)
+
+
+def back_bound(lay, dy, dx):
+    s = np.abs(dy) @ np.abs(lay.W)
+    return UB * s + (lay.m + 16) * U * (1 + UB) * s + UB * np.abs(dx)
+
+
+BACK = [
+    (1, 64, 128, 4, 64, "natural"), (1, 333, 130, 4, 128, "act"), (5, 70, 257, 3, 32, "natural"),
+    (16, 515, 96, 2, 8, "natural"), (33, 129, 640, 4, 128, "natural"), (64, 128, 128, 8, -1, "natural"),
+    (130, 260, 1000, 4, 128, "any"), (300, 1000, 300, 3, 64, "act"), (520, 640, 1100, 4, 128, "natural"),
+    (3, 1, 1, 4, -1, "natural"), (1025, 257, 513, 2, 64, "natural"),
+]
+
+
+@pytest.mark.parametrize("case", BACK, ids=lambda c: "n%d_m%d_d%d_b%d_g%d_%s" % c)
+def test_transposed_product_matches_oracle(dev, case):
+    n, m, d, bits, group, order = case
+    for signed, f16 in ((False, False), (True, True)):
+        lay = Layer(m, d, bits, group, order, signed=signed, f16=f16)
+        dY = bf16(np.random.default_rng([3, n, m]), n, m, scale=1e-3)
+        dX = gq.gptq_dequant_matmul_t(dY.to(dev), *lay.on(dev), signed=signed)
+        torch.cuda.synchronize()
+        dy = dY.double().numpy()
+        want = dy @ lay.W
+        near(dX, want, back_bound(lay, dy, want), "dX")
+
+
+@pytest.mark.parametrize("pad,shift", [(8, 0), (3, 0), (0, 1)])
+def test_transposed_product_strided_gradient(dev, pad, shift):
+    lay = Layer(200, 320, 4, 64)
+    for n in (3, 150):
+        wide = bf16(np.random.default_rng(n), n, 200 + pad + shift, scale=1e-3).to(dev)
+        dY = wide[:, shift:shift + 200]
+        dX = gq.gptq_dequant_matmul_t(dY, *lay.on(dev))
+        torch.cuda.synchronize()
+        dy = dY.cpu().double().numpy()
+        want = dy @ lay.W
+        near(dX, want, back_bound(lay, dy, want), "dX")
+
+
+def check_backward(dev, lay, n, L, r, kind, seed=0, accumulate=False, pad=0):
+    rng = np.random.default_rng([seed, n, L, r, 7])
+    m, d = lay.m, lay.d
+    X = bf16(rng, n, d + pad).to(dev)[:, :d]
+    dY = bf16(rng, n, m + pad, scale=1e-2).to(dev)[:, :m]
+    A, B, alpha = adapters(rng, L, r, m, d)
+    ids = owners(rng, kind, n, L)
+    H = torch.from_numpy(rng.normal(size=(n, r)).astype(np.float32))
+    # what stands in rows without an adapter does not count
+    on = (ids >= 0) & (ids < L)
+    H[torch.from_numpy(~on)] = float("nan")
+    dA0 = torch.from_numpy(rng.normal(size=A.shape).astype(np.float32))
+    dB0 = torch.from_numpy(rng.normal(size=B.shape).astype(np.float32))
+    kw = dict(dA=dA0.to(dev), dB=dB0.to(dev), accumulate=True) if accumulate else {}
+    dX, dA, dB = gq.gptq_lora_backward(
+        dY, X, H.to(dev), *lay.on(dev), A.to(dev), B.to(dev),
+        torch.from_numpy(ids.astype(np.int32)).to(dev), alpha.to(dev), signed=lay.signed, **kw)
+    torch.cuda.synchronize()
+    x, dy, h = X.cpu().double().numpy(), dY.cpu().double().numpy(), H.double().numpy()
+    a64, b64, al = A.double().numpy(), B.double().numpy(), alpha.double().numpy()
+    Xo, Ao, Bo = orc.lora_backward(dy, x, h, lay.W, a64, b64, al, ids)
+    xb = np.zeros((n, d))
+    ab, bb = np.zeros_like(a64), np.zeros_like(b64)
+    for a in range(L):
+        rows = np.nonzero(ids == a)[0]
+        gm = al[a] * (np.abs(dy[rows]) @ np.abs(b64[a]))
+        ge = (m + 16) * U * gm
+        xb[rows] = (ge + (r + 16) * U * gm) @ np.abs(a64[a])
+        ab[a] = (ge + (len(rows) + 16) * U * gm).T @ np.abs(x[rows])
+        bb[a] = (len(rows) + 16) * U * al[a] * (np.abs(dy[rows]).T @ np.abs(h[rows]))
+    # the shared and the adapter part are added before the output is rounded
+    s = np.abs(dy) @ np.abs(lay.W)
+    near(dX, Xo, UB * s + (m + r + 16) * U * (1 + UB) * s + xb + UB * np.abs(Xo), "dX")
+    if accumulate:
+        Ao, Bo = Ao + dA0.double().numpy(), Bo + dB0.double().numpy()
+        ab, bb = ab + U * np.abs(Ao), bb + U * np.abs(Bo)
+    near(dA, Ao, ab, "dA")
+    near(dB, Bo, bb, "dB")
+
+
+GRADS = [
+    (1, 64, 128, 4, 64, "natural", 3, 16, "one"),
+    (5, 130, 300, 3, 128, "act", 2, 5, "random"),
+    (40, 33, 65, 8, 32, "natural", 4, 1, "each"),
+    (64, 256, 512, 4, 128, "natural", 17, 16, "each"),
+    (130, 200, 390, 4, 128, "natural", 5, 33, "runs"),
+    (300, 515, 257, 2, 64, "any", 6, 64, "random"),
+    (300, 96, 128, 4, 32, "natural", 2, 16, "none"),
+    (700, 260, 320, 4, 64, "natural", 1, 16, "one"),
+    (1030, 300, 640, 4, 128, "natural", 9, 8, "runs"),
+    (2500, 130, 96, 4, 32, "natural", 3, 128, "random"),
+    (3, 1, 1, 4, -1, "natural", 2, 2, "each"),
+]
+
+
+@pytest.mark.parametrize("case", GRADS, ids=lambda c: "n%d_m%d_d%d_b%d_g%d_%s_L%d_r%d_%s" % c)
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_lora_gradients_match_oracle(dev, case, accumulate):
+    n, m, d, bits, group, order, L, r, kind = case
+    check_backward(dev, Layer(m, d, bits, group, order), n, L, r, kind, accumulate=accumulate,
+                   pad=3 if accumulate else 0)
+
+
+def make_call(dev, n=37, m=96, d=160, L=4, r=16, seed=5):
+    rng = np.random.default_rng(seed)
+    lay = Layer(m, d, 4, 32)
+    A, B, alpha = adapters(rng, L, r, m, d)
+    ids = torch.from_numpy(owners(rng, "random", n, L).astype(np.int32)).to(dev)
+    return dict(X=bf16(rng, n, d).to(dev), dY=bf16(rng, n, m).to(dev), packed=lay.on(dev),
+                A=A.to(dev), B=B.to(dev), alpha=alpha.to(dev), ids=ids, n=n, m=m, d=d, L=L, r=r)
+
+
+def forward(c, **kw):
+    return gq.gptq_lora_matmul(c["X"], *c["packed"], c["A"], c["B"], c["ids"], c["alpha"],
+                               want_h=True, **kw)
+
+
+def backward(c, H, **kw):
+    return gq.gptq_lora_backward(c["dY"], c["X"], H, *c["packed"], c["A"], c["B"], c["ids"],
+                                 c["alpha"], **kw)
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_no_rows(dev):
+    c = make_call(dev, n=0)
+    Y, H = forward(c)
+    assert Y.shape == (0, c["m"]) and H.shape == (0, c["r"])
+    dA = torch.ones_like(c["A"], dtype=torch.float32)
+    dB = torch.ones_like(c["B"], dtype=torch.float32)
+    dX, dA, dB = backward(c, H, dA=dA, dB=dB, accumulate=True)
+    assert dX.shape == (0, c["d"]) and bool((dA == 1).all()) and bool((dB == 1).all())
+    dX, dA, dB = backward(c, H, dA=dA, dB=dB)
+    assert not dA.any() and not dB.any()
+    assert gq.gptq_dequant_matmul_t(c["dY"], *c["packed"]).shape == (0, c["d"])
+
+
+@pytest.mark.parametrize("n", [1, 16, 37, 300])
+def test_runs_are_the_same_bits_and_other_memory_stays(dev, n):
+    """Twice the same bits, into given outputs inside larger buffers whose
+    other rows keep their bytes; parts of the gradients by themselves give
+    the same bits as all of them."""
+    c = make_call(dev, n=n)
+    Y, H = forward(c)
+    first = (Y, H, *backward(c, H))
+    Yw = torch.full((n + 3, c["m"]), 7.0, device=dev)
+    Hw = torch.full((n + 3, c["r"]), 7.0, device=dev)
+    Xw = torch.full((n + 3, c["d"]), 7.0, device=dev, dtype=torch.bfloat16)
+    forward(c, Y=Yw[:n], H=Hw[:n])
+    dX, dA, dB = backward(c, Hw[:n], dX=Xw[:n])
+    torch.cuda.synchronize()
+    assert same(first, (Yw[:n], Hw[:n], dX, dA, dB))
+    for w in (Yw, Hw, Xw):
+        assert bool((w[n:] == 7.0).all())
+    assert torch.equal(backward(c, H, need_dab=False)[0], dX)
+    part = backward(c, H, need_dx=False)
+    assert part[0] is None and same(part[1:], (dA, dB))
+
+
+@pytest.mark.parametrize("n", [1, 12, 50, 290])
+def test_captured_and_replayed(dev, n):
+    """A captured forward and backward pass, replayed with other inputs in the
+    same buffers and eager calls between, gives the eager results."""
+    c = make_call(dev, n=n)
+    other = make_call(dev, n=n, seed=6)
+    Y, H = forward(c)
+    backward(c, H)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Yg, Hg = forward(c)
+        back = backward(c, Hg)
+        dXt = gq.gptq_dequant_matmul_t(c["dY"], *c["packed"])
+    for k in range(4):
+        src = other if k % 2 else make_call(dev, n=n)
+        for key in ("X", "dY", "A", "B", "ids", "alpha"):
+            c[key].copy_(src[key])
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (Yg, Hg, *back, dXt)]
+        Y, H = forward(c)
+        want = (Y, H, *backward(c, H), gq.gptq_dequant_matmul_t(c["dY"], *c["packed"]))
+        torch.cuda.synchronize()
+        assert same(got, want), k
+
+
+def test_another_stream_and_two_at_once(dev):
+    c, e = make_call(dev, n=200), make_call(dev, n=60, seed=8)
+    want = [(forward(v), backward(v, forward(v)[1])) for v in (c, e)]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(dev), torch.cuda.Stream(dev)
+    got = [None, None]
+    for i, (v, s) in enumerate(((c, s1), (e, s2))):
+        s.wait_stream(torch.cuda.current_stream(dev))
+        with torch.cuda.stream(s):
+            f = forward(v)
+            got[i] = (f, backward(v, f[1]))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert same(w[0], g[0]) and same(w[1], g[1])
+
+
+def test_given_workspace(dev):
+    c = make_call(dev, n=130)
+    need = gq.gptq_lora_workspace_bytes(130, c["m"], c["d"], c["r"])
+    back = gq.gptq_lora_backward_workspace_bytes(130, c["m"], c["d"], c["r"], c["L"])
+    ws = torch.full((max(need, back),), 255, dtype=torch.uint8, device=dev)
+    Y, H = forward(c)
+    grads = backward(c, H)
+    assert same((Y, H), forward(c, ws=ws)) and same(grads, backward(c, H, ws=ws))
+
+
+def test_unread_parts_may_hold_anything(dev):
+    """An adapter without a row, and H in rows without an adapter, are not
+    read into any result."""
+    c = make_call(dev, n=40)
+    c["ids"][c["ids"] == 2] = 1
+    Y, H = forward(c)
+    grads = backward(c, H)
+    c["A"][2] = float("nan")
+    c["B"][2] = float("inf")
+    c["alpha"][2] = float("nan")
+    H2 = H.clone()
+    H2[(c["ids"] < 0) | (c["ids"] >= c["L"])] = float("nan")
+    assert same((Y, H), forward(c)) and same(grads, backward(c, H2))
+    assert not grads[1][2].any() and not grads[2][2].any()
+
+
+def test_not_finite_activations_stay_in_their_row(dev):
+    """A row that holds NaN or inf changes no other row of Y, H and dX."""
+    for n in (9, 80, 300):
+        c = make_call(dev, n=n)
+        c["ids"][:] = torch.arange(n, device=dev) % 3
+        Y, H = forward(c)
+        dX = backward(c, H)[0]
+        c["X"][4, 7] = float("nan")
+        c["X"][5, 1] = float("inf")
+        c["dY"][4, 3] = float("inf")
+        Y2, H2 = forward(c)
+        dX2 = backward(c, H2)[0]
+        rest = torch.ones(n, dtype=torch.bool, device=dev)
+        rest[4] = rest[5] = False
+        assert torch.equal(Y[rest], Y2[rest]) and torch.equal(H[rest], H2[rest])
+        rest[5] = True
+        assert torch.equal(dX[rest], dX2[rest])
+        assert bool(torch.isnan(Y2[4]).all()) and not bool(torch.isfinite(Y2[5]).any())
+        assert not bool(torch.isfinite(dX2[4]).any())
+
+
+def test_bits_of_the_shared_product_alone(dev):
+    """Rows without an adapter agree with gptq_dequant_matmul within the two
+    products' own roundings."""
+    for n in (1, 16, 70, 400):
+        c = make_call(dev, n=n, m=260, d=544)
+        c["ids"][:] = -1
+        Y, H = forward(c)
+        Yd = gq.gptq_dequant_matmul(c["X"], *c["packed"])
+        lay = Layer(260, 544, 4, 32)
+        bound = 2 * (544 + 16) * U * (np.abs(c["X"].cpu().double().numpy()) @ lay.mag.T)
+        near(Y, Yd.cpu().double().numpy(), bound, "Y")
+        assert not H.any()
