@@ -300,7 +300,8 @@ gptq_status gptq_dequant_matmul_t(const void* dY, gptq_dtype dy_dtype, int64_t n
  * The shared product is gptq_dequant_matmul's: exact codes and activations,
  * fp32 sums per group; H is summed and kept in fp32 and enters its product
  * with B as three bf16 parts, i.e. exactly.
- * ws: at least gptq_lora_workspace_bytes(n, m, d, rank) bytes.
+ * ws: at least gptq_lora_workspace_bytes(n, m, d, group_size, rank)
+ *     bytes.
  * Errors: INVALID_ARG (bad sizes, m or d > 65535, rank outside 1 .. 128,
  *         n_adapters outside 1 .. 65535, dtype, bits, group_size, NULL
  *         pointers when n > 0); WORKSPACE; HIP.
@@ -314,7 +315,8 @@ typedef struct gptq_adapters {
   int32_t rank;
 } gptq_adapters;
 
-size_t gptq_lora_workspace_bytes(int64_t n, int64_t m, int64_t d, int32_t rank);
+size_t gptq_lora_workspace_bytes(int64_t n, int64_t m, int64_t d, int32_t group_size,
+                                 int32_t rank);
 gptq_status gptq_lora_matmul(const void* X, gptq_dtype x_dtype, int64_t n, int64_t d,
                              int64_t ldx, const uint32_t* qweight, const void* scales,
                              gptq_dtype scale_dtype, const uint8_t* zeros,

@@ -115,7 +115,7 @@ def load_library():
     lib.gptq_dequant_matmul_t.argtypes = [vp, dt, i64, i64, i64, vp, vp, dt, vp, vp, i64, i32, i32,
                                           i32, vp, i64, vp, sz, vp]
     lib.gptq_lora_workspace_bytes.restype = sz
-    lib.gptq_lora_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.gptq_lora_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
     lib.gptq_lora_matmul.restype = ctypes.c_int
     lib.gptq_lora_matmul.argtypes = [vp, dt, i64, i64, i64, vp, vp, dt, vp, vp, i64, i32, i32, i32,
                                      ap, vp, vp, dt, i64, vp, sz, vp]
@@ -491,8 +491,8 @@ def _launch(dev, where, fn, *args):
         raise GPTQError(st, where)
 
 
-def gptq_lora_workspace_bytes(n: int, m: int, d: int, rank: int) -> int:
-    return int(_lib().gptq_lora_workspace_bytes(n, m, d, rank))
+def gptq_lora_workspace_bytes(n: int, m: int, d: int, group_size: int, rank: int) -> int:
+    return int(_lib().gptq_lora_workspace_bytes(n, m, d, group_size, rank))
 
 
 def gptq_lora_backward_workspace_bytes(n: int, m: int, d: int, rank: int, n_adapters: int) -> int:
@@ -527,7 +527,7 @@ def gptq_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tenso
     if out_dtype is not _F32 and out_dtype is not _BF16:
         raise TypeError(f"Y must be float32 or bfloat16, got {out_dtype}")
     lib = _lib()
-    need = lib.gptq_lora_workspace_bytes(n, m, d, ad.rank)
+    need = lib.gptq_lora_workspace_bytes(n, m, d, group_size, ad.rank)
     ws = _enough(ws, need, dev)
     Y = _out(Y, "Y", out_dtype, (n, m), dev)
     if want_h or H is not None:

@@ -187,7 +187,7 @@ constexpr int64_t kMaxRows = int64_t(65535) * 8;   // activation rows of a produ
 constexpr int kMaxRank = 128;
 
 // Y = X W_hat^T + alpha H B^T, H = X A^T (k_lora.hip); H may be NULL.
-size_t lora_ws_bytes(int64_t n, int64_t m, int64_t d, int rank);
+size_t lora_ws_bytes(int64_t n, int64_t m, int64_t d, int64_t group, int rank);
 gptq_status launch_lora(const uint16_t* X, int64_t ldx, int64_t n, const Packed& w,
                         const gptq_adapters& ad, float* H, void* Y, int out_bf16, int64_t ldy,
                         void* ws, hipStream_t st);

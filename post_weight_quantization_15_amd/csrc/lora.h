@@ -1,0 +1,127 @@
+// Shared by the adapter products: small device helpers and the pieces that
+// the orchestration in k_lora.hip puts together.
+#pragma once
+
+#include "common.h"
+
+namespace gptq {
+
+inline unsigned ceil_div(int64_t a, int64_t b) { return static_cast<unsigned>((a + b - 1) / b); }
+inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
+
+
+// ---------------------------------------------------------------------------
+// The products Y[t][j] = sum_k V[t][k] M[j][k] (+ the adapters' part) of
+// lora_gemm.hip.  Both operands are bf16 with k contiguous, rows 16-byte
+// aligned, k in blocks of 64.
+struct GemmArgs {
+  const uint16_t* V;       // activations [n][ldv]
+  int64_t ldv, n;
+  const uint16_t* V2;      // the same in group order, when the plan asks for it
+  int64_t ldv2;
+  const uint16_t* M;       // [m][ldm]
+  int64_t ldm, m;
+  int kblocks, kwrap;      // blocks of 64 of M; V repeats after kwrap blocks
+  // groups: per 32-step the group whose step Delta multiplies its sums
+  const int32_t* plan;     // header {in order, kblocks}, then the group per 32-step
+  const float* scale_t;    // [ng][mpad] steps
+  int64_t mpad;
+  // the adapters' part: parts [n][3 rp] (three bf16 parts of alpha H), L_a [m][rank] rows
+  const uint16_t* parts;
+  const uint16_t* L;       // [n_adapters][m][rank], or NULL
+  const int32_t* row;
+  int n_adapters, rank, rp;
+  void* Y;
+  int64_t ldy;
+  int out_bf16;
+};
+constexpr int kPlanHeader = 16;   // words before the plan's group list
+
+// Rows of activations handled at once (bounds the reordered copy).
+constexpr int64_t kRowChunk = 16384;
+
+// Columns in group order, every group padded to whole 32-steps, and all to 64.
+int64_t plan_cols(int64_t d, int64_t ng);
+size_t plan_words(int64_t d, int64_t ng);
+gptq_status launch_plan(const Packed& w, int32_t* plan, hipStream_t st);
+// M[j][k] = code - zero, exact in bf16, in the plan's column order; scale_t = steps transposed.
+gptq_status launch_expand_grouped(const Packed& w, const int32_t* plan, uint16_t* M, int64_t ldm,
+                                  float* scale_t, int64_t mpad, hipStream_t st);
+// V2[t][k] = V[t][order[k]] where the plan is not the natural order (or always).
+gptq_status launch_reorder(const uint16_t* V, int64_t ldv, int64_t n, int64_t d,
+                           const int32_t* plan, int64_t ng, int always, uint16_t* V2, int64_t ldv2,
+                           hipStream_t st);
+// M[j][p ldp + c] = part p of three of W_hat[j][c] in bf16 (their sum is exact in fp32).
+gptq_status launch_expand_parts(const Packed& w, uint16_t* M, int64_t ldp, hipStream_t st);
+// M[c][j] = W_hat[j][c] rounded to bf16, columns m .. ldm zero.
+gptq_status launch_expand_transposed(const Packed& w, uint16_t* M, int64_t ldm, hipStream_t st);
+// V2[t][0 .. cols) = V[t][0 .. len) and zeros.
+gptq_status launch_pad_rows(const uint16_t* V, int64_t ldv, int64_t n, int64_t len, uint16_t* V2,
+                            int64_t cols, hipStream_t st);
+gptq_status launch_gemm(const GemmArgs& a, bool grouped, hipStream_t st);
+
+#ifdef __HIPCC__
+namespace {
+
+typedef const void __attribute__((address_space(1)))* gvoid;
+typedef void __attribute__((address_space(3)))* lvoid;
+
+__device__ inline float bf16_f32(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ inline uint16_t f32_bf16(float v) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
+// The three bf16 parts of an fp32 number: each the rounding of what the
+// parts before leave, so that (normal range) their sum is the number itself:
+// 8 + 8 + 8 significant bits.  inf and NaN go into the first part alone.
+__device__ inline void split3(float v, uint16_t p[3]) {
+  p[0] = f32_bf16(v);
+  const float a = bf16_f32(p[0]);
+  const float r1 = (__float_as_uint(a) & 0x7F800000u) == 0x7F800000u ? 0.0f : v - a;
+  p[1] = f32_bf16(r1);
+  const float r2 = r1 - bf16_f32(p[1]);
+  p[2] = f32_bf16(r2);
+}
+
+__device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Eight values [c, c + 8) of a row of len bf16 values, zeros past its end; vec: the row's
+// 16-byte loads are aligned.
+__device__ inline u32x4 load8(const uint16_t* __restrict__ p, int64_t c, int64_t len, bool vec) {
+  if (vec && c + 8 <= len) return *reinterpret_cast<const u32x4*>(p + c);
+  u32x4 v = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < len) v[i >> 1] |= uint32_t(p[c + i]) << (16 * (i & 1));
+  return v;
+}
+
+// Step Delta and code minus zero of weight (r, c).
+__device__ inline float step_at(const Packed& w, int64_t i) {
+  return w.scale_f16 ? static_cast<float>(static_cast<const _Float16*>(w.scales)[i])
+                     : static_cast<const float*>(w.scales)[i];
+}
+__device__ inline int code_at(const Packed& w, int64_t words, int64_t r, int64_t c) {
+  const int64_t p = c * w.bits;
+  const int64_t i = p >> 5;
+  const int off = static_cast<int>(p & 31);
+  uint32_t v = w.qw[r * words + i] >> off;
+  if (off + w.bits > 32) v |= w.qw[r * words + i + 1] << (32 - off);
+  v &= (1u << w.bits) - 1u;
+  const int hb = 1 << (w.bits - 1);
+  return w.sgn ? static_cast<int>(v ^ hb) - hb : static_cast<int>(v);
+}
+
+template <int n>
+__device__ inline void wait_vmcnt() {
+  // vmcnt = n (split field), expcnt and lgkmcnt at maximum
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+}  // namespace
+#endif
+
+}  // namespace gptq

@@ -68,11 +68,12 @@ gptq_status gptq_dequant_matmul_t(const void* dY, gptq_dtype dy_dtype, int64_t n
                               static_cast<hipStream_t>(stream));
 }
 
-size_t gptq_lora_workspace_bytes(int64_t n, int64_t m, int64_t d, int32_t rank) {
+size_t gptq_lora_workspace_bytes(int64_t n, int64_t m, int64_t d, int32_t group_size,
+                                 int32_t rank) {
   if (n < 0 || n > kMaxRows || m <= 0 || d <= 0 || m > kMaxDim || d > kMaxDim || rank < 1 ||
-      rank > kMaxRank)
+      rank > kMaxRank || !(group_size == -1 || group_size > 0))
     return 0;
-  return lora_ws_bytes(n, m, d, rank);
+  return lora_ws_bytes(n, m, d, group_size, rank);
 }
 
 gptq_status gptq_lora_matmul(const void* X, gptq_dtype x_dtype, int64_t n, int64_t d, int64_t ldx,
@@ -88,7 +89,8 @@ gptq_status gptq_lora_matmul(const void* X, gptq_dtype x_dtype, int64_t n, int64
     return GPTQ_ERR_INVALID_ARG;
   if (n > 0 && (!X || !Y || !adapters->A || !adapters->B || !adapters->alpha || !adapters->row))
     return GPTQ_ERR_INVALID_ARG;
-  if (short_ws(ws, ws_bytes, lora_ws_bytes(n, m, d, adapters->rank))) return GPTQ_ERR_WORKSPACE;
+  if (short_ws(ws, ws_bytes, lora_ws_bytes(n, m, d, group_size, adapters->rank)))
+    return GPTQ_ERR_WORKSPACE;
   if (n == 0) return GPTQ_OK;
   const Packed w = make_packed(m, d, qweight, scales, scale_dtype, zeros, g_idx, bits, group_size,
                                signed_codes);

@@ -1,0 +1,618 @@
+// The matrix-core product behind the adapter operators, and the passes that
+// lay its operands out.
+//
+//   Y[t][j] = sum_k V[t][k] M[j][k]  (+ sum_q (alpha H)[t][q] L_a[j][q])
+//
+// Forward (Y = X W_hat^T): M holds code - zero, an integer of at most 8
+// bits and so exact in bf16, with the columns in group order (act-order
+// scatters a group's columns; a sum takes its terms in any order) and every
+// group padded to whole 32-column steps.  A 32-step then lies in one group,
+// the matrix cores form P = sum x (code - zero) over the group exactly as
+// products with fp32 sums, and the group's step folds in once at its end:
+// acc += Delta P.  No weight is rounded.  Groups narrower than a step
+// (g < 32) would pad to several times the work; there M holds Delta (code -
+// zero) as three bf16 parts instead (their sum is the fp32 value), three
+// products per weight and no fold.
+// Backward (dX = dY W_hat): the sum runs over output rows, each with its own
+// step, so no step factors out of it; M is W_hat^T rounded to bf16.
+#include "lora.h"
+
+namespace gptq {
+namespace {
+
+// ---------------------------------------------------------------------------
+// The plan: order[k] = column at place k (-1: padding) and the group of every
+// 32-step.  A wave places one group's columns, in their own order; every
+// workgroup counts all groups for itself (g_idx is small and stays in L2).
+// In natural order with whole steps per group the order is the identity and
+// the activations are used where they lie.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxGroups = 2048;      // groups of at least 32 columns, d <= 65535
+
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __restrict__ g_idx,
+                                                            int d, int ng, int cols_max,
+                                                            int32_t* __restrict__ plan) {
+  __shared__ int32_t cnt[kPlanMaxGroups];
+  __shared__ int32_t start[kPlanMaxGroups + 1];
+  __shared__ int ident;
+  const int tid = threadIdx.x, lane = tid & 63;
+  int32_t* grp = plan + kPlanHeader;
+  int32_t* order = grp + cols_max / 32;
+  for (int i = tid; i < ng; i += kPlanThreads) cnt[i] = 0;
+  if (tid == 0) ident = d % 64 == 0;
+  __syncthreads();
+  bool inc = true;
+  for (int c = tid; c < d; c += kPlanThreads) {
+    const int g = min(max(g_idx[c], 0), ng - 1);
+    atomicAdd(&cnt[g], 1);
+    if (c > 0 && g < g_idx[c - 1]) inc = false;
+  }
+  if (!inc) ident = 0;
+  __syncthreads();
+  if (tid < 64) {                          // padded starts: one wave's running sum
+    int run = 0;
+    for (int b = 0; b < ng; b += 64) {
+      const int g = b + lane;
+      const int c = g < ng ? cnt[g] : 0;
+      if (c % 32) ident = 0;
+      int s = (c + 31) / 32 * 32;
+      const int own = s;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(s, o);
+        if (lane >= o) s += u;
+      }
+      if (g < ng) start[g] = run + s - own;
+      run += __shfl(s, 63);
+    }
+    if (lane == 0) start[ng] = run;
+  }
+  __syncthreads();
+  const int total = start[ng];
+  const int padded = (total + 63) / 64 * 64;
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      plan[0] = ident;
+      plan[1] = padded / 64;
+    }
+    // the step that may pad the last block continues the last group
+    if (tid == 0 && padded > total) grp[total / 32] = total ? -1 : 0;
+    for (int k = total + tid; k < padded; k += kPlanThreads) order[k] = -1;
+  }
+  const int nw = gridDim.x * (kPlanThreads / 64);
+  for (int g = blockIdx.x * (kPlanThreads / 64) + (tid >> 6); g < ng; g += nw) {
+    const int s = start[g], e = start[g + 1], n = cnt[g];
+    for (int k = s / 32 + lane; k < e / 32; k += 64) grp[k] = g;
+    if (ident) {
+      for (int k = s + lane; k < e; k += 64) order[k] = k;
+      continue;
+    }
+    int at = s;
+    for (int c0 = 0; c0 < d && at < s + n; c0 += 64) {
+      const int c = c0 + lane;
+      const bool mine = c < d && min(max(g_idx[c], 0), ng - 1) == g;
+      const uint64_t b = __ballot(mine);
+      if (mine) order[at + __popcll(b & ((uint64_t(1) << lane) - 1))] = c;
+      at += __popcll(b);
+    }
+    for (int k = s + n + lane; k < e; k += 64) order[k] = -1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Layout passes
+// ---------------------------------------------------------------------------
+
+// The eight codes of run ch (columns 8 ch .. + 7) of a row, as integers.
+template <int BITS>
+__device__ inline void codes8(const uint32_t* __restrict__ p, int64_t words, int64_t ch, int c[8]) {
+  uint32_t lo, hi = 0u;
+  if (BITS == 4) {
+    lo = p[min<int64_t>(ch, words - 1)];
+  } else if (BITS == 2) {
+    lo = p[min<int64_t>(ch >> 1, words - 1)] >> (16 * (ch & 1));
+  } else if (BITS == 8) {
+    lo = p[min<int64_t>(2 * ch, words - 1)];
+    hi = p[min<int64_t>(2 * ch + 1, words - 1)];
+  } else {
+    const int64_t bit = 24 * ch;
+    const int64_t i = min<int64_t>(bit >> 5, words - 1);
+    lo = __builtin_amdgcn_alignbit(p[min<int64_t>(i + 1, words - 1)], p[i],
+                                   static_cast<uint32_t>(bit & 31));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t v = BITS == 8 ? (i < 4 ? lo >> (8 * i) : hi >> (8 * (i - 4))) : lo >> (BITS * i);
+    c[i] = static_cast<int>(v & ((1u << BITS) - 1u));
+  }
+}
+
+__device__ inline int signed_code(int c, int bits) {
+  const int hb = 1 << (bits - 1);
+  return (c ^ hb) - hb;
+}
+
+// Thread: 8 places of one row of M.  Blocks past the expansion transpose the steps.
+template <int BITS>
+__global__ __launch_bounds__(256) void expand_grouped_kernel(Packed w, int64_t words,
+                                                             const int32_t* __restrict__ plan,
+                                                             int cols_max, uint16_t* __restrict__ M,
+                                                             int64_t ldm,
+                                                             float* __restrict__ scale_t,
+                                                             int64_t mpad, unsigned blocks) {
+  if (blockIdx.x >= blocks) {
+    const int64_t e = int64_t(blockIdx.x - blocks) * 256 + threadIdx.x;
+    const int64_t j = e / w.ng, g = e % w.ng;
+    if (j < w.m) scale_t[g * mpad + j] = step_at(w, j * w.ng + g);
+    return;
+  }
+  const int units = plan[1] * 8;
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int per = cols_max / 8;
+  const int64_t j = e / per;
+  const int u = static_cast<int>(e % per);
+  if (u >= units || j >= w.m) return;
+  const int32_t* grp = plan + kPlanHeader;
+  const int32_t* order = grp + cols_max / 32;
+  const int g = grp[u / 4];
+  u32x4 out = u32x4{0u, 0u, 0u, 0u};
+  if (g >= 0) {
+    const int z = w.sgn ? 0 : w.zeros[j * w.ng + g];
+    if (plan[0]) {
+      int c[8];
+      codes8<BITS>(w.qw + j * words, words, u, c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int v = (w.sgn ? signed_code(c[i], BITS) : c[i]) - z;
+        out[i >> 1] |= (__float_as_uint(static_cast<float>(v)) >> 16) << (16 * (i & 1));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = order[8 * u + i];
+        if (c < 0) continue;
+        const int v = code_at(w, words, j, c) - z;
+        out[i >> 1] |= (__float_as_uint(static_cast<float>(v)) >> 16) << (16 * (i & 1));
+      }
+    }
+  }
+  *reinterpret_cast<u32x4*>(M + j * ldm + 8 * u) = out;
+}
+
+// One row per workgroup, through LDS (a row's gather is within itself).
+__global__ __launch_bounds__(256) void reorder_kernel(const uint16_t* __restrict__ V, int64_t ldv,
+                                                      int d, const int32_t* __restrict__ plan,
+                                                      int cols_max, int always,
+                                                      uint16_t* __restrict__ V2, int64_t ldv2) {
+  extern __shared__ uint16_t rowbuf[];
+  if (plan[0] && !always) return;
+  const int64_t t = blockIdx.x;
+  const int32_t* order = plan + kPlanHeader + cols_max / 32;
+  const uint16_t* src = V + t * ldv;
+  for (int c = threadIdx.x; c < d; c += 256) rowbuf[c] = src[c];
+  __syncthreads();
+  const int units = plan[1] * 8;
+  for (int u = threadIdx.x; u < units; u += 256) {
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = order[8 * u + i];
+      if (c >= 0) v[i >> 1] |= uint32_t(rowbuf[c]) << (16 * (i & 1));
+    }
+    *reinterpret_cast<u32x4*>(V2 + t * ldv2 + 8 * u) = v;
+  }
+}
+
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ V, int64_t ldv,
+                                                       int64_t n, int64_t len,
+                                                       uint16_t* __restrict__ V2, int64_t cols,
+                                                       bool vec) {
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t per = cols / 8, t = e / per, u = e % per;
+  if (t >= n) return;
+  *reinterpret_cast<u32x4*>(V2 + t * cols + 8 * u) = load8(V + t * ldv, 8 * u, len, vec);
+}
+
+__global__ __launch_bounds__(256) void expand_parts_kernel(Packed w, int64_t words,
+                                                           uint16_t* __restrict__ M, int64_t ldp) {
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t per = ldp / 8, j = e / per, u = e % per;
+  if (j >= w.m) return;
+  u32x4 out[3] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = 8 * u + i;
+    if (c >= w.d) continue;
+    const int64_t g = j * w.ng + w.g_idx[c];
+    const int k = code_at(w, words, j, c) - (w.sgn ? 0 : w.zeros[g]);
+    uint16_t p[3];
+    split3(step_at(w, g) * static_cast<float>(k), p);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) out[q][i >> 1] |= uint32_t(p[q]) << (16 * (i & 1));
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+    *reinterpret_cast<u32x4*>(M + j * 3 * ldp + q * ldp + 8 * u) = out[q];
+}
+
+// 64 weight rows x 64 columns per workgroup: thread t takes row t / 4 and two
+// 8-column runs, the tile turns in LDS (a row of 64 bf16 and 8 of padding, so
+// that the eight rows a run writes to lie in different banks), and leaves
+// as 128 contiguous bytes of a column.
+template <int BITS>
+__global__ __launch_bounds__(256) void expand_transposed_kernel(Packed w, int64_t words,
+                                                                uint16_t* __restrict__ M,
+                                                                int64_t ldm) {
+  __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
+  const int tid = threadIdx.x;
+  const int64_t c0 = int64_t(blockIdx.x) * 64, j0 = int64_t(blockIdx.y) * 64;
+  const int jl = tid >> 2;
+  const int64_t j = j0 + jl;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int run = 2 * (tid & 3) + e;
+    int c[8];
+    float v[8];
+    if (j < w.m) {
+      codes8<BITS>(w.qw + j * words, words, c0 / 8 + run, c);
+      int gp = -1;
+      float s = 0.0f;
+      int z = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t col = min<int64_t>(c0 + 8 * run + i, w.d - 1);
+        const int g = w.g_idx[col];
+        if (g != gp) {
+          s = step_at(w, j * w.ng + g);
+          z = w.sgn ? 0 : w.zeros[j * w.ng + g];
+          gp = g;
+        }
+        v[i] = s * static_cast<float>((w.sgn ? signed_code(c[i], BITS) : c[i]) - z);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tile[8 * run + i][jl] = f32_bf16(v[i]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int cl = tid >> 2, u = 2 * (tid & 3) + e;
+    if (c0 + cl < w.d && j0 + 8 * u < ldm)
+      *reinterpret_cast<u32x4*>(M + (c0 + cl) * ldm + j0 + 8 * u) =
+          *reinterpret_cast<const u32x4*>(&tile[cl][8 * u]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The product.  A workgroup of WM x WN waves owns TM activation rows x TN
+// rows of M; k goes by in blocks of 64 through a ring of S stages in LDS,
+// both operands copied by global_load_lds_dwordx4 (no registers) S - 1
+// blocks ahead, one barrier per block.  Rows are stored as eight 16-byte
+// units, unit c of row r at c ^ ((r / 2) % 8), which the fragment reads (16
+// consecutive rows, one unit each) and the copies (8 rows of 8 units) both
+// pass without bank conflicts.  M is the matrix instruction's first operand:
+// a lane then holds four consecutive j of one activation row, i.e. one
+// 16-byte (fp32) or 8-byte (bf16) store per fragment.
+// ---------------------------------------------------------------------------
+constexpr int kBk = 64;
+
+__device__ inline uint32_t unit_off(int r, int c) {
+  return static_cast<uint32_t>((r * (kBk / 8) + (c ^ ((r >> 1) & 7))) * 16);
+}
+
+template <int TM, int TN, int WM, int WN, int S, bool GROUPED>
+__global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned tiles_j,
+                                                           unsigned tiles, int vec_y, int vec_l) {
+  constexpr int kWaves = WM * WN;
+  constexpr int kFi = TM / WM / 16;          // activation fragments of a wave
+  constexpr int kFj = TN / WN / 16;          // fragments of M
+  constexpr int kRows = TM + TN;
+  constexpr int kLoads = kRows / 8 / kWaves; // copies per wave and block
+  static_assert(kRows % (8 * kWaves) == 0, "copies divide evenly");
+  constexpr int kStage = kRows * kBk * 2;
+  constexpr int kScale = GROUPED ? kWaves * 512 : 0;    // a block's steps, per wave
+  constexpr int kOut = kLoads + (GROUPED ? 1 : 0);      // copies in flight per block
+  static_assert((TN / WN) <= 64, "a wave's steps fit its slot");
+  extern __shared__ __attribute__((aligned(16))) char lds[];   // S x (kStage + kScale)
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, c16 = lane & 15;
+  // each XCD (blocks b, b + 8, ...) walks a contiguous range of tiles
+  unsigned tile = blockIdx.x;
+  const unsigned per = tiles / 8;
+  if (tile < 8 * per) tile = (tile % 8) * per + tile / 8;
+  const int64_t jb = int64_t(tile % tiles_j) * TN;      // first row of M
+  const int64_t tb = int64_t(tile / tiles_j) * TM;      // first activation row
+  const int wi = (wv % WM) * (TM / WM), wj = (wv / WM) * (TN / WN);
+
+  int kblocks = a.kblocks;
+  const uint16_t* V = a.V;
+  int64_t ldv = a.ldv;
+  if (GROUPED) {
+    kblocks = __builtin_amdgcn_readfirstlane(a.plan[1]);
+    if (!__builtin_amdgcn_readfirstlane(a.plan[0]) || !V) {
+      V = a.V2;
+      ldv = a.ldv2;
+    }
+  }
+  const int32_t* grp = a.plan + kPlanHeader;
+  const char* vbase = reinterpret_cast<const char*>(V + tb * ldv);
+  const char* mbase = reinterpret_cast<const char*>(a.M + jb * a.ldm);
+  // copy i of this wave fills rows 8 (kLoads wv + i) .. + 7 of the stage:
+  // activation rows first, then rows of M
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = 8 * (kLoads * wv + i) + (lane >> 3);
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    const int64_t row = r < TM ? min<int64_t>(tb + r, a.n - 1) - tb
+                               : min<int64_t>(jb + r - TM, a.m - 1) - jb;
+    off[i] = static_cast<uint32_t>(row * (r < TM ? ldv : a.ldm) * 2 + 16 * c);
+  }
+  // copies of block kb into its stage (past the end: the last block again,
+  // into a stage nobody reads any more, so that every block counts alike)
+  auto fetch = [&](int kb) {
+    const int st = kb % S;
+    const int k = min(kb, kblocks - 1);
+    const int kv = GROUPED ? k : k % a.kwrap;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const bool act = 8 * (kLoads * wv + i) < TM;
+      const char* src = (act ? vbase + int64_t(kv) * (kBk * 2) : mbase + int64_t(k) * (kBk * 2)) + off[i];
+      __builtin_amdgcn_global_load_lds((gvoid)src,
+                                       (lvoid)(lds + st * (kStage + kScale) +
+                                               8 * (kLoads * wv + i) * (kBk * 2)),
+                                       16, 0, 0);
+    }
+    if (GROUPED) {
+      // the steps of the block's two 32-steps for the wave's rows of M:
+      // lanes 0 .. 15 the first, 16 .. 31 the second, four rows each
+      const int g0 = max(grp[2 * k], 0), g1 = max(grp[2 * k + 1], 0);
+      const float* src = a.scale_t + (lane & 16 ? g1 : g0) * a.mpad + jb + wj + 4 * c16;
+      if (lane < 32)
+        __builtin_amdgcn_global_load_lds((gvoid)src,
+                                         (lvoid)(lds + st * (kStage + kScale) + kStage + wv * 512),
+                                         16, 0, 0);
+    }
+  };
+  f32x4 acc[kFi][kFj];
+  f32x4 P[GROUPED ? kFi : 1][GROUPED ? kFj : 1];
+  const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kFi; ++i)
+#pragma unroll
+    for (int j = 0; j < kFj; ++j) {
+      acc[i][j] = zero;
+      if (GROUPED) P[i][j] = zero;
+    }
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(s);
+  for (int kb = 0; kb < kblocks; ++kb) {
+    wait_vmcnt<(S - 2) * kOut>();
+    // LDS reads of the stage that is filled next are done as well
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    fetch(kb + S - 1);
+    const char* la = lds + (kb % S) * (kStage + kScale);
+    const char* lm = la + TM * kBk * 2;
+    const float* sc = reinterpret_cast<const float*>(la + kStage + wv * 512);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4 fa[kFi], fm[kFj];
+#pragma unroll
+      for (int i = 0; i < kFi; ++i)
+        fa[i] = *reinterpret_cast<const u32x4*>(la + unit_off(wi + 16 * i + c16, 4 * s + q));
+#pragma unroll
+      for (int j = 0; j < kFj; ++j)
+        fm[j] = *reinterpret_cast<const u32x4*>(lm + unit_off(wj + 16 * j + c16, 4 * s + q));
+      if (GROUPED) {
+#pragma unroll
+        for (int i = 0; i < kFi; ++i)
+#pragma unroll
+          for (int j = 0; j < kFj; ++j) P[i][j] = mfma16(fm[j], fa[i], P[i][j]);
+        // the group ends with this step: fold its step Delta in
+        const int step = 2 * kb + s;
+        const bool last = step + 1 >= 2 * kblocks;
+        if (last || grp[step + 1] != grp[step]) {
+#pragma unroll
+          for (int j = 0; j < kFj; ++j) {
+            const f32x4 d = *reinterpret_cast<const f32x4*>(sc + 64 * s + 16 * j + 4 * q);
+#pragma unroll
+            for (int i = 0; i < kFi; ++i) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(d[v], P[i][j][v], acc[i][j][v]);
+              P[i][j] = zero;
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kFi; ++i)
+#pragma unroll
+          for (int j = 0; j < kFj; ++j) acc[i][j] = mfma16(fm[j], fa[i], acc[i][j]);
+      }
+    }
+  }
+  wait_vmcnt<0>();
+
+  // ---- the adapters' part: per adapter among the wave's rows one small
+  //      product, added to the rows of that adapter alone
+  if (a.L) {
+#pragma unroll
+    for (int i = 0; i < kFi; ++i) {
+      const int64_t t = tb + wi + 16 * i + c16;
+      const int id = t < a.n ? a.row[t] : -1;
+      uint32_t left = static_cast<uint32_t>(__ballot(id >= 0 && id < a.n_adapters)) & 0xFFFFu;
+      const uint16_t* part = a.parts + min<int64_t>(t, a.n - 1) * 3 * a.rp + 8 * q;
+      while (left) {
+        const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+        const bool mine = id == ad;
+        left &= ~static_cast<uint32_t>(__ballot(mine));
+        const uint16_t* Lm = a.L + int64_t(ad) * a.m * a.rank;
+        f32x4 D[kFj];
+#pragma unroll
+        for (int j = 0; j < kFj; ++j) D[j] = zero;
+        for (int b = 0; b < a.rp; b += 32) {
+          u32x4 fa[3];
+#pragma unroll
+          for (int p = 0; p < 3; ++p) fa[p] = *reinterpret_cast<const u32x4*>(part + p * a.rp + b);
+#pragma unroll
+          for (int j = 0; j < kFj; ++j) {
+            const int64_t r = min<int64_t>(jb + wj + 16 * j + c16, a.m - 1);
+            const u32x4 fm = load8(Lm + r * a.rank, b + 8 * q, a.rank, vec_l);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) D[j] = mfma16(fm, fa[p], D[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kFj; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (mine) acc[i][j][v] += D[j][v];
+      }
+    }
+  }
+  // ---- results
+#pragma unroll
+  for (int i = 0; i < kFi; ++i) {
+    const int64_t t = tb + wi + 16 * i + c16;
+    if (t >= a.n) continue;
+#pragma unroll
+    for (int j = 0; j < kFj; ++j) {
+      const int64_t r = jb + wj + 16 * j + 4 * q;
+      const f32x4 v = acc[i][j];
+      if (a.out_bf16) {
+        uint16_t* y = static_cast<uint16_t*>(a.Y) + t * a.ldy + r;
+        const uint32_t lo = uint32_t(f32_bf16(v[0])) | (uint32_t(f32_bf16(v[1])) << 16);
+        const uint32_t hi = uint32_t(f32_bf16(v[2])) | (uint32_t(f32_bf16(v[3])) << 16);
+        if (vec_y && r + 4 <= a.m) {
+          *reinterpret_cast<uint2*>(y) = uint2{lo, hi};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r + e < a.m) y[e] = static_cast<uint16_t>((e < 2 ? lo : hi) >> (16 * (e & 1)));
+        }
+      } else {
+        float* y = static_cast<float*>(a.Y) + t * a.ldy + r;
+        if (vec_y && r + 4 <= a.m) {
+          *reinterpret_cast<f32x4*>(y) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r + e < a.m) y[e] = v[e];
+        }
+      }
+    }
+  }
+}
+
+template <int TM, int TN, int WM, int WN, int S, bool GROUPED>
+gptq_status launch_tile(const GemmArgs& a, hipStream_t st) {
+  constexpr int lds =
+      S * ((TM + TN) * kBk * 2 + (GROUPED ? WM * WN * 512 : 0));
+  static_assert(lds <= 160 * 1024, "the ring fits the LDS");
+  const unsigned tj = ceil_div(a.m, TN);
+  const unsigned tiles = tj * ceil_div(a.n, TM);
+  const int item = a.out_bf16 ? 2 : 4;
+  const int vec_y = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.Y) % (4 * item) == 0;
+  const int vec_l = a.L && a.rank % 8 == 0 && reinterpret_cast<uintptr_t>(a.L) % 16 == 0;
+  gemm_kernel<TM, TN, WM, WN, S, GROUPED><<<tiles, WM * WN * 64, lds, st>>>(a, tj, tiles, vec_y, vec_l);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+}  // namespace
+
+int64_t plan_cols(int64_t d, int64_t ng) { return round_up(ng == 1 ? round_up(d, 32) : d + 31 * ng, 64); }
+
+size_t plan_words(int64_t d, int64_t ng) {
+  const int64_t cols = plan_cols(d, ng);
+  return size_t(kPlanHeader + cols / 32 + cols);
+}
+
+gptq_status launch_plan(const Packed& w, int32_t* plan, hipStream_t st) {
+  const unsigned grid = w.ng < 512 ? ceil_div(w.ng, 8) : 64;
+  plan_kernel<<<grid, kPlanThreads, 0, st>>>(w.g_idx, int(w.d), int(w.ng),
+                                             int(plan_cols(w.d, w.ng)), plan);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status launch_expand_grouped(const Packed& w, const int32_t* plan, uint16_t* M, int64_t ldm,
+                                  float* scale_t, int64_t mpad, hipStream_t st) {
+  const int64_t words = (w.d * w.bits + 31) / 32;
+  const int cols = int(plan_cols(w.d, w.ng));
+  const unsigned blocks = ceil_div(w.m * (cols / 8), 256);
+  const unsigned grid = blocks + ceil_div(w.m * w.ng, 256);
+#define GPTQ_EX(B)                                                                            \
+  expand_grouped_kernel<B><<<grid, 256, 0, st>>>(w, words, plan, cols, M, ldm, scale_t, mpad, blocks)
+  switch (w.bits) {
+    case 2: GPTQ_EX(2); break;
+    case 3: GPTQ_EX(3); break;
+    case 4: GPTQ_EX(4); break;
+    default: GPTQ_EX(8); break;
+  }
+#undef GPTQ_EX
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status launch_reorder(const uint16_t* V, int64_t ldv, int64_t n, int64_t d,
+                           const int32_t* plan, int64_t ng, int always, uint16_t* V2,
+                           int64_t ldv2, hipStream_t st) {
+  reorder_kernel<<<unsigned(n), 256, size_t(d) * 2, st>>>(V, ldv, int(d), plan,
+                                                          int(plan_cols(d, ng)), always, V2, ldv2);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status launch_pad_rows(const uint16_t* V, int64_t ldv, int64_t n, int64_t len, uint16_t* V2,
+                            int64_t cols, hipStream_t st) {
+  const bool vec = ldv % 8 == 0 && reinterpret_cast<uintptr_t>(V) % 16 == 0;
+  pad_rows_kernel<<<ceil_div(n * (cols / 8), 256), 256, 0, st>>>(V, ldv, n, len, V2, cols, vec);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status launch_expand_parts(const Packed& w, uint16_t* M, int64_t ldp, hipStream_t st) {
+  expand_parts_kernel<<<ceil_div(w.m * (ldp / 8), 256), 256, 0, st>>>(
+      w, (w.d * w.bits + 31) / 32, M, ldp);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status launch_expand_transposed(const Packed& w, uint16_t* M, int64_t ldm, hipStream_t st) {
+  const int64_t words = (w.d * w.bits + 31) / 32;
+  const dim3 grid(ceil_div(w.d, 64), ceil_div(ldm, 64));
+  switch (w.bits) {
+    case 2: expand_transposed_kernel<2><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
+    case 3: expand_transposed_kernel<3><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
+    case 4: expand_transposed_kernel<4><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
+    default: expand_transposed_kernel<8><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
+  }
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status launch_gemm(const GemmArgs& a, bool grouped, hipStream_t st) {
+  // the widest tile that still gives every CU one: wide tiles read less per
+  // product, narrow ones fill the chip where there are few rows
+  auto fills = [&](int tm, int tn) {
+    return int64_t(ceil_div(a.n, tm)) * ceil_div(a.m, tn) >= 256;
+  };
+  if (grouped) {
+    if (fills(256, 128)) return launch_tile<256, 128, 4, 2, 3, true>(a, st);
+    if (a.n > 64 && fills(128, 64)) return launch_tile<128, 64, 4, 1, 3, true>(a, st);
+    if (a.n > 32) return launch_tile<64, 64, 2, 2, 3, true>(a, st);
+    return launch_tile<32, 32, 1, 2, 3, true>(a, st);
+  }
+  if (fills(256, 128)) return launch_tile<256, 128, 4, 2, 3, false>(a, st);
+  if (a.n > 64 && fills(128, 128)) return launch_tile<128, 128, 2, 2, 3, false>(a, st);
+  if (a.n > 32) return launch_tile<64, 64, 2, 2, 3, false>(a, st);
+  return launch_tile<32, 32, 1, 2, 3, false>(a, st);
+}
+
+}  // namespace gptq

@@ -41,12 +41,12 @@ def test_lora_matmul_refuses(lib):
                dict(ad=adapters(rank=129)), dict(ad=adapters(A=None)), dict(ad=adapters(B=None)),
                dict(ad=adapters(alpha=None)), dict(ad=adapters(row=None))):
         assert lora(lib, **kw) == INV, kw
-    need = lib.gptq_lora_workspace_bytes(4, 32, 64, 8)
+    need = lib.gptq_lora_workspace_bytes(4, 32, 64, 32, 8)
     assert need > 0
     assert lora(lib, wsb=need - 1) == WS and lora(lib, ws=None) == WS
     assert lora(lib, n=0, X=None, Y=None, qw=None, ws=None, wsb=0) == gq.GPTQ_OK
-    for bad in ((-1, 32, 64, 8), (524281, 32, 64, 8), (4, 0, 64, 8), (4, 32, 65536, 8),
-                (4, 32, 64, 0), (4, 32, 64, 129)):
+    for bad in ((-1, 32, 64, 32, 8), (524281, 32, 64, 32, 8), (4, 0, 64, 32, 8),
+                (4, 32, 65536, 32, 8), (4, 32, 64, 32, 0), (4, 32, 64, 32, 129), (4, 32, 64, 0, 8)):
         assert lib.gptq_lora_workspace_bytes(*bad) == 0
 
 

@@ -163,6 +163,11 @@ SHAPES = [
     (1030, 1100, 256, 4, 64, "natural", 2, 64, "runs"),
     (3, 1, 1, 4, -1, "natural", 2, 2, "each"),
     (40, 3, 5, 2, 2, "natural", 2, 3, "random"),
+    # wide enough for the widest tiles: every tile of the chip's, ragged at both ends
+    (2100, 4200, 320, 4, 64, "natural", 5, 16, "runs"),
+    (2100, 4200, 161, 3, 128, "act", 70, 33, "random"),
+    (2100, 4200, 96, 2, 8, "natural", 2, 8, "one"),
+    (1100, 2100, 200, 8, 32, "natural", 3, 100, "runs"),
 ]
 
 
@@ -196,6 +201,8 @@ BACK = [
     (16, 515, 96, 2, 8, "natural"), (33, 129, 640, 4, 128, "natural"), (64, 128, 128, 8, -1, "natural"),
     (130, 260, 1000, 4, 128, "any"), (300, 1000, 300, 3, 64, "act"), (520, 640, 1100, 4, 128, "natural"),
     (3, 1, 1, 4, -1, "natural"), (1025, 257, 513, 2, 64, "natural"),
+    (2100, 200, 4200, 4, 128, "natural"), (1100, 320, 2100, 4, 64, "act"),
+    (4200, 130, 4200, 8, 32, "natural"),
 ]
 
 
@@ -277,6 +284,8 @@ GRADS = [
     (1030, 300, 640, 4, 128, "natural", 9, 8, "runs"),
     (2500, 130, 96, 4, 32, "natural", 3, 128, "random"),
     (3, 1, 1, 4, -1, "natural", 2, 2, "each"),
+    (2100, 128, 4200, 4, 128, "natural", 5, 16, "runs"),
+    (2100, 160, 4200, 4, 32, "natural", 3, 64, "random"),
 ]
 
 
@@ -391,7 +400,7 @@ def test_another_stream_and_two_at_once(dev):
 
 def test_given_workspace(dev):
     c = make_call(dev, n=130)
-    need = gq.gptq_lora_workspace_bytes(130, c["m"], c["d"], c["r"])
+    need = gq.gptq_lora_workspace_bytes(130, c["m"], c["d"], 32, c["r"])
     back = gq.gptq_lora_backward_workspace_bytes(130, c["m"], c["d"], c["r"], c["L"])
     ws = torch.full((max(need, back),), 255, dtype=torch.uint8, device=dev)
     Y, H = forward(c)
