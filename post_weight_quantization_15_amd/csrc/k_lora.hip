@@ -378,6 +378,7 @@ int parts_rank(int rank) { return rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
 // ---- workspaces
 struct LoraWs {
+  float* hidden;
   uint16_t* parts;
   float* sums;
   int32_t* plan;
@@ -386,26 +387,29 @@ struct LoraWs {
   uint16_t* V2;
 };
 
-bool grouped_path(int64_t group) { return group == -1 || group >= 32; }
+// How the shared product is laid out: by groups that fold, by the row's one
+// step, or (groups narrower than a matrix step) as parts of the weights.
+enum { kByGroups, kByRow, kByParts };
+int layout_of(int64_t group) { return group == -1 ? kByRow : group >= 32 ? kByGroups : kByParts; }
 
 LoraWs carve_lora(Carver& c, int64_t n, int64_t m, int64_t d, int64_t group, int rank) {
   const int64_t nc = std::min<int64_t>(n, kRowChunk);
   const int64_t ng = group > 0 ? (d + group - 1) / group : 1;
   LoraWs w{};
+  if (decode_takes(n, ng)) {
+    w.hidden = c.take<float>(size_t(n) * rank);
+    return w;
+  }
   w.parts = c.take<uint16_t>(size_t(nc) * 3 * parts_rank(rank));
   const int shares = shrink_shares(nc, d);
   w.sums = c.take<float>(shares > 1 ? size_t(shares) * nc * rank : 0);
-  if (grouped_path(group)) {
-    const int64_t cols = plan_cols(d, ng), mpad = round_up(m, 256) + 64;
-    w.plan = c.take<int32_t>(plan_words(d, ng));
-    w.M = c.take<uint16_t>(size_t(m) * cols);
-    w.scale_t = c.take<float>(size_t(ng) * mpad);
-    w.V2 = c.take<uint16_t>(size_t(nc) * cols);
-  } else {
-    const int64_t ldp = round_up(d, 64);
-    w.M = c.take<uint16_t>(size_t(m) * 3 * ldp);
-    w.V2 = c.take<uint16_t>(size_t(nc) * ldp);
-  }
+  const int64_t mpad = round_up(m, 256) + 64, ldp = round_up(d, 64);
+  const int lay = layout_of(group);
+  const int64_t cols = lay == kByGroups ? plan_cols(d, ng, group) : ldp;
+  if (lay == kByGroups) w.plan = c.take<int32_t>(plan_words(d, ng, group));
+  if (lay != kByParts) w.scale_t = c.take<float>(size_t(ng) * mpad);
+  w.M = c.take<uint16_t>(size_t(m) * (lay == kByParts ? 3 * ldp : cols));
+  w.V2 = c.take<uint16_t>(size_t(nc) * cols);
   return w;
 }
 
@@ -449,9 +453,12 @@ gptq_status launch_lora(const uint16_t* X, int64_t ldx, int64_t n, const Packed&
                         void* ws, hipStream_t st) {
   Carver c(ws);
   const LoraWs b = carve_lora(c, n, w.m, w.d, w.group, ad.rank);
-  const bool grouped = grouped_path(w.group);
+  if (decode_takes(n, w.ng))
+    return launch_lora_decode(X, ldx, n, w, ad, H ? H : b.hidden, Y, out_bf16, ldy, st);
+  const int lay = layout_of(w.group);
   const bool direct = as_is(X, ldx, w.d);
   const int rp = parts_rank(ad.rank);
+  const int64_t ldp = round_up(w.d, 64);
   GemmArgs g{};
   g.m = w.m;
   g.M = b.M;
@@ -462,21 +469,24 @@ gptq_status launch_lora(const uint16_t* X, int64_t ldx, int64_t n, const Packed&
   g.parts = b.parts;
   g.ldy = ldy;
   g.out_bf16 = out_bf16;
+  g.mpad = round_up(w.m, 256) + 64;
+  g.scale_t = b.scale_t;
+  g.kwrap = int(ldp / 64);
   gptq_status s;
-  if (grouped) {
-    const int64_t cols = plan_cols(w.d, w.ng);
+  if (lay == kByGroups) {
     g.plan = b.plan;
-    g.mpad = round_up(w.m, 256) + 64;
-    g.scale_t = b.scale_t;
-    g.ldm = g.ldv2 = cols;
+    g.ldm = g.ldv2 = plan_cols(w.d, w.ng, w.group);
     g.V2 = b.V2;
     if ((s = launch_plan(w, b.plan, st)) != GPTQ_OK) return s;
-    if ((s = launch_expand_grouped(w, b.plan, b.M, cols, b.scale_t, g.mpad, st)) != GPTQ_OK) return s;
+    if ((s = launch_expand_grouped(w, b.plan, b.M, g.ldm, b.scale_t, g.mpad, st)) != GPTQ_OK)
+      return s;
+  } else if (lay == kByRow) {
+    g.ldm = ldp;
+    g.kblocks = g.kwrap;
+    if ((s = launch_expand_row(w, b.M, ldp, b.scale_t, st)) != GPTQ_OK) return s;
   } else {
-    const int64_t ldp = round_up(w.d, 64);
     g.ldm = 3 * ldp;
-    g.kblocks = int(3 * ldp / 64);
-    g.kwrap = int(ldp / 64);
+    g.kblocks = 3 * g.kwrap;
     if ((s = launch_expand_parts(w, b.M, ldp, st)) != GPTQ_OK) return s;
   }
   for (int64_t t0 = 0; t0 < n; t0 += kRowChunk) {
@@ -488,19 +498,19 @@ gptq_status launch_lora(const uint16_t* X, int64_t ldx, int64_t n, const Packed&
     if ((s = launch_shrink(h, st)) != GPTQ_OK) return s;
     g.V = direct ? Xc : nullptr;
     g.ldv = ldx;
-    if (grouped) {
-      if ((s = launch_reorder(Xc, ldx, nc, w.d, b.plan, w.ng, !direct, b.V2, g.ldv2, st)) != GPTQ_OK)
+    if (lay == kByGroups) {
+      if ((s = launch_reorder(Xc, ldx, nc, w, b.plan, !direct, b.V2, g.ldv2, st)) != GPTQ_OK)
         return s;
     } else if (!direct) {
-      if ((s = launch_pad_rows(Xc, ldx, nc, w.d, b.V2, round_up(w.d, 64), st)) != GPTQ_OK) return s;
+      if ((s = launch_pad_rows(Xc, ldx, nc, w.d, b.V2, ldp, st)) != GPTQ_OK) return s;
       g.V = b.V2;
-      g.ldv = round_up(w.d, 64);
+      g.ldv = ldp;
     }
     g.n = nc;
     g.row = ad.row + t0;
     g.Y = out_bf16 ? static_cast<void*>(static_cast<uint16_t*>(Y) + t0 * ldy)
                    : static_cast<void*>(static_cast<float*>(Y) + t0 * ldy);
-    if ((s = launch_gemm(g, grouped, st)) != GPTQ_OK) return s;
+    if ((s = launch_gemm(g, lay == kByGroups ? fold_unit(w.group) : 0, st)) != GPTQ_OK) return s;
   }
   return GPTQ_OK;
 }
@@ -585,7 +595,7 @@ gptq_status launch_lora_backward(const uint16_t* dY, int64_t lddy, int64_t n, co
     g.row = adp ? ad.row + t0 : nullptr;
     g.parts = adp ? b.parts + t0 * 3 * rp : nullptr;
     g.Y = dX + t0 * lddx;
-    if ((s = launch_gemm(g, false, st)) != GPTQ_OK) return s;
+    if ((s = launch_gemm(g, 0, st)) != GPTQ_OK) return s;
   }
   return GPTQ_OK;
 }

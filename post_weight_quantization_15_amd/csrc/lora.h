@@ -22,9 +22,9 @@ struct GemmArgs {
   const uint16_t* M;       // [m][ldm]
   int64_t ldm, m;
   int kblocks, kwrap;      // blocks of 64 of M; V repeats after kwrap blocks
-  // groups: per 32-step the group whose step Delta multiplies its sums
-  const int32_t* plan;     // header {in order, kblocks}, then the group per 32-step
-  const float* scale_t;    // [ng][mpad] steps
+  // groups: per unit of columns the group whose step Delta multiplies its sums
+  const int32_t* plan;     // header {in order, kblocks}, then the group per unit
+  const float* scale_t;    // [ng][mpad] steps (without a plan: [mpad], or NULL)
   int64_t mpad;
   // the adapters' part: parts [n][3 rp] (three bf16 parts of alpha H), L_a [m][rank] rows
   const uint16_t* parts;
@@ -40,16 +40,21 @@ constexpr int kPlanHeader = 16;   // words before the plan's group list
 // Rows of activations handled at once (bounds the reordered copy).
 constexpr int64_t kRowChunk = 16384;
 
-// Columns in group order, every group padded to whole 32-steps, and all to 64.
-int64_t plan_cols(int64_t d, int64_t ng);
-size_t plan_words(int64_t d, int64_t ng);
+// Columns in group order, every group padded to whole units (64
+// columns where they divide the group size, else 32), and all to whole blocks.
+int fold_unit(int64_t group);
+int64_t plan_cols(int64_t d, int64_t ng, int64_t group);
+size_t plan_words(int64_t d, int64_t ng, int64_t group);
 gptq_status launch_plan(const Packed& w, int32_t* plan, hipStream_t st);
 // M[j][k] = code - zero, exact in bf16, in the plan's column order; scale_t = steps transposed.
 gptq_status launch_expand_grouped(const Packed& w, const int32_t* plan, uint16_t* M, int64_t ldm,
                                   float* scale_t, int64_t mpad, hipStream_t st);
+// The same for the whole-row grid, in the columns' own order.
+gptq_status launch_expand_row(const Packed& w, uint16_t* M, int64_t ldm, float* scale,
+                              hipStream_t st);
 // V2[t][k] = V[t][order[k]] where the plan is not the natural order (or always).
-gptq_status launch_reorder(const uint16_t* V, int64_t ldv, int64_t n, int64_t d,
-                           const int32_t* plan, int64_t ng, int always, uint16_t* V2, int64_t ldv2,
+gptq_status launch_reorder(const uint16_t* V, int64_t ldv, int64_t n, const Packed& w,
+                           const int32_t* plan, int always, uint16_t* V2, int64_t ldv2,
                            hipStream_t st);
 // M[j][p ldp + c] = part p of three of W_hat[j][c] in bf16 (their sum is exact in fp32).
 gptq_status launch_expand_parts(const Packed& w, uint16_t* M, int64_t ldp, hipStream_t st);
@@ -58,7 +63,15 @@ gptq_status launch_expand_transposed(const Packed& w, uint16_t* M, int64_t ldm, 
 // V2[t][0 .. cols) = V[t][0 .. len) and zeros.
 gptq_status launch_pad_rows(const uint16_t* V, int64_t ldv, int64_t n, int64_t len, uint16_t* V2,
                             int64_t cols, hipStream_t st);
-gptq_status launch_gemm(const GemmArgs& a, bool grouped, hipStream_t st);
+// fold: the unit of columns whose sums one step multiplies; 0: none.
+gptq_status launch_gemm(const GemmArgs& a, int fold, hipStream_t st);
+
+// Few rows (lora_decode.hip): no workspace but H [n][rank].
+constexpr int64_t kDecodeMaxRows = 64;
+bool decode_takes(int64_t n, int64_t ng);
+gptq_status launch_lora_decode(const uint16_t* X, int64_t ldx, int64_t n, const Packed& w,
+                               const gptq_adapters& ad, float* H, void* Y, int out_bf16,
+                               int64_t ldy, hipStream_t st);
 
 #ifdef __HIPCC__
 namespace {

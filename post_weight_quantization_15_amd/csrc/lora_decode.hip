@@ -1,0 +1,388 @@
+// The adapter product for few activation rows (single tokens of up to 64
+// requests): the packed weights are read once, straight into matrix-core
+// operands, and nothing is laid out first.
+//
+// hidden_kernel: H[t][p] = X[t] . A_a[p], one wave per value (fp32, exact
+//   bf16 products in pairs); the rows of A are the traffic.
+// decode_kernel: a workgroup of eight waves owns 16 output rows; the waves
+//   share the input dimension in chunks of 128 columns.  In a chunk lane
+//   (j, q) loads the 32 codes of row j, columns 32 q .. 32 q + 31, in one
+//   load (16 rows x 64 bytes at 4 bits), four register swaps turn them so that
+//   the lane holds columns 32 s + 8 q .. + 7 of each 32-step s, and each
+//   8-code run becomes a matrix operand in about ten instructions.
+//
+// A 32-step whose columns share one group enters as exact small numbers -- 16
+// + k for 2 to 4 bits (the code in the mantissa under the exponent of 16), k
+// for 8 -- and the group's grid comes out of the sums: acc += Delta (P - zz
+// Xs) with Xs = sum x from one more product with ones and zz the zero point
+// (plus 16).  A step that mixes groups (act-order, groups under 32) forms
+// Delta (code - zero) per column in fp32 and multiplies its three bf16 parts.
+// The grids of the 16 rows lie in LDS for both.
+#include "lora.h"
+
+namespace gptq {
+namespace {
+
+constexpr int kDecodeRows = 16;            // output rows per workgroup
+constexpr int kDecodeWaves = 8;
+constexpr int kDecodeMaxGroups = 768;      // 96 KB of grids in LDS
+
+// ---------------------------------------------------------------------------
+struct HiddenArgs {
+  const uint16_t* X;
+  int64_t ldx, d;
+  const uint16_t* A;
+  const int32_t* row;
+  int n_adapters, rank;
+  float* H;
+};
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ inline float dot2(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
+                                         __builtin_bit_cast(bf16x2, b), c, false);
+}
+__device__ inline float dot8(const u32x4& a, const u32x4& b, float c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = dot2(a[i], b[i], c);
+  return c;
+}
+
+__global__ __launch_bounds__(256) void hidden_kernel(HiddenArgs a, bool vec_x, bool vec_a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = blockIdx.y;
+  const int p = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (p >= a.rank) return;
+  const int id = a.row[t];
+  float s = 0.0f;
+  if (id >= 0 && id < a.n_adapters) {
+    const uint16_t* x = a.X + t * a.ldx;
+    const uint16_t* w = a.A + (int64_t(id) * a.rank + p) * a.d;
+#pragma unroll 8
+    for (int64_t c = 8 * lane; c < a.d; c += 512)
+      s = dot8(load8(x, c, a.d, vec_x), load8(w, c, a.d, vec_a), s);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  }
+  if (lane == 0) a.H[t * a.rank + p] = s;
+}
+
+// ---------------------------------------------------------------------------
+struct DecodeArgs {
+  const uint16_t* X;
+  int64_t ldx, n;
+  Packed w;
+  int64_t words;
+  const float* H;
+  const uint16_t* B;
+  const float* alpha;
+  const int32_t* row;
+  int n_adapters, rank;
+  void* Y;
+  int64_t ldy;
+  int out_bf16;
+};
+
+// Eight codes in nibbles as four bf16 pairs 16 + k, in order.
+__device__ inline u32x4 nibbles_to_bf16(uint32_t w) {
+  const uint32_t even = ((w << 3) & 0x78787878u) | 0x80808080u;
+  const uint32_t odd = ((w >> 1) & 0x78787878u) | 0x80808080u;
+  return u32x4{__builtin_amdgcn_perm(odd, even, 0x0C040C00u) | 0x41004100u,
+               __builtin_amdgcn_perm(odd, even, 0x0C050C01u) | 0x41004100u,
+               __builtin_amdgcn_perm(odd, even, 0x0C060C02u) | 0x41004100u,
+               __builtin_amdgcn_perm(odd, even, 0x0C070C03u) | 0x41004100u};
+}
+
+template <int BITS>
+struct Run {                               // the codes of an 8-column run
+  uint32_t w[BITS == 8 ? 2 : 1];
+};
+
+// Run `s` of the 32 codes in w[0 .. BITS).
+template <int BITS>
+__device__ inline Run<BITS> run_of(const uint32_t* w, int s) {
+  Run<BITS> r;
+  if constexpr (BITS == 4) {
+    r.w[0] = w[s];
+  } else if constexpr (BITS == 2) {
+    r.w[0] = (w[s >> 1] >> (16 * (s & 1))) & 0xFFFFu;
+  } else if constexpr (BITS == 3) {
+    const uint32_t v = s == 0 ? w[0] : s == 3 ? w[2] >> 8
+                     : __builtin_amdgcn_alignbit(w[s], w[s - 1], s == 1 ? 24 : 16);
+    r.w[0] = v & 0xFFFFFFu;
+  } else {
+    r.w[0] = w[2 * s];
+    r.w[1] = w[2 * s + 1];
+  }
+  return r;
+}
+
+// Spreads 3- and 2-bit fields to nibbles (4: as they are).
+template <int BITS>
+__device__ inline uint32_t to_nibbles(uint32_t w) {
+  if (BITS == 3) {
+    uint32_t u = (w & 0xFFFu) | ((w & 0xFFF000u) << 4);
+    u = (u & 0x003F003Fu) | ((u & 0x0FC00FC0u) << 2);
+    return (u & 0x07070707u) | ((u & 0x38383838u) << 1);
+  }
+  if (BITS == 2) {
+    uint32_t u = (w & 0xFFu) | ((w & 0xFF00u) << 8);
+    u = (u & 0x000F000Fu) | ((u & 0x00F000F0u) << 4);
+    return (u & 0x03030303u) | ((u & 0x0C0C0C0Cu) << 2);
+  }
+  return w;
+}
+
+// Unsigned code i of a run (signed codes arrive with their top bit flipped).
+template <int BITS>
+__device__ inline uint32_t run_code(const Run<BITS>& r, int i) {
+  if (BITS == 8) return (r.w[(i >> 2) % (BITS == 8 ? 2 : 1)] >> (8 * (i & 3))) & 0xFFu;
+  return (r.w[0] >> (BITS * i)) & ((1u << BITS) - 1u);
+}
+
+template <int BITS>
+__device__ inline u32x4 run_operand(const Run<BITS>& r) {
+  if constexpr (BITS == 8) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = r.w[i >> 1] >> (16 * (i & 1));
+      o[i] = __builtin_amdgcn_perm(__float_as_uint(static_cast<float>((v >> 8) & 0xFFu)),
+                                   __float_as_uint(static_cast<float>(v & 0xFFu)), 0x07060302u);
+    }
+    return o;
+  } else {
+    return nibbles_to_bf16(to_nibbles<BITS>(r.w[0]));
+  }
+}
+
+// Every code's top bit, for the runs' word layouts.
+template <int BITS>
+constexpr uint32_t top_bits() {
+  return BITS == 8 ? 0x80808080u : BITS == 4 ? 0x88888888u : BITS == 3 ? 0x00924924u : 0x0000AAAAu;
+}
+
+// Turns the 4 x 4 block that lanes q = 0 .. 3 (16 lanes each) hold in r[0 .. 3]:
+// lane q's r[s] becomes lane s's r[q].
+__device__ inline void turn4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  auto x = __builtin_amdgcn_permlane32_swap(a, c, false, false);
+  auto y = __builtin_amdgcn_permlane32_swap(b, d, false, false);
+  auto u = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
+  auto v = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
+  a = u[0];
+  b = u[1];
+  c = v[0];
+  d = v[1];
+}
+
+template <int BITS, int NT>
+__global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a, bool vec_x,
+                                                                   bool vec_w) {
+  constexpr int kW = BITS == 8 ? 8 : BITS;      // words of 32 codes
+  extern __shared__ __attribute__((aligned(16))) float grid[];   // [ng][16 rows] (Delta, zz)
+  __shared__ float red[kDecodeWaves][NT][16][17];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, c16 = lane & 15;
+  const Packed& w = a.w;
+  const int64_t j0 = int64_t(blockIdx.x) * kDecodeRows;
+  const int64_t jr = min<int64_t>(j0 + c16, w.m - 1);
+  const int ng = static_cast<int>(w.ng);
+  const int chunks = static_cast<int>((w.d + 127) / 128);
+  const uint32_t* wrow = w.qw + jr * a.words;
+
+  auto load_codes = [&](int ch, uint32_t* v) {
+    const int64_t at = int64_t(ch) * (4 * kW) + q * kW;     // first word of the lane's 32 codes
+    if (vec_w && at + kW <= a.words) {
+      if constexpr (BITS == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(wrow + at);
+        v[0] = u.x;
+        v[1] = u.y;
+      } else if constexpr (BITS == 3) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[i] = wrow[at + i];
+      } else {
+#pragma unroll
+        for (int h = 0; h < kW / 4; ++h) {
+          const u32x4 u = *reinterpret_cast<const u32x4*>(wrow + at + 4 * h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[4 * h + i] = u[i];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kW; ++i) v[i] = at + i < a.words ? wrow[at + i] : 0u;
+    }
+  };
+  // the first chunks' codes are on their way while the grids are staged
+  constexpr int kAhead = BITS == 8 ? 2 : 4;
+  uint32_t codes[kAhead][kW];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (wv + kDecodeWaves * u < chunks) load_codes(wv + kDecodeWaves * u, codes[u]);
+
+  constexpr bool kMagic = BITS != 8;
+  for (int e = tid; e < ng * kDecodeRows; e += kDecodeWaves * 64) {
+    const int r = e / ng, g = e % ng;
+    const int64_t at = min<int64_t>(j0 + r, w.m - 1) * ng + g;
+    grid[(g * kDecodeRows + r) * 2] = step_at(w, at);
+    grid[(g * kDecodeRows + r) * 2 + 1] =
+        w.sgn ? static_cast<float>(1 << (BITS - 1)) : static_cast<float>(w.zeros[at]);
+  }
+  __syncthreads();
+
+  f32x4 acc[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const u32x4 ones = u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  const uint16_t* xr[NT];
+  bool on[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    on[i] = 16 * i + c16 < a.n;
+    xr[i] = a.X + (on[i] ? 16 * i + c16 : 0) * a.ldx;
+  }
+
+  for (int cb = wv; cb < chunks; cb += kDecodeWaves * kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int ch = cb + kDecodeWaves * u;
+      if (ch >= chunks) break;
+      const int64_t k0 = int64_t(ch) * 128;
+      u32x4 x[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          x[i][s] = u32x4{0u, 0u, 0u, 0u};
+          if (on[i]) x[i][s] = load8(xr[i], k0 + 32 * s + 8 * q, w.d, vec_x);
+        }
+      // group ids of columns 2 lane, 2 lane + 1 of the chunk
+      const int64_t gc = k0 + 2 * lane;
+      const int ga = w.g_idx[min<int64_t>(gc, w.d - 1)], gb = w.g_idx[min<int64_t>(gc + 1, w.d - 1)];
+      Run<BITS> run[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) run[s] = run_of<BITS>(codes[u], s);
+      {
+        const int nx = ch + kDecodeWaves * kAhead;
+        if (nx < chunks) load_codes(nx, codes[u]);
+      }
+#pragma unroll
+      for (int h = 0; h < (BITS == 8 ? 2 : 1); ++h)
+        turn4(run[0].w[h], run[1].w[h], run[2].w[h], run[3].w[h]);
+      if (w.sgn) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int h = 0; h < (BITS == 8 ? 2 : 1); ++h) run[s].w[h] ^= top_bits<BITS>();
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (k0 + 32 * s >= w.d) break;
+        const int G = __builtin_amdgcn_readlane(ga, 16 * s);
+        const uint64_t diff = __ballot(ga != G || gb != G);
+        if (!((diff >> (16 * s)) & 0xFFFFu)) {
+          const u32x4 m = run_operand<BITS>(run[s]);
+          const int gi = min(max(G, 0), ng - 1);
+          const float dl = grid[(gi * kDecodeRows + c16) * 2];
+          const float zz = grid[(gi * kDecodeRows + c16) * 2 + 1] + (kMagic ? 16.0f : 0.0f);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
+            const f32x4 P = mfma16(x[i][s], m, z), Xs = mfma16(x[i][s], ones, z);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(dl, fmaf(-zz, Xs[v], P[v]), acc[i][v]);
+          }
+        } else {
+          u32x4 part[3] = {};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int src = 16 * s + 4 * q + (i >> 1);
+            const int g = min(max(__shfl(i & 1 ? gb : ga, src), 0), ng - 1);
+            const float dl = grid[(g * kDecodeRows + c16) * 2];
+            const float zz = grid[(g * kDecodeRows + c16) * 2 + 1];
+            uint16_t p[3];
+            split3(dl * (static_cast<float>(run_code<BITS>(run[s], i)) - zz), p);
+#pragma unroll
+            for (int h = 0; h < 3; ++h) part[h][i >> 1] |= uint32_t(p[h]) << (16 * (i & 1));
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int h = 0; h < 3; ++h) acc[i] = mfma16(x[i][s], part[h], acc[i]);
+        }
+      }
+    }
+  }
+  // ---- the waves' shares, in their order, and the adapter's part
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[wv][i][4 * q + v][c16] = acc[i][v];
+  __syncthreads();
+  for (int e = tid; e < NT * 256; e += kDecodeWaves * 64) {
+    const int64_t t = e >> 4, j = j0 + (e & 15);
+    if (t >= a.n || j >= w.m) continue;
+    float y = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kDecodeWaves; ++v) y += red[v][e >> 8][(e >> 4) & 15][e & 15];
+    const int id = a.row[t];
+    if (id >= 0 && id < a.n_adapters) {
+      const uint16_t* b = a.B + (int64_t(id) * w.m + j) * a.rank;
+      const float* h = a.H + t * a.rank;
+      float s = 0.0f;
+      int p = 0;
+      if (a.rank % 8 == 0 && reinterpret_cast<uintptr_t>(a.B) % 16 == 0)
+        for (; p < a.rank; p += 8) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(b + p);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            s = fmaf(h[p + i], bf16_f32((v[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), s);
+        }
+      for (; p < a.rank; ++p) s = fmaf(h[p], bf16_f32(b[p]), s);
+      y = fmaf(a.alpha[id], s, y);
+    }
+    if (a.out_bf16) static_cast<uint16_t*>(a.Y)[t * a.ldy + j] = f32_bf16(y);
+    else static_cast<float*>(a.Y)[t * a.ldy + j] = y;
+  }
+}
+
+template <int BITS>
+void launch_bits(const DecodeArgs& a, bool vx, bool vw, hipStream_t st) {
+  const unsigned grid = ceil_div(a.w.m, kDecodeRows);
+  const size_t lds = size_t(a.w.ng) * kDecodeRows * 8;
+  if (a.n <= 16) decode_kernel<BITS, 1><<<grid, kDecodeWaves * 64, lds, st>>>(a, vx, vw);
+  else if (a.n <= 32) decode_kernel<BITS, 2><<<grid, kDecodeWaves * 64, lds, st>>>(a, vx, vw);
+  else decode_kernel<BITS, 4><<<grid, kDecodeWaves * 64, lds, st>>>(a, vx, vw);
+}
+
+}  // namespace
+
+bool decode_takes(int64_t n, int64_t ng) { return n <= kDecodeMaxRows && ng <= kDecodeMaxGroups; }
+
+gptq_status launch_lora_decode(const uint16_t* X, int64_t ldx, int64_t n, const Packed& w,
+                               const gptq_adapters& ad, float* H, void* Y, int out_bf16,
+                               int64_t ldy, hipStream_t st) {
+  const bool vx = ldx % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;
+  const bool va = w.d % 8 == 0 && reinterpret_cast<uintptr_t>(ad.A) % 16 == 0;
+  const HiddenArgs h{X, ldx, w.d, static_cast<const uint16_t*>(ad.A), ad.row, ad.n_adapters,
+                     ad.rank, H};
+  hidden_kernel<<<dim3(ceil_div(ad.rank, 4), unsigned(n)), 256, 0, st>>>(h, vx, va);
+  GPTQ_CHECK_LAUNCH();
+  const int64_t words = (w.d * w.bits + 31) / 32;
+  const int bytes = w.bits == 2 ? 8 : w.bits == 3 ? 4 : 16;
+  const bool vw = words * 4 % bytes == 0 && reinterpret_cast<uintptr_t>(w.qw) % bytes == 0;
+  const DecodeArgs a{X, ldx, n, w, words, H, static_cast<const uint16_t*>(ad.B), ad.alpha, ad.row,
+                     ad.n_adapters, ad.rank, Y, ldy, out_bf16};
+  switch (w.bits) {
+    case 2: launch_bits<2>(a, vx, vw, st); break;
+    case 3: launch_bits<3>(a, vx, vw, st); break;
+    case 4: launch_bits<4>(a, vx, vw, st); break;
+    default: launch_bits<8>(a, vx, vw, st); break;
+  }
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+}  // namespace gptq

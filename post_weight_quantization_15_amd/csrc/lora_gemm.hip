@@ -15,6 +15,8 @@
 // products per weight and no fold.
 // Backward (dX = dY W_hat): the sum runs over output rows, each with its own
 // step, so no step factors out of it; M is W_hat^T rounded to bf16.
+#include <algorithm>
+
 #include "lora.h"
 
 namespace gptq {
@@ -22,7 +24,7 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // The plan: order[k] = column at place k (-1: padding) and the group of every
-// 32-step.  A wave places one group's columns, in their own order; every
+// unit of 32 or 64 places.  A wave places one group's columns, in their own order; every
 // workgroup counts all groups for itself (g_idx is small and stays in L2).
 // In natural order with whole steps per group the order is the identity and
 // the activations are used where they lie.
@@ -31,16 +33,17 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxGroups = 2048;      // groups of at least 32 columns, d <= 65535
 
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __restrict__ g_idx,
-                                                            int d, int ng, int cols_max,
+                                                            int d, int ng, int unit, int cols_max,
                                                             int32_t* __restrict__ plan) {
   __shared__ int32_t cnt[kPlanMaxGroups];
   __shared__ int32_t start[kPlanMaxGroups + 1];
   __shared__ int ident;
   const int tid = threadIdx.x, lane = tid & 63;
   int32_t* grp = plan + kPlanHeader;
-  int32_t* order = grp + cols_max / 32;
+  int32_t* order = grp + cols_max / unit;
+  const int block = max(unit, 64);
   for (int i = tid; i < ng; i += kPlanThreads) cnt[i] = 0;
-  if (tid == 0) ident = d % 64 == 0;
+  if (tid == 0) ident = d % block == 0;
   __syncthreads();
   bool inc = true;
   for (int c = tid; c < d; c += kPlanThreads) {
@@ -55,8 +58,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
     for (int b = 0; b < ng; b += 64) {
       const int g = b + lane;
       const int c = g < ng ? cnt[g] : 0;
-      if (c % 32) ident = 0;
-      int s = (c + 31) / 32 * 32;
+      if (c % unit) ident = 0;
+      int s = (c + unit - 1) / unit * unit;
       const int own = s;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -70,20 +73,19 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
   }
   __syncthreads();
   const int total = start[ng];
-  const int padded = (total + 63) / 64 * 64;
+  const int padded = (total + block - 1) / block * block;
   if (blockIdx.x == 0) {
     if (tid == 0) {
       plan[0] = ident;
       plan[1] = padded / 64;
     }
-    // the step that may pad the last block continues the last group
-    if (tid == 0 && padded > total) grp[total / 32] = total ? -1 : 0;
+    if (tid == 0 && padded > total) grp[total / unit] = -1;   // fills the last block
     for (int k = total + tid; k < padded; k += kPlanThreads) order[k] = -1;
   }
   const int nw = gridDim.x * (kPlanThreads / 64);
   for (int g = blockIdx.x * (kPlanThreads / 64) + (tid >> 6); g < ng; g += nw) {
     const int s = start[g], e = start[g + 1], n = cnt[g];
-    for (int k = s / 32 + lane; k < e / 32; k += 64) grp[k] = g;
+    for (int k = s / unit + lane; k < e / unit; k += 64) grp[k] = g;
     if (ident) {
       for (int k = s + lane; k < e; k += 64) order[k] = k;
       continue;
@@ -137,7 +139,8 @@ __device__ inline int signed_code(int c, int bits) {
 template <int BITS>
 __global__ __launch_bounds__(256) void expand_grouped_kernel(Packed w, int64_t words,
                                                              const int32_t* __restrict__ plan,
-                                                             int cols_max, uint16_t* __restrict__ M,
+                                                             int unit, int cols_max,
+                                                             uint16_t* __restrict__ M,
                                                              int64_t ldm,
                                                              float* __restrict__ scale_t,
                                                              int64_t mpad, unsigned blocks) {
@@ -154,8 +157,8 @@ __global__ __launch_bounds__(256) void expand_grouped_kernel(Packed w, int64_t w
   const int u = static_cast<int>(e % per);
   if (u >= units || j >= w.m) return;
   const int32_t* grp = plan + kPlanHeader;
-  const int32_t* order = grp + cols_max / 32;
-  const int g = grp[u / 4];
+  const int32_t* order = grp + cols_max / unit;
+  const int g = grp[8 * u / unit];
   u32x4 out = u32x4{0u, 0u, 0u, 0u};
   if (g >= 0) {
     const int z = w.sgn ? 0 : w.zeros[j * w.ng + g];
@@ -180,15 +183,41 @@ __global__ __launch_bounds__(256) void expand_grouped_kernel(Packed w, int64_t w
   *reinterpret_cast<u32x4*>(M + j * ldm + 8 * u) = out;
 }
 
+// The whole-row grid: the columns stay as they are.
+template <int BITS>
+__global__ __launch_bounds__(256) void expand_row_kernel(Packed w, int64_t words,
+                                                         uint16_t* __restrict__ M, int64_t ldm,
+                                                         float* __restrict__ scale,
+                                                         unsigned blocks) {
+  if (blockIdx.x >= blocks) {
+    const int64_t j = int64_t(blockIdx.x - blocks) * 256 + threadIdx.x;
+    if (j < w.m) scale[j] = step_at(w, j);
+    return;
+  }
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t per = ldm / 8, j = e / per, u = e % per;
+  if (j >= w.m) return;
+  const int z = w.sgn ? 0 : w.zeros[j];
+  int c[8];
+  codes8<BITS>(w.qw + j * words, words, u, c);
+  u32x4 out = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int v = 8 * u + i < w.d ? (w.sgn ? signed_code(c[i], BITS) : c[i]) - z : 0;
+    out[i >> 1] |= (__float_as_uint(static_cast<float>(v)) >> 16) << (16 * (i & 1));
+  }
+  *reinterpret_cast<u32x4*>(M + j * ldm + 8 * u) = out;
+}
+
 // One row per workgroup, through LDS (a row's gather is within itself).
 __global__ __launch_bounds__(256) void reorder_kernel(const uint16_t* __restrict__ V, int64_t ldv,
                                                       int d, const int32_t* __restrict__ plan,
-                                                      int cols_max, int always,
+                                                      int unit, int cols_max, int always,
                                                       uint16_t* __restrict__ V2, int64_t ldv2) {
   extern __shared__ uint16_t rowbuf[];
   if (plan[0] && !always) return;
   const int64_t t = blockIdx.x;
-  const int32_t* order = plan + kPlanHeader + cols_max / 32;
+  const int32_t* order = plan + kPlanHeader + cols_max / unit;
   const uint16_t* src = V + t * ldv;
   for (int c = threadIdx.x; c < d; c += 256) rowbuf[c] = src[c];
   __syncthreads();
@@ -304,7 +333,28 @@ __device__ inline uint32_t unit_off(int r, int c) {
   return static_cast<uint32_t>((r * (kBk / 8) + (c ^ ((r >> 1) & 7))) * 16);
 }
 
-template <int TM, int TN, int WM, int WN, int S, bool GROUPED>
+// P = A B and P += A B.  With two sets of accumulators the register allocator
+// moves whole sets about; IN_PLACE pins each to its registers (the product
+// written out, P tied).  The compiler then does not know that a matrix
+// instruction writes P: what reads P comes behind a barrier (its steps are
+// loaded there), or behind wait states written out.
+template <bool IN_PLACE>
+__device__ inline void open_sum(f32x4& P, const u32x4& a, const u32x4& b) {
+  if (IN_PLACE) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "+v"(P) : "v"(a), "v"(b));
+  else P = mfma16(a, b, f32x4{0.f, 0.f, 0.f, 0.f});
+}
+template <bool IN_PLACE>
+__device__ inline void add_sum(f32x4& P, const u32x4& a, const u32x4& b) {
+  if (IN_PLACE) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(P) : "v"(a), "v"(b));
+  else P = mfma16(a, b, P);
+}
+
+// FOLD = 0: one sum per output (times a row's step at the end where scale_t
+// is given); FOLD = 1, 2: every FOLD 32-steps are one group's, whose step
+// folds in.  The fold of a finished group runs fragment by fragment between
+// the matrix instructions that open the next one over its registers, so its
+// vector work hides behind them.
+template <int TM, int TN, int WM, int WN, int S, int FOLD>
 __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned tiles_j,
                                                            unsigned tiles, int vec_y, int vec_l) {
   constexpr int kWaves = WM * WN;
@@ -314,10 +364,13 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
   constexpr int kLoads = kRows / 8 / kWaves; // copies per wave and block
   static_assert(kRows % (8 * kWaves) == 0, "copies divide evenly");
   constexpr int kStage = kRows * kBk * 2;
-  constexpr int kScale = GROUPED ? kWaves * 512 : 0;    // a block's steps, per wave
-  constexpr int kOut = kLoads + (GROUPED ? 1 : 0);      // copies in flight per block
+  constexpr int kScale = FOLD ? kWaves * 512 : 0;       // a block's steps, per wave
+  constexpr int kOut = kLoads + (FOLD ? 1 : 0);         // copies in flight per block
+  constexpr bool kInPlace = kFi * kFj >= 16;
   static_assert((TN / WN) <= 64, "a wave's steps fit its slot");
-  extern __shared__ __attribute__((aligned(16))) char lds[];   // S x (kStage + kScale)
+  // S stages, then S + 1 blocks' steps: those of the block before the one in
+  // work are still there when its group folds
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, c16 = lane & 15;
@@ -332,14 +385,16 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
   int kblocks = a.kblocks;
   const uint16_t* V = a.V;
   int64_t ldv = a.ldv;
-  if (GROUPED) {
+  if (FOLD) {
     kblocks = __builtin_amdgcn_readfirstlane(a.plan[1]);
     if (!__builtin_amdgcn_readfirstlane(a.plan[0]) || !V) {
       V = a.V2;
       ldv = a.ldv2;
     }
   }
-  const int32_t* grp = a.plan + kPlanHeader;
+  // the units' groups, through the scalar cache (uniform, and no vector load
+  // whose wait would drain the copies in flight)
+  const auto grp = (const int32_t __attribute__((address_space(4)))*)(a.plan + kPlanHeader);
   const char* vbase = reinterpret_cast<const char*>(V + tb * ldv);
   const char* mbase = reinterpret_cast<const char*>(a.M + jb * a.ldm);
   // copy i of this wave fills rows 8 (kLoads wv + i) .. + 7 of the stage:
@@ -353,90 +408,152 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
                                : min<int64_t>(jb + r - TM, a.m - 1) - jb;
     off[i] = static_cast<uint32_t>(row * (r < TM ? ldv : a.ldm) * 2 + 16 * c);
   }
+  // groups of a block (past the end: the last one's)
+  auto groups_of = [&](int kb, int& ga, int& gb) {
+    const int k = min(kb, kblocks - 1);
+    ga = gb = 0;
+    if (FOLD == 1) {
+      ga = max(grp[2 * k], 0);
+      gb = max(grp[2 * k + 1], 0);
+    } else if (FOLD) {
+      ga = max(grp[k], 0);
+    }
+  };
   // copies of block kb into its stage (past the end: the last block again,
   // into a stage nobody reads any more, so that every block counts alike)
-  auto fetch = [&](int kb) {
+  auto fetch = [&](int kb, int ga, int gb) {
     const int st = kb % S;
     const int k = min(kb, kblocks - 1);
-    const int kv = GROUPED ? k : k % a.kwrap;
+    const int kv = FOLD ? k : k % a.kwrap;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const bool act = 8 * (kLoads * wv + i) < TM;
-      const char* src = (act ? vbase + int64_t(kv) * (kBk * 2) : mbase + int64_t(k) * (kBk * 2)) + off[i];
-      __builtin_amdgcn_global_load_lds((gvoid)src,
-                                       (lvoid)(lds + st * (kStage + kScale) +
+      const char* base = act ? vbase + int64_t(kv) * (kBk * 2) : mbase + int64_t(k) * (kBk * 2);
+      // opaque here, so that the copy takes a scalar base and a 32-bit offset
+      uint32_t o = off[i];
+      asm volatile("" : "+s"(base), "+v"(o));
+      __builtin_amdgcn_global_load_lds((gvoid)(base + o),
+                                       (lvoid)(lds + st * kStage +
                                                8 * (kLoads * wv + i) * (kBk * 2)),
                                        16, 0, 0);
     }
-    if (GROUPED) {
-      // the steps of the block's two 32-steps for the wave's rows of M:
-      // lanes 0 .. 15 the first, 16 .. 31 the second, four rows each
-      const int g0 = max(grp[2 * k], 0), g1 = max(grp[2 * k + 1], 0);
-      const float* src = a.scale_t + (lane & 16 ? g1 : g0) * a.mpad + jb + wj + 4 * c16;
+    if (FOLD) {
+      // the wave's rows' steps for the block's group (FOLD = 1: its two groups,
+      // lanes 0 .. 15 the first, 16 .. 31 the second), four rows a lane
+      const char* base = reinterpret_cast<const char*>(a.scale_t + int64_t(ga) * a.mpad + jb + wj);
+      uint32_t o = 16 * c16;
+      if (FOLD == 1 && gb != ga) {
+        const char* second = reinterpret_cast<const char*>(a.scale_t + int64_t(gb) * a.mpad + jb + wj);
+        if (lane & 16) base = second;
+      }
+      asm volatile("" : "+v"(o));
       if (lane < 32)
-        __builtin_amdgcn_global_load_lds((gvoid)src,
-                                         (lvoid)(lds + st * (kStage + kScale) + kStage + wv * 512),
+        __builtin_amdgcn_global_load_lds((gvoid)(base + o),
+                                         (lvoid)(lds + S * kStage + (kb % (S + 1)) * kScale + wv * 512),
                                          16, 0, 0);
     }
   };
+  // the lane's unit of its operand rows: 16 rows further is 2048 bytes on
+  // (the swizzle repeats), the second 32-step flips bit 2 of the unit
+  const uint32_t oa = unit_off(wi + c16, q), om = TM * kBk * 2 + unit_off(wj + c16, q);
   f32x4 acc[kFi][kFj];
-  f32x4 P[GROUPED ? kFi : 1][GROUPED ? kFj : 1];
+  f32x4 P[FOLD ? kFi : 1][FOLD ? kFj : 1];
   const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < kFi; ++i)
+  for (int j = 0; j < kFj; ++j) {
 #pragma unroll
-    for (int j = 0; j < kFj; ++j) {
+    for (int i = 0; i < kFi; ++i) {
       acc[i][j] = zero;
-      if (GROUPED) P[i][j] = zero;
+      if (FOLD) P[i][j] = zero;
     }
+  }
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) fetch(s);
+  for (int s = 0; s < S - 1; ++s) {
+    int ga, gb;
+    groups_of(s, ga, gb);
+    fetch(s, ga, gb);
+  }
+  if (FOLD) {                                // steps of the block before the first
+    float* none = reinterpret_cast<float*>(lds + S * kStage + S * kScale + wv * 512);
+    none[lane] = none[lane + 64] = 0.0f;
+  }
+  int na, nb;                                // groups of the next block to fetch
+  groups_of(S - 1, na, nb);
   for (int kb = 0; kb < kblocks; ++kb) {
     wait_vmcnt<(S - 2) * kOut>();
     // LDS reads of the stage that is filled next are done as well
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    fetch(kb + S - 1);
-    const char* la = lds + (kb % S) * (kStage + kScale);
-    const char* lm = la + TM * kBk * 2;
-    const float* sc = reinterpret_cast<const float*>(la + kStage + wv * 512);
+    fetch(kb + S - 1, na, nb);
+    groups_of(kb + S, na, nb);
+    const char* la = lds + (kb % S) * kStage;
+    // steps of this block and of the one before
+    const char* sc = lds + S * kStage + wv * 512 + 16 * q;
+    const char* sc0 = sc + ((kb + S) % (S + 1)) * kScale;
+    const char* sc1 = sc + (kb % (S + 1)) * kScale;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
+      // sums opened by this block's first step are read in its second: all
+      // of them behind the wait states a matrix result needs
+      if (FOLD == 1 && s && kInPlace) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_nop 7\n\ts_nop 7" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      }
       u32x4 fa[kFi], fm[kFj];
 #pragma unroll
       for (int i = 0; i < kFi; ++i)
-        fa[i] = *reinterpret_cast<const u32x4*>(la + unit_off(wi + 16 * i + c16, 4 * s + q));
+        fa[i] = *reinterpret_cast<const u32x4*>(la + (oa ^ (64 * s)) + 2048 * i);
 #pragma unroll
       for (int j = 0; j < kFj; ++j)
-        fm[j] = *reinterpret_cast<const u32x4*>(lm + unit_off(wj + 16 * j + c16, 4 * s + q));
-      if (GROUPED) {
+        fm[j] = *reinterpret_cast<const u32x4*>(la + (om ^ (64 * s)) + 2048 * j);
+      if (FOLD && s % (FOLD ? FOLD : 1) == 0) {
 #pragma unroll
-        for (int i = 0; i < kFi; ++i)
+        for (int j = 0; j < kFj; ++j) {
+          // the closing group's steps: the block before's (its second group
+          // where a block has two), or this block's first
+          const f32x4 d = *reinterpret_cast<const f32x4*>(
+              (FOLD == 1 && s ? sc1 : sc0 + (FOLD == 1 ? 256 : 0)) + 64 * j);
 #pragma unroll
-          for (int j = 0; j < kFj; ++j) P[i][j] = mfma16(fm[j], fa[i], P[i][j]);
-        // the group ends with this step: fold its step Delta in
-        const int step = 2 * kb + s;
-        const bool last = step + 1 >= 2 * kblocks;
-        if (last || grp[step + 1] != grp[step]) {
+          for (int i = 0; i < kFi; ++i) {
 #pragma unroll
-          for (int j = 0; j < kFj; ++j) {
-            const f32x4 d = *reinterpret_cast<const f32x4*>(sc + 64 * s + 16 * j + 4 * q);
-#pragma unroll
-            for (int i = 0; i < kFi; ++i) {
-#pragma unroll
-              for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(d[v], P[i][j][v], acc[i][j][v]);
-              P[i][j] = zero;
-            }
+            for (int v = 0; v < 4; ++v)
+              acc[i][j][v] = fmaf(d[v], P[i][j][v], acc[i][j][v]);
+            open_sum<kInPlace>(P[i][j], fm[j], fa[i]);
           }
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < kFi; ++i)
+        for (int j = 0; j < kFj; ++j)
 #pragma unroll
-          for (int j = 0; j < kFj; ++j) acc[i][j] = mfma16(fm[j], fa[i], acc[i][j]);
+          for (int i = 0; i < kFi; ++i) {
+            if (FOLD) add_sum<kInPlace>(P[FOLD ? i : 0][FOLD ? j : 0], fm[j], fa[i]);
+            else acc[i][j] = mfma16(fm[j], fa[i], acc[i][j]);
+          }
       }
     }
   }
   wait_vmcnt<0>();
+  if (FOLD) {
+    if (kInPlace) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    const char* sc = lds + S * kStage + ((kblocks - 1) % (S + 1)) * kScale + wv * 512 + 16 * q;
+#pragma unroll
+    for (int j = 0; j < kFj; ++j) {
+      const f32x4 d = *reinterpret_cast<const f32x4*>(sc + (FOLD == 1 ? 256 : 0) + 64 * j);
+#pragma unroll
+      for (int i = 0; i < kFi; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(d[v], P[i][j][v], acc[i][j][v]);
+    }
+  } else if (a.scale_t) {
+#pragma unroll
+    for (int j = 0; j < kFj; ++j) {
+      const f32x4 d = *reinterpret_cast<const f32x4*>(a.scale_t + jb + wj + 16 * j + 4 * q);
+#pragma unroll
+      for (int i = 0; i < kFi; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] *= d[v];
+    }
+  }
 
   // ---- the adapters' part: per adapter among the wave's rows one small
   //      product, added to the rows of that adapter alone
@@ -509,34 +626,53 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
   }
 }
 
-template <int TM, int TN, int WM, int WN, int S, bool GROUPED>
+template <int TM, int TN, int WM, int WN, int S, int FOLD>
 gptq_status launch_tile(const GemmArgs& a, hipStream_t st) {
-  constexpr int lds =
-      S * ((TM + TN) * kBk * 2 + (GROUPED ? WM * WN * 512 : 0));
+  constexpr int lds = S * (TM + TN) * kBk * 2 + (FOLD ? (S + 1) * WM * WN * 512 : 0);
   static_assert(lds <= 160 * 1024, "the ring fits the LDS");
   const unsigned tj = ceil_div(a.m, TN);
   const unsigned tiles = tj * ceil_div(a.n, TM);
   const int item = a.out_bf16 ? 2 : 4;
   const int vec_y = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.Y) % (4 * item) == 0;
   const int vec_l = a.L && a.rank % 8 == 0 && reinterpret_cast<uintptr_t>(a.L) % 16 == 0;
-  gemm_kernel<TM, TN, WM, WN, S, GROUPED><<<tiles, WM * WN * 64, lds, st>>>(a, tj, tiles, vec_y, vec_l);
+  gemm_kernel<TM, TN, WM, WN, S, FOLD><<<tiles, WM * WN * 64, lds, st>>>(a, tj, tiles, vec_y, vec_l);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
 
+// The widest tile that still gives every CU one: wide tiles read less per
+// product, narrow ones fill the chip where there are few rows.
+template <int FOLD>
+gptq_status launch_fold(const GemmArgs& a, hipStream_t st) {
+  auto fills = [&](int tm, int tn) {
+    return int64_t(ceil_div(a.n, tm)) * ceil_div(a.m, tn) >= 200;
+  };
+  if (fills(256, 128)) return launch_tile<256, 128, 4, 2, 3, FOLD>(a, st);
+  if (a.n > 64 && fills(128, 128)) return launch_tile<128, 128, 2, 2, 3, FOLD>(a, st);
+  if (a.n > 32) return launch_tile<64, 64, 2, 2, 3, FOLD>(a, st);
+  return launch_tile<32, 32, 1, 2, 3, FOLD>(a, st);
+}
+
 }  // namespace
 
-int64_t plan_cols(int64_t d, int64_t ng) { return round_up(ng == 1 ? round_up(d, 32) : d + 31 * ng, 64); }
+int fold_unit(int64_t group) {
+  return group % 64 == 0 ? 64 : 32;
+}
 
-size_t plan_words(int64_t d, int64_t ng) {
-  const int64_t cols = plan_cols(d, ng);
-  return size_t(kPlanHeader + cols / 32 + cols);
+int64_t plan_cols(int64_t d, int64_t ng, int64_t group) {
+  const int u = fold_unit(group);
+  return round_up(d + (u - 1) * ng, std::max(u, 64));
+}
+
+size_t plan_words(int64_t d, int64_t ng, int64_t group) {
+  const int64_t cols = plan_cols(d, ng, group);
+  return size_t(kPlanHeader + cols / fold_unit(group) + cols);
 }
 
 gptq_status launch_plan(const Packed& w, int32_t* plan, hipStream_t st) {
   const unsigned grid = w.ng < 512 ? ceil_div(w.ng, 8) : 64;
-  plan_kernel<<<grid, kPlanThreads, 0, st>>>(w.g_idx, int(w.d), int(w.ng),
-                                             int(plan_cols(w.d, w.ng)), plan);
+  plan_kernel<<<grid, kPlanThreads, 0, st>>>(w.g_idx, int(w.d), int(w.ng), fold_unit(w.group),
+                                             int(plan_cols(w.d, w.ng, w.group)), plan);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
@@ -544,11 +680,12 @@ gptq_status launch_plan(const Packed& w, int32_t* plan, hipStream_t st) {
 gptq_status launch_expand_grouped(const Packed& w, const int32_t* plan, uint16_t* M, int64_t ldm,
                                   float* scale_t, int64_t mpad, hipStream_t st) {
   const int64_t words = (w.d * w.bits + 31) / 32;
-  const int cols = int(plan_cols(w.d, w.ng));
+  const int cols = int(plan_cols(w.d, w.ng, w.group)), unit = fold_unit(w.group);
   const unsigned blocks = ceil_div(w.m * (cols / 8), 256);
   const unsigned grid = blocks + ceil_div(w.m * w.ng, 256);
 #define GPTQ_EX(B)                                                                            \
-  expand_grouped_kernel<B><<<grid, 256, 0, st>>>(w, words, plan, cols, M, ldm, scale_t, mpad, blocks)
+  expand_grouped_kernel<B><<<grid, 256, 0, st>>>(w, words, plan, unit, cols, M, ldm, scale_t, mpad, \
+                                                 blocks)
   switch (w.bits) {
     case 2: GPTQ_EX(2); break;
     case 3: GPTQ_EX(3); break;
@@ -560,11 +697,30 @@ gptq_status launch_expand_grouped(const Packed& w, const int32_t* plan, uint16_t
   return GPTQ_OK;
 }
 
-gptq_status launch_reorder(const uint16_t* V, int64_t ldv, int64_t n, int64_t d,
-                           const int32_t* plan, int64_t ng, int always, uint16_t* V2,
-                           int64_t ldv2, hipStream_t st) {
-  reorder_kernel<<<unsigned(n), 256, size_t(d) * 2, st>>>(V, ldv, int(d), plan,
-                                                          int(plan_cols(d, ng)), always, V2, ldv2);
+gptq_status launch_expand_row(const Packed& w, uint16_t* M, int64_t ldm, float* scale,
+                              hipStream_t st) {
+  const int64_t words = (w.d * w.bits + 31) / 32;
+  const unsigned blocks = ceil_div(w.m * (ldm / 8), 256);
+  const unsigned grid = blocks + ceil_div(w.m, 256);
+#define GPTQ_EX(B) \
+  expand_row_kernel<B><<<grid, 256, 0, st>>>(w, words, M, ldm, scale, blocks)
+  switch (w.bits) {
+    case 2: GPTQ_EX(2); break;
+    case 3: GPTQ_EX(3); break;
+    case 4: GPTQ_EX(4); break;
+    default: GPTQ_EX(8); break;
+  }
+#undef GPTQ_EX
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+gptq_status launch_reorder(const uint16_t* V, int64_t ldv, int64_t n, const Packed& w,
+                           const int32_t* plan, int always, uint16_t* V2, int64_t ldv2,
+                           hipStream_t st) {
+  reorder_kernel<<<unsigned(n), 256, size_t(w.d) * 2, st>>>(
+      V, ldv, int(w.d), plan, fold_unit(w.group), int(plan_cols(w.d, w.ng, w.group)), always, V2,
+      ldv2);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
@@ -597,22 +753,12 @@ gptq_status launch_expand_transposed(const Packed& w, uint16_t* M, int64_t ldm, 
   return GPTQ_OK;
 }
 
-gptq_status launch_gemm(const GemmArgs& a, bool grouped, hipStream_t st) {
-  // the widest tile that still gives every CU one: wide tiles read less per
-  // product, narrow ones fill the chip where there are few rows
-  auto fills = [&](int tm, int tn) {
-    return int64_t(ceil_div(a.n, tm)) * ceil_div(a.m, tn) >= 256;
-  };
-  if (grouped) {
-    if (fills(256, 128)) return launch_tile<256, 128, 4, 2, 3, true>(a, st);
-    if (a.n > 64 && fills(128, 64)) return launch_tile<128, 64, 4, 1, 3, true>(a, st);
-    if (a.n > 32) return launch_tile<64, 64, 2, 2, 3, true>(a, st);
-    return launch_tile<32, 32, 1, 2, 3, true>(a, st);
+gptq_status launch_gemm(const GemmArgs& a, int fold, hipStream_t st) {
+  switch (fold) {
+    case 64: return launch_fold<2>(a, st);
+    case 32: return launch_fold<1>(a, st);
   }
-  if (fills(256, 128)) return launch_tile<256, 128, 4, 2, 3, false>(a, st);
-  if (a.n > 64 && fills(128, 128)) return launch_tile<128, 128, 2, 2, 3, false>(a, st);
-  if (a.n > 32) return launch_tile<64, 64, 2, 2, 3, false>(a, st);
-  return launch_tile<32, 32, 1, 2, 3, false>(a, st);
+  return launch_fold<0>(a, st);
 }
 
 }  // namespace gptq
