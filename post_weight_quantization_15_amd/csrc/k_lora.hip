@@ -78,8 +78,27 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a, bool vec_v, b
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int64_t s = s0 + wv; s < s1; s += 4) {
+    int64_t s = s0 + wv;
+    if (vec_v && vec_m) {                  // whole steps, loads back to back
+      const int64_t whole = min(s1, a.len / 32);
+      const uint16_t* mr[NF];
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        mr[f] = Ma + int64_t(min(16 * f + c16, a.rank - 1)) * a.ldm + 8 * q;
+#pragma unroll(NF > 2 ? 2 : 4)
+      for (; s < whole; s += 4) {
+        u32x4 fv[2], fm[NF];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fv[i] = *reinterpret_cast<const u32x4*>(vr[i] + 32 * s + 8 * q);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) fm[f] = *reinterpret_cast<const u32x4*>(mr[f] + 32 * s);
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[i][f] = mfma16(fm[f], fv[i], acc[i][f]);
+      }
+    }
+    for (; s < s1; s += 4) {
       u32x4 fv[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) fv[i] = load8(vr[i], 32 * s + 8 * q, a.len, vec_v);
@@ -137,7 +156,7 @@ __global__ __launch_bounds__(256) void shrink_sum_kernel(ShrinkArgs a, int share
 // few, at least 16 steps each.
 int shrink_shares(int64_t n, int64_t len) {
   const int64_t tiles = (n + kShrinkRows - 1) / kShrinkRows;
-  return int(std::max<int64_t>(1, std::min<int64_t>(512 / tiles, (len + 511) / 512)));
+  return tiles >= 128 ? 1 : int(std::max<int64_t>(1, std::min<int64_t>(512 / tiles, (len + 511) / 512)));
 }
 
 gptq_status launch_shrink(const ShrinkArgs& a, hipStream_t st) {
@@ -478,8 +497,6 @@ gptq_status launch_lora(const uint16_t* X, int64_t ldx, int64_t n, const Packed&
     g.ldm = g.ldv2 = plan_cols(w.d, w.ng, w.group);
     g.V2 = b.V2;
     if ((s = launch_plan(w, b.plan, st)) != GPTQ_OK) return s;
-    if ((s = launch_expand_grouped(w, b.plan, b.M, g.ldm, b.scale_t, g.mpad, st)) != GPTQ_OK)
-      return s;
   } else if (lay == kByRow) {
     g.ldm = ldp;
     g.kblocks = g.kwrap;
@@ -499,7 +516,8 @@ gptq_status launch_lora(const uint16_t* X, int64_t ldx, int64_t n, const Packed&
     g.V = direct ? Xc : nullptr;
     g.ldv = ldx;
     if (lay == kByGroups) {
-      if ((s = launch_reorder(Xc, ldx, nc, w, b.plan, !direct, b.V2, g.ldv2, st)) != GPTQ_OK)
+      if ((s = launch_layout(w, b.plan, t0 ? nullptr : b.M, g.ldm, b.scale_t, g.mpad, Xc, ldx, nc,
+                             !direct, b.V2, g.ldv2, st)) != GPTQ_OK)
         return s;
     } else if (!direct) {
       if ((s = launch_pad_rows(Xc, ldx, nc, w.d, b.V2, ldp, st)) != GPTQ_OK) return s;

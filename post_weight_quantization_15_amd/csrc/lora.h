@@ -46,16 +46,15 @@ int fold_unit(int64_t group);
 int64_t plan_cols(int64_t d, int64_t ng, int64_t group);
 size_t plan_words(int64_t d, int64_t ng, int64_t group);
 gptq_status launch_plan(const Packed& w, int32_t* plan, hipStream_t st);
-// M[j][k] = code - zero, exact in bf16, in the plan's column order; scale_t = steps transposed.
-gptq_status launch_expand_grouped(const Packed& w, const int32_t* plan, uint16_t* M, int64_t ldm,
-                                  float* scale_t, int64_t mpad, hipStream_t st);
+// M[j][k] = code - zero, exact in bf16, in the plan's column order; scale_t =
+// steps transposed; V2[t][k] = V[t][order[k]] where the plan is not the natural
+// order (or always).  M NULL: the activations alone.
+gptq_status launch_layout(const Packed& w, const int32_t* plan, uint16_t* M, int64_t ldm,
+                          float* scale_t, int64_t mpad, const uint16_t* V, int64_t ldv, int64_t n,
+                          int always, uint16_t* V2, int64_t ldv2, hipStream_t st);
 // The same for the whole-row grid, in the columns' own order.
 gptq_status launch_expand_row(const Packed& w, uint16_t* M, int64_t ldm, float* scale,
                               hipStream_t st);
-// V2[t][k] = V[t][order[k]] where the plan is not the natural order (or always).
-gptq_status launch_reorder(const uint16_t* V, int64_t ldv, int64_t n, const Packed& w,
-                           const int32_t* plan, int always, uint16_t* V2, int64_t ldv2,
-                           hipStream_t st);
 // M[j][p ldp + c] = part p of three of W_hat[j][c] in bf16 (their sum is exact in fp32).
 gptq_status launch_expand_parts(const Packed& w, uint16_t* M, int64_t ldp, hipStream_t st);
 // M[c][j] = W_hat[j][c] rounded to bf16, columns m .. ldm zero.

@@ -59,8 +59,14 @@ __global__ __launch_bounds__(256) void hidden_kernel(HiddenArgs a, bool vec_x, b
   if (id >= 0 && id < a.n_adapters) {
     const uint16_t* x = a.X + t * a.ldx;
     const uint16_t* w = a.A + (int64_t(id) * a.rank + p) * a.d;
+    int64_t b = 0;
+    if (vec_x && vec_a) {                  // whole 512-column rounds, loads back to back
 #pragma unroll 8
-    for (int64_t c = 8 * lane; c < a.d; c += 512)
+      for (; b + 512 <= a.d; b += 512)
+        s = dot8(*reinterpret_cast<const u32x4*>(x + b + 8 * lane),
+                 *reinterpret_cast<const u32x4*>(w + b + 8 * lane), s);
+    }
+    for (int64_t c = b + 8 * lane; c < a.d; c += 512)
       s = dot8(load8(x, c, a.d, vec_x), load8(w, c, a.d, vec_a), s);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
@@ -192,35 +198,59 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
   const int chunks = static_cast<int>((w.d + 127) / 128);
   const uint32_t* wrow = w.qw + jr * a.words;
 
-  auto load_codes = [&](int ch, uint32_t* v) {
+  // A chunk's codes, activations and group ids.  Chunks are loaded kAhead
+  // ahead of their use; whole ones (of aligned rows) in wide loads without
+  // a condition among them, the last one of the row piece by piece.
+  // Activation rows past n read row n - 1: their sums are not stored.
+  constexpr int kAhead = NT == 1 ? (BITS == 8 ? 3 : 4) : NT == 2 ? 2 : 1;
+  uint32_t codes[kAhead][kW];
+  u32x4 x[kAhead][NT][4];
+  int ga[kAhead], gb[kAhead];              // group ids of columns 2 lane, 2 lane + 1
+  const uint16_t* xr[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) xr[i] = a.X + min<int64_t>(16 * i + c16, a.n - 1) * a.ldx;
+  const int whole = vec_x && vec_w ? static_cast<int>(w.d / 128) : 0;
+  auto load_chunk = [&](int ch, uint32_t* cv, u32x4 (*xv)[4], int& g0, int& g1) {
+    const int64_t k0 = int64_t(ch) * 128;
     const int64_t at = int64_t(ch) * (4 * kW) + q * kW;     // first word of the lane's 32 codes
-    if (vec_w && at + kW <= a.words) {
+    if (ch < whole) {
       if constexpr (BITS == 2) {
         const uint2 u = *reinterpret_cast<const uint2*>(wrow + at);
-        v[0] = u.x;
-        v[1] = u.y;
+        cv[0] = u.x;
+        cv[1] = u.y;
       } else if constexpr (BITS == 3) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) v[i] = wrow[at + i];
+        for (int i = 0; i < 3; ++i) cv[i] = wrow[at + i];
       } else {
 #pragma unroll
         for (int h = 0; h < kW / 4; ++h) {
           const u32x4 u = *reinterpret_cast<const u32x4*>(wrow + at + 4 * h);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[4 * h + i] = u[i];
+          for (int i = 0; i < 4; ++i) cv[4 * h + i] = u[i];
         }
       }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          xv[i][s] = *reinterpret_cast<const u32x4*>(xr[i] + k0 + 32 * s + 8 * q);
+      g0 = w.g_idx[k0 + 2 * lane];
+      g1 = w.g_idx[k0 + 2 * lane + 1];
     } else {
 #pragma unroll
-      for (int i = 0; i < kW; ++i) v[i] = at + i < a.words ? wrow[at + i] : 0u;
+      for (int i = 0; i < kW; ++i) cv[i] = at + i < a.words ? wrow[at + i] : 0u;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) xv[i][s] = load8(xr[i], k0 + 32 * s + 8 * q, w.d, vec_x);
+      g0 = w.g_idx[min<int64_t>(k0 + 2 * lane, w.d - 1)];
+      g1 = w.g_idx[min<int64_t>(k0 + 2 * lane + 1, w.d - 1)];
     }
   };
-  // the first chunks' codes are on their way while the grids are staged
-  constexpr int kAhead = BITS == 8 ? 2 : 4;
-  uint32_t codes[kAhead][kW];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u)
-    if (wv + kDecodeWaves * u < chunks) load_codes(wv + kDecodeWaves * u, codes[u]);
+    if (wv + kDecodeWaves * u < chunks)
+      load_chunk(wv + kDecodeWaves * u, codes[u], x[u], ga[u], gb[u]);
 
   constexpr bool kMagic = BITS != 8;
   for (int e = tid; e < ng * kDecodeRows; e += kDecodeWaves * 64) {
@@ -236,38 +266,15 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const u32x4 ones = u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  const uint16_t* xr[NT];
-  bool on[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    on[i] = 16 * i + c16 < a.n;
-    xr[i] = a.X + (on[i] ? 16 * i + c16 : 0) * a.ldx;
-  }
-
   for (int cb = wv; cb < chunks; cb += kDecodeWaves * kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int ch = cb + kDecodeWaves * u;
       if (ch >= chunks) break;
       const int64_t k0 = int64_t(ch) * 128;
-      u32x4 x[NT][4];
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          x[i][s] = u32x4{0u, 0u, 0u, 0u};
-          if (on[i]) x[i][s] = load8(xr[i], k0 + 32 * s + 8 * q, w.d, vec_x);
-        }
-      // group ids of columns 2 lane, 2 lane + 1 of the chunk
-      const int64_t gc = k0 + 2 * lane;
-      const int ga = w.g_idx[min<int64_t>(gc, w.d - 1)], gb = w.g_idx[min<int64_t>(gc + 1, w.d - 1)];
       Run<BITS> run[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) run[s] = run_of<BITS>(codes[u], s);
-      {
-        const int nx = ch + kDecodeWaves * kAhead;
-        if (nx < chunks) load_codes(nx, codes[u]);
-      }
 #pragma unroll
       for (int h = 0; h < (BITS == 8 ? 2 : 1); ++h)
         turn4(run[0].w[h], run[1].w[h], run[2].w[h], run[3].w[h]);
@@ -280,8 +287,8 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         if (k0 + 32 * s >= w.d) break;
-        const int G = __builtin_amdgcn_readlane(ga, 16 * s);
-        const uint64_t diff = __ballot(ga != G || gb != G);
+        const int G = __builtin_amdgcn_readlane(ga[u], 16 * s);
+        const uint64_t diff = __ballot(ga[u] != G || gb[u] != G);
         if (!((diff >> (16 * s)) & 0xFFFFu)) {
           const u32x4 m = run_operand<BITS>(run[s]);
           const int gi = min(max(G, 0), ng - 1);
@@ -290,7 +297,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             const f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
-            const f32x4 P = mfma16(x[i][s], m, z), Xs = mfma16(x[i][s], ones, z);
+            const f32x4 P = mfma16(x[u][i][s], m, z), Xs = mfma16(x[u][i][s], ones, z);
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(dl, fmaf(-zz, Xs[v], P[v]), acc[i][v]);
           }
@@ -299,7 +306,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int src = 16 * s + 4 * q + (i >> 1);
-            const int g = min(max(__shfl(i & 1 ? gb : ga, src), 0), ng - 1);
+            const int g = min(max(__shfl(i & 1 ? gb[u] : ga[u], src), 0), ng - 1);
             const float dl = grid[(g * kDecodeRows + c16) * 2];
             const float zz = grid[(g * kDecodeRows + c16) * 2 + 1];
             uint16_t p[3];
@@ -310,9 +317,11 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int h = 0; h < 3; ++h) acc[i] = mfma16(x[i][s], part[h], acc[i]);
+            for (int h = 0; h < 3; ++h) acc[i] = mfma16(x[u][i][s], part[h], acc[i]);
         }
       }
+      const int next = ch + kDecodeWaves * kAhead;
+      if (next < chunks) load_chunk(next, codes[u], x[u], ga[u], gb[u]);
     }
   }
   // ---- the waves' shares, in their order, and the adapter's part

@@ -46,10 +46,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
   if (tid == 0) ident = d % block == 0;
   __syncthreads();
   bool inc = true;
+#pragma unroll 4
   for (int c = tid; c < d; c += kPlanThreads) {
     const int g = min(max(g_idx[c], 0), ng - 1);
+    const int before = g_idx[max(c - 1, 0)];
     atomicAdd(&cnt[g], 1);
-    if (c > 0 && g < g_idx[c - 1]) inc = false;
+    if (g < before) inc = false;
   }
   if (!inc) ident = 0;
   __syncthreads();
@@ -91,12 +93,20 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
       continue;
     }
     int at = s;
-    for (int c0 = 0; c0 < d && at < s + n; c0 += 64) {
-      const int c = c0 + lane;
-      const bool mine = c < d && min(max(g_idx[c], 0), ng - 1) == g;
-      const uint64_t b = __ballot(mine);
-      if (mine) order[at + __popcll(b & ((uint64_t(1) << lane) - 1))] = c;
-      at += __popcll(b);
+    for (int c0 = 0; c0 < d && at < s + n; c0 += 512) {     // eight loads at a time
+      int v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + 64 * i + lane;
+        v[i] = c < d ? min(max(g_idx[c], 0), ng - 1) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool mine = v[i] == g;
+        const uint64_t b = __ballot(mine);
+        if (mine) order[at + __popcll(b & ((uint64_t(1) << lane) - 1))] = c0 + 64 * i + lane;
+        at += __popcll(b);
+      }
     }
     for (int k = s + n + lane; k < e; k += 64) order[k] = -1;
   }
@@ -135,52 +145,107 @@ __device__ inline int signed_code(int c, int bits) {
   return (c ^ hb) - hb;
 }
 
-// Thread: 8 places of one row of M.  Blocks past the expansion transpose the steps.
-template <int BITS>
-__global__ __launch_bounds__(256) void expand_grouped_kernel(Packed w, int64_t words,
-                                                             const int32_t* __restrict__ plan,
-                                                             int unit, int cols_max,
-                                                             uint16_t* __restrict__ M,
-                                                             int64_t ldm,
-                                                             float* __restrict__ scale_t,
-                                                             int64_t mpad, unsigned blocks) {
-  if (blockIdx.x >= blocks) {
-    const int64_t e = int64_t(blockIdx.x - blocks) * 256 + threadIdx.x;
-    const int64_t j = e / w.ng, g = e % w.ng;
-    if (j < w.m) scale_t[g * mpad + j] = step_at(w, j * w.ng + g);
+// One launch lays out everything the plan orders: the first blocks R rows of M
+// each (out of natural order through the rows' words in LDS), then the steps
+// transposed, then the activations (a block a row at a time, through LDS; nothing to
+// do where they are used as they lie).
+struct LayoutArgs {
+  Packed w;
+  int64_t words;
+  const int32_t* plan;
+  int unit, cols_max;
+  uint16_t* M;
+  int64_t ldm;
+  float* scale_t;
+  int64_t mpad;
+  const uint16_t* V;
+  int64_t ldv, n;
+  int always;
+  uint16_t* V2;
+  int64_t ldv2;
+  unsigned blocks_m, blocks_s, blocks_v;
+};
+
+template <int BITS, int R>
+__global__ __launch_bounds__(256) void layout_kernel(LayoutArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint32_t lay_lds[];
+  const Packed& w = a.w;
+  const int tid = threadIdx.x;
+  const int32_t* grp = a.plan + kPlanHeader;
+  const int32_t* order = grp + a.cols_max / a.unit;
+  const bool ident = a.plan[0];
+  const int units = a.plan[1] * 8;
+  if (blockIdx.x < a.blocks_m) {
+    const int64_t j0 = int64_t(blockIdx.x) * R;
+    if (!ident) {
+      for (int r = 0; r < R; ++r) {
+        const uint32_t* src = w.qw + min<int64_t>(j0 + r, w.m - 1) * a.words;
+        for (int i = tid; i < a.words; i += 256) lay_lds[r * a.words + i] = src[i];
+      }
+      __syncthreads();
+    }
+    for (int u = tid; u < units; u += 256) {
+      const int g = grp[8 * u / a.unit];
+      int at[8];
+      if (!ident) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) at[i] = order[8 * u + i];
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int64_t j = j0 + r;
+        if (j >= w.m) break;
+        u32x4 out = u32x4{0u, 0u, 0u, 0u};
+        if (g >= 0) {
+          const int z = w.sgn ? 0 : w.zeros[j * w.ng + g];
+          int c[8];
+          if (ident) {
+            codes8<BITS>(w.qw + j * a.words, a.words, u, c);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int p = max(at[i], 0) * BITS;
+              const uint32_t* word = lay_lds + r * a.words + (p >> 5);
+              uint32_t v = word[0] >> (p & 31);
+              if (BITS == 3 && (p & 31) > 29) v |= word[1] << (32 - (p & 31));
+              c[i] = static_cast<int>(v & ((1u << BITS) - 1u));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int v = (w.sgn ? signed_code(c[i], BITS) : c[i]) - z;
+            const uint32_t h = __float_as_uint(static_cast<float>(v)) >> 16;
+            out[i >> 1] |= (ident || at[i] >= 0 ? h : 0u) << (16 * (i & 1));
+          }
+        }
+        *reinterpret_cast<u32x4*>(a.M + j * a.ldm + 8 * u) = out;
+      }
+    }
     return;
   }
-  const int units = plan[1] * 8;
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int per = cols_max / 8;
-  const int64_t j = e / per;
-  const int u = static_cast<int>(e % per);
-  if (u >= units || j >= w.m) return;
-  const int32_t* grp = plan + kPlanHeader;
-  const int32_t* order = grp + cols_max / unit;
-  const int g = grp[8 * u / unit];
-  u32x4 out = u32x4{0u, 0u, 0u, 0u};
-  if (g >= 0) {
-    const int z = w.sgn ? 0 : w.zeros[j * w.ng + g];
-    if (plan[0]) {
-      int c[8];
-      codes8<BITS>(w.qw + j * words, words, u, c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int v = (w.sgn ? signed_code(c[i], BITS) : c[i]) - z;
-        out[i >> 1] |= (__float_as_uint(static_cast<float>(v)) >> 16) << (16 * (i & 1));
-      }
-    } else {
+  if (blockIdx.x < a.blocks_m + a.blocks_s) {
+    const int64_t e = int64_t(blockIdx.x - a.blocks_m) * 256 + tid;
+    const int64_t j = e / w.ng, g = e % w.ng;
+    if (j < w.m) a.scale_t[g * a.mpad + j] = step_at(w, j * w.ng + g);
+    return;
+  }
+  if (ident && !a.always) return;
+  uint16_t* rowbuf = reinterpret_cast<uint16_t*>(lay_lds);
+  for (int64_t t = blockIdx.x - a.blocks_m - a.blocks_s; t < a.n; t += a.blocks_v) {
+    const uint16_t* src = a.V + t * a.ldv;
+    __syncthreads();
+    for (int c = tid; c < w.d; c += 256) rowbuf[c] = src[c];
+    __syncthreads();
+    for (int u = tid; u < units; u += 256) {
+      u32x4 v = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c = order[8 * u + i];
-        if (c < 0) continue;
-        const int v = code_at(w, words, j, c) - z;
-        out[i >> 1] |= (__float_as_uint(static_cast<float>(v)) >> 16) << (16 * (i & 1));
+        v[i >> 1] |= (c >= 0 ? uint32_t(rowbuf[c]) : 0u) << (16 * (i & 1));
       }
+      *reinterpret_cast<u32x4*>(a.V2 + t * a.ldv2 + 8 * u) = v;
     }
   }
-  *reinterpret_cast<u32x4*>(M + j * ldm + 8 * u) = out;
 }
 
 // The whole-row grid: the columns stay as they are.
@@ -207,30 +272,6 @@ __global__ __launch_bounds__(256) void expand_row_kernel(Packed w, int64_t words
     out[i >> 1] |= (__float_as_uint(static_cast<float>(v)) >> 16) << (16 * (i & 1));
   }
   *reinterpret_cast<u32x4*>(M + j * ldm + 8 * u) = out;
-}
-
-// One row per workgroup, through LDS (a row's gather is within itself).
-__global__ __launch_bounds__(256) void reorder_kernel(const uint16_t* __restrict__ V, int64_t ldv,
-                                                      int d, const int32_t* __restrict__ plan,
-                                                      int unit, int cols_max, int always,
-                                                      uint16_t* __restrict__ V2, int64_t ldv2) {
-  extern __shared__ uint16_t rowbuf[];
-  if (plan[0] && !always) return;
-  const int64_t t = blockIdx.x;
-  const int32_t* order = plan + kPlanHeader + cols_max / unit;
-  const uint16_t* src = V + t * ldv;
-  for (int c = threadIdx.x; c < d; c += 256) rowbuf[c] = src[c];
-  __syncthreads();
-  const int units = plan[1] * 8;
-  for (int u = threadIdx.x; u < units; u += 256) {
-    u32x4 v = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = order[8 * u + i];
-      if (c >= 0) v[i >> 1] |= uint32_t(rowbuf[c]) << (16 * (i & 1));
-    }
-    *reinterpret_cast<u32x4*>(V2 + t * ldv2 + 8 * u) = v;
-  }
 }
 
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ V, int64_t ldv,
@@ -265,54 +306,71 @@ __global__ __launch_bounds__(256) void expand_parts_kernel(Packed w, int64_t wor
     *reinterpret_cast<u32x4*>(M + j * 3 * ldp + q * ldp + 8 * u) = out[q];
 }
 
-// 64 weight rows x 64 columns per workgroup: thread t takes row t / 4 and two
-// 8-column runs, the tile turns in LDS (a row of 64 bf16 and 8 of padding, so
-// that the eight rows a run writes to lie in different banks), and leaves
-// as 128 contiguous bytes of a column.
+// 64 weight rows x 128 columns per workgroup.  A thread takes the same 8-column
+// run of two neighbouring rows, so that it writes pairs (two bf16 of one
+// column) to the turned tile in LDS: 32 lanes write 32 consecutive words, and
+// a column's stride of 144 bytes puts the wave's two runs in different halves
+// of the banks.  The tile leaves as 128 contiguous bytes of a column.
 template <int BITS>
 __global__ __launch_bounds__(256) void expand_transposed_kernel(Packed w, int64_t words,
                                                                 uint16_t* __restrict__ M,
                                                                 int64_t ldm) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
+  constexpr int kCols = 128;
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kCols][36];
   const int tid = threadIdx.x;
-  const int64_t c0 = int64_t(blockIdx.x) * 64, j0 = int64_t(blockIdx.y) * 64;
-  const int jl = tid >> 2;
-  const int64_t j = j0 + jl;
+  const int64_t c0 = int64_t(blockIdx.x) * kCols, j0 = int64_t(blockIdx.y) * 64;
+  const int pair = tid & 31;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int run = 2 * (tid & 3) + e;
-    int c[8];
-    float v[8];
-    if (j < w.m) {
-      codes8<BITS>(w.qw + j * words, words, c0 / 8 + run, c);
-      int gp = -1;
-      float s = 0.0f;
-      int z = 0;
+  for (int e = 0; e < kCols / 64; ++e) {
+    const int run = (tid >> 5) + 8 * e;
+    if (c0 + 8 * run >= w.d) break;
+    int g[8];
+    bool one = true;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t col = min<int64_t>(c0 + 8 * run + i, w.d - 1);
-        const int g = w.g_idx[col];
-        if (g != gp) {
-          s = step_at(w, j * w.ng + g);
-          z = w.sgn ? 0 : w.zeros[j * w.ng + g];
-          gp = g;
-        }
-        v[i] = s * static_cast<float>((w.sgn ? signed_code(c[i], BITS) : c[i]) - z);
-      }
-    } else {
+    for (int i = 0; i < 8; ++i) {
+      g[i] = w.g_idx[min<int64_t>(c0 + 8 * run + i, w.d - 1)];
+      one = one && g[i] == g[0];
+    }
+    uint32_t out[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t j = j0 + 2 * pair + h;
+      float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      if (j < w.m) {
+        int c[8];
+        codes8<BITS>(w.qw + j * words, words, c0 / 8 + run, c);
+        if (one) {
+          const float s = step_at(w, j * w.ng + g[0]);
+          const int z = w.sgn ? 0 : w.zeros[j * w.ng + g[0]];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = s * static_cast<float>((w.sgn ? signed_code(c[i], BITS) : c[i]) - z);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = step_at(w, j * w.ng + g[i]) *
+                   static_cast<float>((w.sgn ? signed_code(c[i], BITS) : c[i]) -
+                                      (w.sgn ? 0 : w.zeros[j * w.ng + g[i]]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (h == 0) out[i] = f32_bf16(v[i]);
+        else out[i] |= uint32_t(f32_bf16(v[i])) << 16;
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tile[8 * run + i][jl] = f32_bf16(v[i]);
+    for (int i = 0; i < 8; ++i) tile[8 * run + i][pair] = out[i];
   }
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int cl = tid >> 2, u = 2 * (tid & 3) + e;
+  for (int e = 0; e < kCols * 8 / 256; ++e) {
+    const int cl = (tid >> 3) + 32 * e, u = tid & 7;
     if (c0 + cl < w.d && j0 + 8 * u < ldm)
       *reinterpret_cast<u32x4*>(M + (c0 + cl) * ldm + j0 + 8 * u) =
-          *reinterpret_cast<const u32x4*>(&tile[cl][8 * u]);
+          *reinterpret_cast<const u32x4*>(&tile[cl][4 * u]);
   }
 }
 
@@ -349,15 +407,18 @@ __device__ inline void add_sum(f32x4& P, const u32x4& a, const u32x4& b) {
   else P = mfma16(a, b, P);
 }
 
+// KS shares of k, each with its own waves and ring, take the blocks of a tile
+// side by side where tiles are few and small: a block's time is then latency
+// (barrier, LDS read, a short chain of products), not work.
 // FOLD = 0: one sum per output (times a row's step at the end where scale_t
 // is given); FOLD = 1, 2: every FOLD 32-steps are one group's, whose step
 // folds in.  The fold of a finished group runs fragment by fragment between
 // the matrix instructions that open the next one over its registers, so its
 // vector work hides behind them.
-template <int TM, int TN, int WM, int WN, int S, int FOLD>
-__global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned tiles_j,
+template <int TM, int TN, int WM, int WN, int KS, int S, int FOLD, bool LORA>
+__global__ __launch_bounds__(WM* WN* KS * 64) void gemm_kernel(GemmArgs a, unsigned tiles_j,
                                                            unsigned tiles, int vec_y, int vec_l) {
-  constexpr int kWaves = WM * WN;
+  constexpr int kWaves = WM * WN;            // of one share of k
   constexpr int kFi = TM / WM / 16;          // activation fragments of a wave
   constexpr int kFj = TN / WN / 16;          // fragments of M
   constexpr int kRows = TM + TN;
@@ -370,16 +431,25 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
   static_assert((TN / WN) <= 64, "a wave's steps fit its slot");
   // S stages, then S + 1 blocks' steps: those of the block before the one in
   // work are still there when its group folds
-  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int kRing = S * kStage + (FOLD ? (S + 1) * kScale : 0);
+  extern __shared__ __attribute__((aligned(16))) char lds_all[];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = __builtin_amdgcn_readfirstlane((tid >> 6) / kWaves);   // the wave's share of k
+  const int wv = __builtin_amdgcn_readfirstlane((tid >> 6) % kWaves);
+  char* lds = lds_all + kg * kRing;
   const int q = lane >> 4, c16 = lane & 15;
-  // each XCD (blocks b, b + 8, ...) walks a contiguous range of tiles
+  // Each XCD (blocks b, b + 8, ...) walks a contiguous range of tiles, in bands
+  // of kBand activation tiles: the tiles it runs at once then form a block of
+  // them, and its L2 takes in the fewest rows per step.
+  constexpr unsigned kBand = 4;
   unsigned tile = blockIdx.x;
   const unsigned per = tiles / 8;
   if (tile < 8 * per) tile = (tile % 8) * per + tile / 8;
-  const int64_t jb = int64_t(tile % tiles_j) * TN;      // first row of M
-  const int64_t tb = int64_t(tile / tiles_j) * TM;      // first activation row
+  const unsigned tiles_t = tiles / tiles_j, band = tile / (kBand * tiles_j);
+  const unsigned high = min(kBand, tiles_t - band * kBand), rest = tile - band * kBand * tiles_j;
+  // first row of M, first activation row (divided on the vector unit: made uniform)
+  const int64_t jb = int64_t(__builtin_amdgcn_readfirstlane(rest / high)) * TN;
+  const int64_t tb = int64_t(__builtin_amdgcn_readfirstlane(band * kBand + rest % high)) * TM;
   const int wi = (wv % WM) * (TM / WM), wj = (wv / WM) * (TN / WN);
 
   int kblocks = a.kblocks;
@@ -392,6 +462,9 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
       ldv = a.ldv2;
     }
   }
+  // this share's blocks; all shares turn as often as the longest
+  const int kb0 = kblocks * kg / KS, kb1 = kblocks * (kg + 1) / KS;
+  const int turns = (kblocks + KS - 1) / KS;
   // the units' groups, through the scalar cache (uniform, and no vector load
   // whose wait would drain the copies in flight)
   const auto grp = (const int32_t __attribute__((address_space(4)))*)(a.plan + kPlanHeader);
@@ -410,7 +483,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
   }
   // groups of a block (past the end: the last one's)
   auto groups_of = [&](int kb, int& ga, int& gb) {
-    const int k = min(kb, kblocks - 1);
+    const int k = max(min(kb0 + kb, kb1 - 1), 0);
     ga = gb = 0;
     if (FOLD == 1) {
       ga = max(grp[2 * k], 0);
@@ -423,8 +496,9 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
   // into a stage nobody reads any more, so that every block counts alike)
   auto fetch = [&](int kb, int ga, int gb) {
     const int st = kb % S;
-    const int k = min(kb, kblocks - 1);
-    const int kv = FOLD ? k : k % a.kwrap;
+    const int k = __builtin_amdgcn_readfirstlane(max(min(kb0 + kb, kb1 - 1), 0));
+    // V repeats for each of up to three parts of M
+    const int kv = FOLD ? k : k - (k >= 2 * a.kwrap ? 2 * a.kwrap : k >= a.kwrap ? a.kwrap : 0);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const bool act = 8 * (kLoads * wv + i) < TM;
@@ -479,7 +553,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
   }
   int na, nb;                                // groups of the next block to fetch
   groups_of(S - 1, na, nb);
-  for (int kb = 0; kb < kblocks; ++kb) {
+  for (int kb = 0; kb < turns; ++kb) {
     wait_vmcnt<(S - 2) * kOut>();
     // LDS reads of the stage that is filled next are done as well
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -490,6 +564,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
     const char* sc = lds + S * kStage + wv * 512 + 16 * q;
     const char* sc0 = sc + ((kb + S) % (S + 1)) * kScale;
     const char* sc1 = sc + (kb % (S + 1)) * kScale;
+    if (KS > 1 && kb >= kb1 - kb0) continue;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       // sums opened by this block's first step are read in its second: all
@@ -527,15 +602,18 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
 #pragma unroll
           for (int i = 0; i < kFi; ++i) {
             if (FOLD) add_sum<kInPlace>(P[FOLD ? i : 0][FOLD ? j : 0], fm[j], fa[i]);
-            else acc[i][j] = mfma16(fm[j], fa[i], acc[i][j]);
+            else add_sum<kInPlace>(acc[i][j], fm[j], fa[i]);
           }
       }
     }
   }
   wait_vmcnt<0>();
+  if (kInPlace) {
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
   if (FOLD) {
-    if (kInPlace) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-    const char* sc = lds + S * kStage + ((kblocks - 1) % (S + 1)) * kScale + wv * 512 + 16 * q;
+    const char* sc = lds + S * kStage + ((kb1 - kb0 + S) % (S + 1)) * kScale + wv * 512 + 16 * q;
 #pragma unroll
     for (int j = 0; j < kFj; ++j) {
       const f32x4 d = *reinterpret_cast<const f32x4*>(sc + (FOLD == 1 ? 256 : 0) + 64 * j);
@@ -555,9 +633,35 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
     }
   }
 
+  // ---- the shares of k, added in their order
+  if constexpr (KS > 1) {
+    __syncthreads();
+    f32x4* sums = reinterpret_cast<f32x4*>(lds_all) + wv * kFi * kFj * 64 + lane;
+    constexpr int kAll = kWaves * kFi * kFj * 64;
+    static_assert((KS - 1) * kAll * 16 <= KS * kRing, "the shares' sums fit the rings");
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < kFi; ++i)
+#pragma unroll
+        for (int j = 0; j < kFj; ++j) sums[(kg - 1) * kAll + (i * kFj + j) * 64] = acc[i][j];
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 0; g < KS - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < kFi; ++i)
+#pragma unroll
+        for (int j = 0; j < kFj; ++j) {
+          const f32x4 o = sums[g * kAll + (i * kFj + j) * 64];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] += o[v];
+        }
+  }
+
   // ---- the adapters' part: per adapter among the wave's rows one small
   //      product, added to the rows of that adapter alone
-  if (a.L) {
+  if (LORA) {
 #pragma unroll
     for (int i = 0; i < kFi; ++i) {
       const int64_t t = tb + wi + 16 * i + c16;
@@ -596,6 +700,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
 #pragma unroll
   for (int i = 0; i < kFi; ++i) {
     const int64_t t = tb + wi + 16 * i + c16;
+    asm volatile("" ::: "memory");           // one row of fragments' addresses at a time
     if (t >= a.n) continue;
 #pragma unroll
     for (int j = 0; j < kFj; ++j) {
@@ -626,31 +731,43 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_kernel(GemmArgs a, unsigned 
   }
 }
 
-template <int TM, int TN, int WM, int WN, int S, int FOLD>
+template <int TM, int TN, int WM, int WN, int KS, int S, int FOLD, bool LORA>
 gptq_status launch_tile(const GemmArgs& a, hipStream_t st) {
-  constexpr int lds = S * (TM + TN) * kBk * 2 + (FOLD ? (S + 1) * WM * WN * 512 : 0);
+  constexpr int lds =
+      KS * (S * (TM + TN) * kBk * 2 + (FOLD ? (S + 1) * WM * WN * 512 : 0));
   static_assert(lds <= 160 * 1024, "the ring fits the LDS");
   const unsigned tj = ceil_div(a.m, TN);
   const unsigned tiles = tj * ceil_div(a.n, TM);
   const int item = a.out_bf16 ? 2 : 4;
   const int vec_y = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.Y) % (4 * item) == 0;
   const int vec_l = a.L && a.rank % 8 == 0 && reinterpret_cast<uintptr_t>(a.L) % 16 == 0;
-  gemm_kernel<TM, TN, WM, WN, S, FOLD><<<tiles, WM * WN * 64, lds, st>>>(a, tj, tiles, vec_y, vec_l);
+  gemm_kernel<TM, TN, WM, WN, KS, S, FOLD, LORA><<<tiles, WM * WN * KS * 64, lds, st>>>(a, tj, tiles, vec_y, vec_l);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
 
-// The widest tile that still gives every CU one: wide tiles read less per
-// product, narrow ones fill the chip where there are few rows.
-template <int FOLD>
+// Tiles by the time they take on 256 CUs: rounds of workgroups times a tile's
+// area over the rate measured for its shape (relative; wide tiles read less
+// per product).  Narrow tiles run several workgroups a CU.
+template <int FOLD, bool LORA>
 gptq_status launch_fold(const GemmArgs& a, hipStream_t st) {
-  auto fills = [&](int tm, int tn) {
-    return int64_t(ceil_div(a.n, tm)) * ceil_div(a.m, tn) >= 200;
+  auto cost = [&](int tm, int tn, int per_cu, double rate) {
+    const int64_t tiles = int64_t(ceil_div(a.n, tm)) * ceil_div(a.m, tn);
+    const int64_t rounds = (tiles + 256 * per_cu - 1) / (256 * per_cu);
+    // a last round that leaves CUs with fewer workgroups than others is as long
+    const int64_t left = tiles - (rounds - 1) * 256 * per_cu;
+    const int64_t last = (left + 255) / 256;
+    return double((rounds - 1) * per_cu + last) * tm * tn / rate;
   };
-  if (fills(256, 128)) return launch_tile<256, 128, 4, 2, 3, FOLD>(a, st);
-  if (a.n > 64 && fills(128, 128)) return launch_tile<128, 128, 2, 2, 3, FOLD>(a, st);
-  if (a.n > 32) return launch_tile<64, 64, 2, 2, 3, FOLD>(a, st);
-  return launch_tile<32, 32, 1, 2, 3, FOLD>(a, st);
+  const double c256 = FOLD == 0 ? cost(256, 256, 1, 1.05) : 1e30, cw = cost(256, 128, 1, 1.0);
+  const double c128 = cost(128, 128, 1, 0.75), c64 = cost(64, 64, 3, 0.40), c32 = cost(32, 32, 6, 0.18);
+  const double best = std::min(std::min(std::min(c256, cw), std::min(c128, c64)), c32);
+  if constexpr (FOLD == 0)
+    if (best == c256) return launch_tile<256, 256, 2, 4, 1, 2, 0, LORA>(a, st);
+  if (best == cw) return launch_tile<256, 128, 4, 2, 1, 3, FOLD, LORA>(a, st);
+  if (best == c128) return launch_tile<128, 128, 2, 2, 2, 2, FOLD, LORA>(a, st);
+  if (best == c64) return launch_tile<64, 64, 2, 2, 4, 2, FOLD, LORA>(a, st);
+  return launch_tile<32, 32, 1, 2, 8, 2, FOLD, LORA>(a, st);
 }
 
 }  // namespace
@@ -677,22 +794,33 @@ gptq_status launch_plan(const Packed& w, int32_t* plan, hipStream_t st) {
   return GPTQ_OK;
 }
 
-gptq_status launch_expand_grouped(const Packed& w, const int32_t* plan, uint16_t* M, int64_t ldm,
-                                  float* scale_t, int64_t mpad, hipStream_t st) {
-  const int64_t words = (w.d * w.bits + 31) / 32;
-  const int cols = int(plan_cols(w.d, w.ng, w.group)), unit = fold_unit(w.group);
-  const unsigned blocks = ceil_div(w.m * (cols / 8), 256);
-  const unsigned grid = blocks + ceil_div(w.m * w.ng, 256);
-#define GPTQ_EX(B)                                                                            \
-  expand_grouped_kernel<B><<<grid, 256, 0, st>>>(w, words, plan, unit, cols, M, ldm, scale_t, mpad, \
-                                                 blocks)
-  switch (w.bits) {
-    case 2: GPTQ_EX(2); break;
-    case 3: GPTQ_EX(3); break;
-    case 4: GPTQ_EX(4); break;
-    default: GPTQ_EX(8); break;
+gptq_status launch_layout(const Packed& w, const int32_t* plan, uint16_t* M, int64_t ldm,
+                          float* scale_t, int64_t mpad, const uint16_t* V, int64_t ldv, int64_t n,
+                          int always, uint16_t* V2, int64_t ldv2, hipStream_t st) {
+  LayoutArgs a{w, (w.d * w.bits + 31) / 32, plan, fold_unit(w.group),
+               int(plan_cols(w.d, w.ng, w.group)), M, ldm, scale_t, mpad, V, ldv, n, always, V2,
+               ldv2, 0, 0, 0};
+  // four rows share the loads of the order where their words fit in LDS
+  const int rows = a.words * 16 <= 64 * 1024 ? 4 : 1;
+  if (M) {
+    a.blocks_m = ceil_div(w.m, rows);
+    a.blocks_s = ceil_div(w.m * w.ng, 256);
   }
-#undef GPTQ_EX
+  a.blocks_v = unsigned(std::min<int64_t>(n, 2048));
+  const size_t lds = std::max<size_t>(M ? size_t(a.words) * 4 * rows : 0, size_t(w.d) * 2);
+  const unsigned grid = a.blocks_m + a.blocks_s + a.blocks_v;
+#define GPTQ_LAY(B)                                                     \
+  do {                                                                  \
+    if (rows == 4) layout_kernel<B, 4><<<grid, 256, lds, st>>>(a);      \
+    else layout_kernel<B, 1><<<grid, 256, lds, st>>>(a);                \
+  } while (0)
+  switch (w.bits) {
+    case 2: GPTQ_LAY(2); break;
+    case 3: GPTQ_LAY(3); break;
+    case 4: GPTQ_LAY(4); break;
+    default: GPTQ_LAY(8); break;
+  }
+#undef GPTQ_LAY
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
@@ -715,16 +843,6 @@ gptq_status launch_expand_row(const Packed& w, uint16_t* M, int64_t ldm, float* 
   return GPTQ_OK;
 }
 
-gptq_status launch_reorder(const uint16_t* V, int64_t ldv, int64_t n, const Packed& w,
-                           const int32_t* plan, int always, uint16_t* V2, int64_t ldv2,
-                           hipStream_t st) {
-  reorder_kernel<<<unsigned(n), 256, size_t(w.d) * 2, st>>>(
-      V, ldv, int(w.d), plan, fold_unit(w.group), int(plan_cols(w.d, w.ng, w.group)), always, V2,
-      ldv2);
-  GPTQ_CHECK_LAUNCH();
-  return GPTQ_OK;
-}
-
 gptq_status launch_pad_rows(const uint16_t* V, int64_t ldv, int64_t n, int64_t len, uint16_t* V2,
                             int64_t cols, hipStream_t st) {
   const bool vec = ldv % 8 == 0 && reinterpret_cast<uintptr_t>(V) % 16 == 0;
@@ -742,7 +860,7 @@ gptq_status launch_expand_parts(const Packed& w, uint16_t* M, int64_t ldp, hipSt
 
 gptq_status launch_expand_transposed(const Packed& w, uint16_t* M, int64_t ldm, hipStream_t st) {
   const int64_t words = (w.d * w.bits + 31) / 32;
-  const dim3 grid(ceil_div(w.d, 64), ceil_div(ldm, 64));
+  const dim3 grid(ceil_div(w.d, 128), ceil_div(ldm, 64));
   switch (w.bits) {
     case 2: expand_transposed_kernel<2><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
     case 3: expand_transposed_kernel<3><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
@@ -755,10 +873,10 @@ gptq_status launch_expand_transposed(const Packed& w, uint16_t* M, int64_t ldm, 
 
 gptq_status launch_gemm(const GemmArgs& a, int fold, hipStream_t st) {
   switch (fold) {
-    case 64: return launch_fold<2>(a, st);
-    case 32: return launch_fold<1>(a, st);
+    case 64: return launch_fold<2, true>(a, st);
+    case 32: return launch_fold<1, true>(a, st);
   }
-  return launch_fold<0>(a, st);
+  return a.L ? launch_fold<0, true>(a, st) : launch_fold<0, false>(a, st);
 }
 
 }  // namespace gptq
