@@ -138,6 +138,25 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a, bool vec_v, b
     }
 }
 
+// Few values: one wave per value, fp32 sums of exact products in pairs.  Where a
+// tile's rows have an adapter each, the tiles above would run once per row.
+__global__ __launch_bounds__(256) void values_kernel(ShrinkArgs a, bool vec) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = blockIdx.y;
+  const int p = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int id = a.row[t];
+  const bool on = id >= 0 && id < a.n_adapters;
+  float s = 0.0f;
+  if (on && p < a.rank) {
+    const uint16_t* v = a.V + t * a.ldv;
+    const uint16_t* m = a.M + (int64_t(id) * a.rank + p) * a.ldm;
+    s = dot_wave(v, m, a.len, vec, lane);
+  }
+  if (lane != 0) return;
+  if (on) put_hidden(a, t, p, s, a.alpha[id]);
+  else if (a.H && p < a.rank) a.H[t * a.rank + p] = 0.0f;
+}
+
 // The shares of grid.y, added in their order.
 __global__ __launch_bounds__(256) void shrink_sum_kernel(ShrinkArgs a, int shares) {
   const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -162,6 +181,12 @@ int shrink_shares(int64_t n, int64_t len) {
 gptq_status launch_shrink(const ShrinkArgs& a, hipStream_t st) {
   const bool vv = a.ldv % 8 == 0 && reinterpret_cast<uintptr_t>(a.V) % 16 == 0;
   const bool vm = a.ldm % 8 == 0 && reinterpret_cast<uintptr_t>(a.M) % 16 == 0;
+  // up to 64 MB of V and M rows in all, mostly from L2
+  if (a.n <= 65535 && a.n * a.rank * a.len <= (int64_t(32) << 20)) {
+    values_kernel<<<dim3(a.rp / 4, unsigned(a.n)), 256, 0, st>>>(a, vv && vm);
+    GPTQ_CHECK_LAUNCH();
+    return GPTQ_OK;
+  }
   const int shares = shrink_shares(a.n, a.len);
   const dim3 grid(ceil_div(a.n, kShrinkRows), shares);
   if (a.rank <= 16) shrink_kernel<1><<<grid, 256, 0, st>>>(a, vv, vm);
@@ -174,32 +199,6 @@ gptq_status launch_shrink(const ShrinkArgs& a, hipStream_t st) {
     GPTQ_CHECK_LAUNCH();
   }
   return GPTQ_OK;
-}
-
-// parts[t] = the three parts of alpha_a H[t] (dB); rows without an adapter are never read.
-__global__ __launch_bounds__(256) void split_kernel(ShrinkArgs a, const float* __restrict__ H) {
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t t = e / a.rp;
-  const int p = static_cast<int>(e % a.rp);
-  if (t >= a.n) return;
-  const int id = a.row[t];
-  if (id < 0 || id >= a.n_adapters) return;
-  put_hidden(a, t, p, p < a.rank ? H[t * a.rank + p] : 0.0f, a.alpha[id]);
-}
-
-// out[b][x][y] = in[b][y][x], 64 x 64 tiles; rows of `out` at stride ldo, zeros past `ny`.
-__global__ __launch_bounds__(256) void turn_kernel(const uint16_t* __restrict__ in, int64_t ny,
-                                                   int64_t nx, uint16_t* __restrict__ out,
-                                                   int64_t ldo) {
-  __shared__ uint16_t tile[64][66];
-  const int64_t x0 = int64_t(blockIdx.x) * 64, y0 = int64_t(blockIdx.y) * 64;
-  const int64_t b = blockIdx.z;
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int r = w; r < 64; r += 4)
-    tile[r][l] = y0 + r < ny && x0 + l < nx ? in[(b * ny + y0 + r) * nx + x0 + l] : uint16_t(0);
-  __syncthreads();
-  for (int r = w; r < 64; r += 4)
-    if (x0 + r < nx && y0 + l < ldo) out[(b * nx + x0 + r) * ldo + y0 + l] = tile[l][r];
 }
 
 // ---------------------------------------------------------------------------
@@ -218,15 +217,23 @@ __global__ __launch_bounds__(256) void turn_kernel(const uint16_t* __restrict__ 
 constexpr int kOuterCols = 128;
 constexpr int kOuterList = 4096;
 
-struct OuterArgs {
-  const uint16_t* V;
-  int64_t ldv, n, len;
+struct OuterSide {
+  const uint16_t* V;         // NULL: not asked for
+  int64_t ldv, len;
   const uint16_t* parts;     // [n][3 rp]
-  const int32_t* row;
-  int rank, rp, shares;
   int by_column;             // 1: out_a [len][rank] (dB), 0: [rank][len] (dA)
+  int shares;
+  float* sums;               // [a][share] where shares > 1
+  float* out;
+  int vec;
+  unsigned blocks;
+};
+struct OuterArgs {           // both gradients in one launch, a range of blocks each
+  OuterSide side[2];
+  int64_t n;
+  const int32_t* row;
+  int rank, rp;
   int accumulate;
-  float* out;                // shares == 1: the result, else [a][share] sums
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -243,18 +250,24 @@ __device__ inline uint2 tr_read(const char* p) {
 __device__ inline int swz(int r) { return 2 * ((r & 3) | (((r >> 3) & 1) << 2)); }
 
 template <int NF>
-__global__ __launch_bounds__(256) void outer_kernel(OuterArgs a, bool vec_v) {
+__global__ __launch_bounds__(256) void outer_kernel(OuterArgs args) {
   constexpr int kRp = NF <= 2 ? 32 : 16 * NF;               // padded rank
   constexpr int kPartRow = kRp * 2 + 16;                    // bytes of a row of one part in LDS
+  constexpr int kChunks = (3 * kRp / 8 + 7) / 8;            // 16-byte chunks of parts a thread moves
   __shared__ __attribute__((aligned(16))) char lv[32 * kOuterCols * 2];
   __shared__ __attribute__((aligned(16))) char lp[3][32 * kPartRow];
   __shared__ int32_t list[kOuterList];
   __shared__ int wcount[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int kg = lane >> 4, c16 = lane & 15;
-  const int64_t c0 = int64_t(blockIdx.x) * kOuterCols;
-  const int ad = blockIdx.z, share = blockIdx.y;
-  const int64_t r0 = a.n * share / a.shares, r1 = a.n * (share + 1) / a.shares;
+  const bool second = blockIdx.x >= args.side[0].blocks;
+  const OuterSide& a = args.side[second ? 1 : 0];
+  const unsigned bx = blockIdx.x - (second ? args.side[0].blocks : 0);
+  const unsigned tiles = static_cast<unsigned>((a.len + kOuterCols - 1) / kOuterCols);
+  const int64_t c0 = int64_t(bx % tiles) * kOuterCols;
+  const int share = bx / tiles % a.shares, ad = bx / tiles / a.shares;
+  const int64_t r0 = args.n * share / a.shares, r1 = args.n * (share + 1) / a.shares;
+  const bool vec_v = a.vec;
   f32x4 acc[NF][2];
 #pragma unroll
   for (int f = 0; f < NF; ++f)
@@ -267,7 +280,7 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a, bool vec_v) {
     int count = 0;
     for (int b = 0; b < piece; b += 256) {
       const int e = b + tid;
-      const bool mine = e < piece && a.row[p0 + e] == ad;
+      const bool mine = e < piece && args.row[p0 + e] == ad;
       const uint64_t m = __ballot(mine);
       __syncthreads();
       if (lane == 0) wcount[wv] = __popcll(m);
@@ -278,24 +291,47 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a, bool vec_v) {
       count += wcount[0] + wcount[1] + wcount[2] + wcount[3];
     }
     __syncthreads();
-    for (int s = 0; s < count; s += 32) {
-      // ---- stage the step: thread t the two 16-byte chunks 2 (t % 8), + 1 of row t / 8 of V
-      const int rl = tid >> 3;
+    // ---- a step: thread t holds the two 16-byte chunks 2 (t % 8), + 1 of row t / 8
+    //      of V and every eighth chunk of its parts, loaded a step ahead
+    const int rl = tid >> 3;
+    const bool fast = vec_v && c0 + kOuterCols <= a.len;
+    u32x4 nv[2], np[kChunks];
+    auto load_step = [&](int s) {
       const bool have = s + rl < count;
-      const int64_t t = p0 + (have ? list[s + rl] : 0);
+      const int64_t t = p0 + list[have ? s + rl : 0];
+      const uint16_t* src = a.V + t * a.ldv + c0 + 16 * (tid & 7);
+      if (fast) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int ch = 2 * (tid & 7) + h;
-        u32x4 v = u32x4{0u, 0u, 0u, 0u};
-        if (have) v = load8(a.V + t * a.ldv, c0 + 8 * ch, a.len, vec_v);
-        *reinterpret_cast<u32x4*>(lv + rl * (kOuterCols * 2) + 16 * (ch ^ swz(rl))) = v;
+        for (int h = 0; h < 2; ++h) nv[h] = *reinterpret_cast<const u32x4*>(src + 8 * h);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          nv[h] = load8(a.V + t * a.ldv, c0 + 16 * (tid & 7) + 8 * h, a.len, vec_v);
       }
-      for (int ch = tid & 7; ch < 3 * kRp / 8; ch += 8) {
-        u32x4 v = u32x4{0u, 0u, 0u, 0u};
-        if (have) v = *reinterpret_cast<const u32x4*>(a.parts + t * 3 * a.rp + 8 * ch);
-        *reinterpret_cast<u32x4*>(lp[ch / (kRp / 8)] + rl * kPartRow + 16 * (ch % (kRp / 8))) = v;
+#pragma unroll
+      for (int u = 0; u < kChunks; ++u) {
+        const int ch = min((tid & 7) + 8 * u, 3 * kRp / 8 - 1);
+        np[u] = *reinterpret_cast<const u32x4*>(a.parts + t * 3 * args.rp + 8 * ch);
+      }
+      if (!have) {
+        nv[0] = nv[1] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int u = 0; u < kChunks; ++u) np[u] = u32x4{0u, 0u, 0u, 0u};
+      }
+    };
+    if (count) load_step(0);
+    for (int s = 0; s < count; s += 32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4*>(lv + rl * (kOuterCols * 2) + 16 * ((2 * (tid & 7) + h) ^ swz(rl))) = nv[h];
+#pragma unroll
+      for (int u = 0; u < kChunks; ++u) {
+        const int ch = (tid & 7) + 8 * u;
+        if (ch < 3 * kRp / 8)
+          *reinterpret_cast<u32x4*>(lp[ch / (kRp / 8)] + rl * kPartRow + 16 * (ch % (kRp / 8))) = np[u];
       }
       __syncthreads();
+      if (s + 32 < count) load_step(s + 32);
       u32x4 fv[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -320,7 +356,7 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a, bool vec_v) {
   }
   // ---- by row (dA): lane holds p = 16 f + 4 kg + v, column c16; by column
   //      (dB): lane holds columns 4 kg + v, p = 16 f + c16
-  float* out = a.out + (int64_t(ad) * a.shares + share) * a.rank * a.len;
+  float* out = (a.shares > 1 ? a.sums : a.out) + (int64_t(ad) * a.shares + share) * args.rank * a.len;
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
@@ -329,21 +365,27 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a, bool vec_v) {
       for (int v = 0; v < 4; ++v) {
         const int p = 16 * f + (a.by_column ? c16 : 4 * kg + v);
         const int64_t c = c0 + 32 * wv + 16 * j + (a.by_column ? 4 * kg + v : c16);
-        if (p >= a.rank || c >= a.len) continue;
-        float* o = out + (a.by_column ? c * a.rank + p : p * a.len + c);
-        *o = a.accumulate && a.shares == 1 ? *o + acc[f][j][v] : acc[f][j][v];
+        if (p >= args.rank || c >= a.len) continue;
+        float* o = out + (a.by_column ? c * args.rank + p : p * a.len + c);
+        *o = args.accumulate && a.shares == 1 ? *o + acc[f][j][v] : acc[f][j][v];
       }
 }
 
-__global__ __launch_bounds__(256) void outer_sum_kernel(const float* __restrict__ sums, int shares,
-                                                        int64_t per, int64_t total, int accumulate,
-                                                        float* __restrict__ out) {
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (e >= total) return;
-  const float* s = sums + e / per * shares * per + e % per;
-  float v = s[0];
-  for (int i = 1; i < shares; ++i) v += s[i * per];
-  out[e] = accumulate ? out[e] + v : v;
+// The shares' sums, four values a thread, in their order.
+__global__ __launch_bounds__(256) void outer_sum_kernel(OuterArgs args, int count, unsigned blocks0) {
+  const bool second = blockIdx.x >= blocks0;
+  const OuterSide& a = args.side[second ? 1 : 0];
+  const int64_t e = (int64_t(blockIdx.x - (second ? blocks0 : 0)) * 256 + threadIdx.x) * 4;
+  const int64_t per = int64_t(args.rank) * a.len;
+  if (e >= per * count) return;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (e + u >= per * count) break;
+    const float* s = a.sums + (e + u) / per * a.shares * per + (e + u) % per;
+    float v = s[0];
+    for (int i = 1; i < a.shares; ++i) v += s[i * per];
+    a.out[e + u] = args.accumulate ? a.out[e + u] + v : v;
+  }
 }
 
 __global__ void zero_kernel(float* __restrict__ p, int64_t n) {
@@ -366,19 +408,26 @@ size_t outer_floats(int64_t n, int64_t len, int rank, int count) {
   return s > 1 ? size_t(s) * count * rank * len : 0;
 }
 
-gptq_status launch_outer(OuterArgs a, int count, float* sums, float* out, hipStream_t st) {
-  const bool vec = a.ldv % 8 == 0 && reinterpret_cast<uintptr_t>(a.V) % 16 == 0;
-  a.out = a.shares > 1 ? sums : out;
-  const dim3 grid(ceil_div(a.len, kOuterCols), a.shares, count);
-  if (a.rank <= 16) outer_kernel<1><<<grid, 256, 0, st>>>(a, vec);
-  else if (a.rank <= 32) outer_kernel<2><<<grid, 256, 0, st>>>(a, vec);
-  else if (a.rank <= 64) outer_kernel<4><<<grid, 256, 0, st>>>(a, vec);
-  else outer_kernel<8><<<grid, 256, 0, st>>>(a, vec);
+gptq_status launch_outer(OuterArgs a, int count, hipStream_t st) {
+  unsigned sum_blocks[2] = {0, 0};
+  for (int i = 0; i < 2; ++i) {
+    OuterSide& o = a.side[i];
+    o.blocks = 0;
+    if (!o.out) continue;
+    o.vec = o.ldv % 8 == 0 && reinterpret_cast<uintptr_t>(o.V) % 16 == 0;
+    o.shares = outer_shares(a.n, o.len, a.rank, count);
+    o.blocks = ceil_div(o.len, kOuterCols) * o.shares * count;
+    if (o.shares > 1) sum_blocks[i] = ceil_div(int64_t(a.rank) * o.len * count, 1024);
+  }
+  const unsigned grid = a.side[0].blocks + a.side[1].blocks;
+  if (!grid) return GPTQ_OK;
+  if (a.rank <= 16) outer_kernel<1><<<grid, 256, 0, st>>>(a);
+  else if (a.rank <= 32) outer_kernel<2><<<grid, 256, 0, st>>>(a);
+  else if (a.rank <= 64) outer_kernel<4><<<grid, 256, 0, st>>>(a);
+  else outer_kernel<8><<<grid, 256, 0, st>>>(a);
   GPTQ_CHECK_LAUNCH();
-  if (a.shares > 1) {
-    const int64_t per = int64_t(a.rank) * a.len, total = per * count;
-    outer_sum_kernel<<<ceil_div(total, 256), 256, 0, st>>>(sums, a.shares, per, total,
-                                                           a.accumulate, out);
+  if (sum_blocks[0] + sum_blocks[1]) {
+    outer_sum_kernel<<<sum_blocks[0] + sum_blocks[1], 256, 0, st>>>(a, count, sum_blocks[0]);
     GPTQ_CHECK_LAUNCH();
   }
   return GPTQ_OK;
@@ -433,13 +482,14 @@ LoraWs carve_lora(Carver& c, int64_t n, int64_t m, int64_t d, int64_t group, int
 }
 
 struct BackWs {
-  uint16_t* parts;
+  uint16_t* parts;   // of G
+  uint16_t* hparts;  // of alpha H
   float* sums;
   uint16_t* At;      // [count][d][rank]
   uint16_t* Bt;      // [count][rank][mp]
   uint16_t* Wt;      // [d][mp]
   uint16_t* V2;      // [rows][mp]
-  float* outer;
+  float* outer[2];
 };
 
 BackWs carve_back(Carver& c, int64_t n, int64_t m, int64_t d, int rank, int count) {
@@ -450,11 +500,13 @@ BackWs carve_back(Carver& c, int64_t n, int64_t m, int64_t d, int rank, int coun
   w.V2 = c.take<uint16_t>(size_t(nc) * mp);
   if (count == 0) return w;
   w.parts = c.take<uint16_t>(size_t(n) * 3 * parts_rank(rank));
+  w.hparts = c.take<uint16_t>(size_t(n) * 3 * parts_rank(rank));
   const int shares = shrink_shares(n, m);
   w.sums = c.take<float>(shares > 1 ? size_t(shares) * n * rank : 0);
   w.At = c.take<uint16_t>(size_t(count) * d * rank);
   w.Bt = c.take<uint16_t>(size_t(count) * rank * mp);
-  w.outer = c.take<float>(std::max(outer_floats(n, d, rank, count), outer_floats(n, m, rank, count)));
+  w.outer[0] = c.take<float>(outer_floats(n, d, rank, count));
+  w.outer[1] = c.take<float>(outer_floats(n, m, rank, count));
   return w;
 }
 
@@ -558,35 +610,22 @@ gptq_status launch_lora_backward(const uint16_t* dY, int64_t lddy, int64_t n, co
   const BackWs b = carve_back(c, n, w.m, w.d, ad.rank, ad.n_adapters);
   const int64_t mp = round_up(w.m, 64);
   const int rp = parts_rank(ad.rank);
-  ShrinkArgs h{dY, lddy, n, w.m, b.Bt, mp, ad.row, ad.n_adapters, ad.rank, rp, ad.alpha, 1,
-               nullptr, b.parts, b.sums};
-  if (dB) {
-    // alpha H as parts, then the sums over rows
-    split_kernel<<<ceil_div(n * rp, 256), 256, 0, st>>>(h, H);
-    GPTQ_CHECK_LAUNCH();
-    OuterArgs o{dY, lddy, n, w.m, b.parts, ad.row, ad.rank, rp,
-                outer_shares(n, w.m, ad.rank, ad.n_adapters), 1, accumulate, nullptr};
-    if ((s = launch_outer(o, ad.n_adapters, b.outer, dB, st)) != GPTQ_OK) return s;
-  }
-  if (adp && (dX || dA)) {
-    // G as parts (over those of H)
-    turn_kernel<<<dim3(ceil_div(ad.rank, 64), ceil_div(mp, 64), ad.n_adapters), 256, 0, st>>>(
-        static_cast<const uint16_t*>(ad.B), w.m, ad.rank, b.Bt, mp);
-    GPTQ_CHECK_LAUNCH();
+  const bool need_g = adp && (dX || dA);
+  PrepareArgs pa{w, mp, dX ? b.Wt : nullptr, ad, rp, need_g ? b.Bt : nullptr,
+                 adp && dX ? b.At : nullptr, H, n, dB ? b.hparts : nullptr};
+  if ((s = launch_prepare(pa, st)) != GPTQ_OK) return s;
+  if (need_g) {
+    const ShrinkArgs h{dY, lddy, n, w.m, b.Bt, mp, ad.row, ad.n_adapters, ad.rank, rp, ad.alpha, 1,
+                       nullptr, b.parts, b.sums};
     if ((s = launch_shrink(h, st)) != GPTQ_OK) return s;
   }
-  if (dA) {
-    OuterArgs o{X, ldx, n, w.d, b.parts, ad.row, ad.rank, rp,
-                outer_shares(n, w.d, ad.rank, ad.n_adapters), 0, accumulate, nullptr};
-    if ((s = launch_outer(o, ad.n_adapters, b.outer, dA, st)) != GPTQ_OK) return s;
+  if (dA || dB) {
+    OuterArgs o{{OuterSide{X, ldx, w.d, b.parts, 0, 1, b.outer[0], dA, 0, 0},
+                 OuterSide{dY, lddy, w.m, b.hparts, 1, 1, b.outer[1], dB, 0, 0}},
+                n, ad.row, ad.rank, rp, accumulate};
+    if ((s = launch_outer(o, ad.n_adapters, st)) != GPTQ_OK) return s;
   }
   if (!dX) return GPTQ_OK;
-  if (adp) {
-    turn_kernel<<<dim3(ceil_div(w.d, 64), ceil_div(ad.rank, 64), ad.n_adapters), 256, 0, st>>>(
-        static_cast<const uint16_t*>(ad.A), ad.rank, w.d, b.At, ad.rank);
-    GPTQ_CHECK_LAUNCH();
-  }
-  if ((s = launch_expand_transposed(w, b.Wt, mp, st)) != GPTQ_OK) return s;
   const bool direct = as_is(dY, lddy, w.m);
   GemmArgs g{};
   g.m = w.d;

@@ -57,8 +57,20 @@ gptq_status launch_expand_row(const Packed& w, uint16_t* M, int64_t ldm, float* 
                               hipStream_t st);
 // M[j][p ldp + c] = part p of three of W_hat[j][c] in bf16 (their sum is exact in fp32).
 gptq_status launch_expand_parts(const Packed& w, uint16_t* M, int64_t ldp, hipStream_t st);
-// M[c][j] = W_hat[j][c] rounded to bf16, columns m .. ldm zero.
-gptq_status launch_expand_transposed(const Packed& w, uint16_t* M, int64_t ldm, hipStream_t st);
+// What the backward pass lays out (NULL: not asked for).
+struct PrepareArgs {
+  Packed w;
+  int64_t mp;          // m padded to 64
+  uint16_t* Wt;        // [d][mp] W_hat^T rounded to bf16, zeros past m
+  gptq_adapters ad;
+  int rp;
+  uint16_t* Bt;        // [n_adapters][rank][mp]
+  uint16_t* At;        // [n_adapters][d][rank]
+  const float* H;
+  int64_t n;
+  uint16_t* hparts;    // [n][3 rp] parts of alpha H
+};
+gptq_status launch_prepare(const PrepareArgs& a, hipStream_t st);
 // V2[t][0 .. cols) = V[t][0 .. len) and zeros.
 gptq_status launch_pad_rows(const uint16_t* V, int64_t ldv, int64_t n, int64_t len, uint16_t* V2,
                             int64_t cols, hipStream_t st);
@@ -66,7 +78,7 @@ gptq_status launch_pad_rows(const uint16_t* V, int64_t ldv, int64_t n, int64_t l
 gptq_status launch_gemm(const GemmArgs& a, int fold, hipStream_t st);
 
 // Few rows (lora_decode.hip): no workspace but H [n][rank].
-constexpr int64_t kDecodeMaxRows = 64;
+constexpr int64_t kDecodeMaxRows = 128;
 bool decode_takes(int64_t n, int64_t ng);
 gptq_status launch_lora_decode(const uint16_t* X, int64_t ldx, int64_t n, const Packed& w,
                                const gptq_adapters& ad, float* H, void* Y, int out_bf16,
@@ -109,6 +121,36 @@ __device__ inline u32x4 load8(const uint16_t* __restrict__ p, int64_t c, int64_t
   for (int i = 0; i < 8; ++i)
     if (c + i < len) v[i >> 1] |= uint32_t(p[c + i]) << (16 * (i & 1));
   return v;
+}
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ inline float dot2(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
+                                         __builtin_bit_cast(bf16x2, b), c, false);
+}
+__device__ inline float dot8(const u32x4& a, const u32x4& b, float c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = dot2(a[i], b[i], c);
+  return c;
+}
+
+// Dot product of two rows by a wave, the sum in every lane; vec: 16-byte aligned.
+__device__ inline float dot_wave(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
+                                 int64_t len, bool vec, int lane) {
+  float s = 0.0f;
+  int64_t b = 0;
+  if (vec) {                               // whole 512-column rounds, loads back to back
+#pragma unroll 8
+    for (; b + 512 <= len; b += 512)
+      s = dot8(*reinterpret_cast<const u32x4*>(x + b + 8 * lane),
+               *reinterpret_cast<const u32x4*>(w + b + 8 * lane), s);
+  }
+  for (int64_t c = b + 8 * lane; c < len; c += 512)
+    s = dot8(load8(x, c, len, vec), load8(w, c, len, vec), s);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  return s;
 }
 
 // Step Delta and code minus zero of weight (r, c).

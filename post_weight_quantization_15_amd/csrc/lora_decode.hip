@@ -37,18 +37,6 @@ struct HiddenArgs {
   float* H;
 };
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-__device__ inline float dot2(uint32_t a, uint32_t b, float c) {
-  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
-                                         __builtin_bit_cast(bf16x2, b), c, false);
-}
-__device__ inline float dot8(const u32x4& a, const u32x4& b, float c) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c = dot2(a[i], b[i], c);
-  return c;
-}
-
 __global__ __launch_bounds__(256) void hidden_kernel(HiddenArgs a, bool vec_x, bool vec_a) {
   const int lane = threadIdx.x & 63;
   const int64_t t = blockIdx.y;
@@ -59,17 +47,7 @@ __global__ __launch_bounds__(256) void hidden_kernel(HiddenArgs a, bool vec_x, b
   if (id >= 0 && id < a.n_adapters) {
     const uint16_t* x = a.X + t * a.ldx;
     const uint16_t* w = a.A + (int64_t(id) * a.rank + p) * a.d;
-    int64_t b = 0;
-    if (vec_x && vec_a) {                  // whole 512-column rounds, loads back to back
-#pragma unroll 8
-      for (; b + 512 <= a.d; b += 512)
-        s = dot8(*reinterpret_cast<const u32x4*>(x + b + 8 * lane),
-                 *reinterpret_cast<const u32x4*>(w + b + 8 * lane), s);
-    }
-    for (int64_t c = b + 8 * lane; c < a.d; c += 512)
-      s = dot8(load8(x, c, a.d, vec_x), load8(w, c, a.d, vec_a), s);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    s = dot_wave(x, w, a.d, vec_x && vec_a, lane);
   }
   if (lane == 0) a.H[t * a.rank + p] = s;
 }
@@ -182,6 +160,7 @@ __device__ inline void turn4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d)
   d = v[1];
 }
 
+// grid.y: passes of 64 rows.
 template <int BITS, int NT>
 __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a, bool vec_x,
                                                                    bool vec_w) {
@@ -192,6 +171,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, c16 = lane & 15;
   const Packed& w = a.w;
+  const int64_t tb = int64_t(blockIdx.y) * 64;
   const int64_t j0 = int64_t(blockIdx.x) * kDecodeRows;
   const int64_t jr = min<int64_t>(j0 + c16, w.m - 1);
   const int ng = static_cast<int>(w.ng);
@@ -208,7 +188,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
   int ga[kAhead], gb[kAhead];              // group ids of columns 2 lane, 2 lane + 1
   const uint16_t* xr[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xr[i] = a.X + min<int64_t>(16 * i + c16, a.n - 1) * a.ldx;
+  for (int i = 0; i < NT; ++i) xr[i] = a.X + min<int64_t>(tb + 16 * i + c16, a.n - 1) * a.ldx;
   const int whole = vec_x && vec_w ? static_cast<int>(w.d / 128) : 0;
   auto load_chunk = [&](int ch, uint32_t* cv, u32x4 (*xv)[4], int& g0, int& g1) {
     const int64_t k0 = int64_t(ch) * 128;
@@ -331,7 +311,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
     for (int v = 0; v < 4; ++v) red[wv][i][4 * q + v][c16] = acc[i][v];
   __syncthreads();
   for (int e = tid; e < NT * 256; e += kDecodeWaves * 64) {
-    const int64_t t = e >> 4, j = j0 + (e & 15);
+    const int64_t t = tb + (e >> 4), j = j0 + (e & 15);
     if (t >= a.n || j >= w.m) continue;
     float y = 0.0f;
 #pragma unroll
@@ -359,7 +339,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 
 template <int BITS>
 void launch_bits(const DecodeArgs& a, bool vx, bool vw, hipStream_t st) {
-  const unsigned grid = ceil_div(a.w.m, kDecodeRows);
+  const dim3 grid(ceil_div(a.w.m, kDecodeRows), ceil_div(a.n, 64));
   const size_t lds = size_t(a.w.ng) * kDecodeRows * 8;
   if (a.n <= 16) decode_kernel<BITS, 1><<<grid, kDecodeWaves * 64, lds, st>>>(a, vx, vw);
   else if (a.n <= 32) decode_kernel<BITS, 2><<<grid, kDecodeWaves * 64, lds, st>>>(a, vx, vw);

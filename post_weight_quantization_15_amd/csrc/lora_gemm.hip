@@ -35,6 +35,7 @@ constexpr int kPlanMaxGroups = 2048;      // groups of at least 32 columns, d <=
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __restrict__ g_idx,
                                                             int d, int ng, int unit, int cols_max,
                                                             int32_t* __restrict__ plan) {
+  extern __shared__ uint16_t of[];         // the columns' groups
   __shared__ int32_t cnt[kPlanMaxGroups];
   __shared__ int32_t start[kPlanMaxGroups + 1];
   __shared__ int ident;
@@ -49,10 +50,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
 #pragma unroll 4
   for (int c = tid; c < d; c += kPlanThreads) {
     const int g = min(max(g_idx[c], 0), ng - 1);
-    const int before = g_idx[max(c - 1, 0)];
+    of[c] = static_cast<uint16_t>(g);
     atomicAdd(&cnt[g], 1);
-    if (g < before) inc = false;
   }
+  __syncthreads();
+  for (int c = tid + 1; c < d; c += kPlanThreads) inc = inc && of[c] >= of[c - 1];
   if (!inc) ident = 0;
   __syncthreads();
   if (tid < 64) {                          // padded starts: one wave's running sum
@@ -93,18 +95,16 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
       continue;
     }
     int at = s;
-    for (int c0 = 0; c0 < d && at < s + n; c0 += 512) {     // eight loads at a time
+    for (int c0 = 0; c0 < d && at < s + n; c0 += 512) {     // eight reads at a time
       int v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = of[min(c0 + 64 * i + lane, d - 1)];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c = c0 + 64 * i + lane;
-        v[i] = c < d ? min(max(g_idx[c], 0), ng - 1) : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool mine = v[i] == g;
+        const bool mine = c < d && v[i] == g;
         const uint64_t b = __ballot(mine);
-        if (mine) order[at + __popcll(b & ((uint64_t(1) << lane) - 1))] = c0 + 64 * i + lane;
+        if (mine) order[at + __popcll(b & ((uint64_t(1) << lane) - 1))] = c;
         at += __popcll(b);
       }
     }
@@ -311,14 +311,15 @@ __global__ __launch_bounds__(256) void expand_parts_kernel(Packed w, int64_t wor
 // column) to the turned tile in LDS: 32 lanes write 32 consecutive words, and
 // a column's stride of 144 bytes puts the wave's two runs in different halves
 // of the banks.  The tile leaves as 128 contiguous bytes of a column.
+constexpr int kTurnCols = 128;
+
 template <int BITS>
-__global__ __launch_bounds__(256) void expand_transposed_kernel(Packed w, int64_t words,
-                                                                uint16_t* __restrict__ M,
-                                                                int64_t ldm) {
-  constexpr int kCols = 128;
-  __shared__ __attribute__((aligned(16))) uint32_t tile[kCols][36];
+__device__ inline void expand_transposed(const Packed& w, int64_t words, uint16_t* __restrict__ M,
+                                         int64_t ldm, unsigned bx, unsigned by, char* lds) {
+  constexpr int kCols = kTurnCols;
+  auto tile = reinterpret_cast<uint32_t(*)[36]>(lds);
   const int tid = threadIdx.x;
-  const int64_t c0 = int64_t(blockIdx.x) * kCols, j0 = int64_t(blockIdx.y) * 64;
+  const int64_t c0 = int64_t(bx) * kCols, j0 = int64_t(by) * 64;
   const int pair = tid & 31;
 #pragma unroll
   for (int e = 0; e < kCols / 64; ++e) {
@@ -372,6 +373,58 @@ __global__ __launch_bounds__(256) void expand_transposed_kernel(Packed w, int64_
       *reinterpret_cast<u32x4*>(M + (c0 + cl) * ldm + j0 + 8 * u) =
           *reinterpret_cast<const u32x4*>(&tile[cl][4 * u]);
   }
+}
+
+// out[b][x][y] = in[b][y][x], a 64 x 64 tile; rows of `out` at stride ldo, zeros past ny.
+__device__ inline void turn_tile(const uint16_t* __restrict__ in, int64_t ny, int64_t nx,
+                                 uint16_t* __restrict__ out, int64_t ldo, int64_t b, int64_t x0,
+                                 int64_t y0, char* lds) {
+  auto tile = reinterpret_cast<uint16_t(*)[66]>(lds);
+  const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int r = w; r < 64; r += 4)
+    tile[r][l] = y0 + r < ny && x0 + l < nx ? in[(b * ny + y0 + r) * nx + x0 + l] : uint16_t(0);
+  __syncthreads();
+  for (int r = w; r < 64; r += 4)
+    if (x0 + r < nx && y0 + l < ldo) out[(b * nx + x0 + r) * ldo + y0 + l] = tile[l][r];
+}
+
+// Everything the backward pass lays out, one launch: W_hat^T, B and A turned,
+// alpha H as parts; each by its range of blocks (0: not asked for).
+template <int BITS>
+__global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs a, unsigned nw, unsigned wx,
+                                                      unsigned nb, unsigned nta, unsigned) {
+  __shared__ __attribute__((aligned(16))) char lds[kTurnCols * 36 * 4];
+  unsigned b = blockIdx.x;
+  if (b < nw) {
+    expand_transposed<BITS>(a.w, (a.w.d * BITS + 31) / 32, a.Wt, a.mp, b % wx, b / wx, lds);
+    return;
+  }
+  b -= nw;
+  const int rank = a.ad.rank;
+  if (b < nb) {                              // Bt[a][q][j] = B[a][j][q]
+    const unsigned tx = (rank + 63) / 64, ty = static_cast<unsigned>(a.mp / 64);
+    turn_tile(static_cast<const uint16_t*>(a.ad.B), a.w.m, rank, a.Bt, a.mp, b / (tx * ty),
+              int64_t(b % tx) * 64, int64_t(b / tx % ty) * 64, lds);
+    return;
+  }
+  b -= nb;
+  if (b < nta) {                             // At[a][c][q] = A[a][q][c]
+    const unsigned tx = static_cast<unsigned>((a.w.d + 63) / 64), ty = (rank + 63) / 64;
+    turn_tile(static_cast<const uint16_t*>(a.ad.A), rank, a.w.d, a.At, rank, b / (tx * ty),
+              int64_t(b % tx) * 64, int64_t(b / tx % ty) * 64, lds);
+    return;
+  }
+  b -= nta;
+  const int64_t e = int64_t(b) * 256 + threadIdx.x;
+  const int64_t t = e / a.rp;
+  const int p = static_cast<int>(e % a.rp);
+  if (t >= a.n) return;
+  const int id = a.ad.row[t];                // rows without an adapter are never read
+  if (id < 0 || id >= a.ad.n_adapters) return;
+  uint16_t part[3];
+  split3(p < rank ? a.ad.alpha[id] * a.H[t * rank + p] : 0.0f, part);
+#pragma unroll
+  for (int u = 0; u < 3; ++u) a.hparts[t * 3 * a.rp + u * a.rp + p] = part[u];
 }
 
 // ---------------------------------------------------------------------------
@@ -788,7 +841,7 @@ size_t plan_words(int64_t d, int64_t ng, int64_t group) {
 
 gptq_status launch_plan(const Packed& w, int32_t* plan, hipStream_t st) {
   const unsigned grid = w.ng < 512 ? ceil_div(w.ng, 8) : 64;
-  plan_kernel<<<grid, kPlanThreads, 0, st>>>(w.g_idx, int(w.d), int(w.ng), fold_unit(w.group),
+  plan_kernel<<<grid, kPlanThreads, size_t(w.d) * 2, st>>>(w.g_idx, int(w.d), int(w.ng), fold_unit(w.group),
                                              int(plan_cols(w.d, w.ng, w.group)), plan);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
@@ -858,14 +911,20 @@ gptq_status launch_expand_parts(const Packed& w, uint16_t* M, int64_t ldp, hipSt
   return GPTQ_OK;
 }
 
-gptq_status launch_expand_transposed(const Packed& w, uint16_t* M, int64_t ldm, hipStream_t st) {
-  const int64_t words = (w.d * w.bits + 31) / 32;
-  const dim3 grid(ceil_div(w.d, 128), ceil_div(ldm, 64));
-  switch (w.bits) {
-    case 2: expand_transposed_kernel<2><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
-    case 3: expand_transposed_kernel<3><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
-    case 4: expand_transposed_kernel<4><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
-    default: expand_transposed_kernel<8><<<grid, 256, 0, st>>>(w, words, M, ldm); break;
+gptq_status launch_prepare(const PrepareArgs& a, hipStream_t st) {
+  const unsigned wx = ceil_div(a.w.d, kTurnCols);
+  const unsigned nw = a.Wt ? wx * ceil_div(a.mp, 64) : 0;
+  const unsigned count = static_cast<unsigned>(a.ad.n_adapters), tr = (a.ad.rank + 63) / 64;
+  const unsigned nb = a.Bt ? tr * ceil_div(a.mp, 64) * count : 0;
+  const unsigned na = a.At ? tr * ceil_div(a.w.d, 64) * count : 0;
+  const unsigned nh = a.hparts ? ceil_div(a.n * a.rp, 256) : 0;
+  const unsigned grid = nw + nb + na + nh;
+  if (!grid) return GPTQ_OK;
+  switch (a.w.bits) {
+    case 2: prepare_kernel<2><<<grid, 256, 0, st>>>(a, nw, wx, nb, na, nh); break;
+    case 3: prepare_kernel<3><<<grid, 256, 0, st>>>(a, nw, wx, nb, na, nh); break;
+    case 4: prepare_kernel<4><<<grid, 256, 0, st>>>(a, nw, wx, nb, na, nh); break;
+    default: prepare_kernel<8><<<grid, 256, 0, st>>>(a, nw, wx, nb, na, nh); break;
   }
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
