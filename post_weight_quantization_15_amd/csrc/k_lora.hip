@@ -19,7 +19,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // Down to the hidden values: out[t][p] = sum_k V[t][k] M_a[p][k].
 //
-// A workgroup owns 32 rows; its four waves take every fourth 32-step of k
+// A workgroup owns 32 rows; its eight waves take every eighth 32-step of k
 // (and grid.y a share of the steps where there are few rows), and their
 // sums meet in LDS.  Rows are independent in the product, so a tile with
 // several adapters runs once per adapter and keeps each adapter's rows.
@@ -53,9 +53,9 @@ __device__ inline void put_hidden(const ShrinkArgs& a, int64_t t, int p, float v
   for (int u = 0; u < 3; ++u) a.parts[t * 3 * a.rp + u * a.rp + p] = part[u];
 }
 
-template <int NF>
-__global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a, bool vec_v, bool vec_m) {
-  __shared__ float red[4][kShrinkRows][16 * NF + 4];
+template <int NF, int NW>
+__global__ __launch_bounds__(NW * 64) void shrink_kernel(ShrinkArgs a, bool vec_v, bool vec_m) {
+  __shared__ float red[NW][kShrinkRows][16 * NF + 4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int q = lane >> 4, c16 = lane & 15;
   const int64_t t0 = int64_t(blockIdx.x) * kShrinkRows;
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a, bool vec_v, b
       for (int f = 0; f < NF; ++f)
         mr[f] = Ma + int64_t(min(16 * f + c16, a.rank - 1)) * a.ldm + 8 * q;
 #pragma unroll(NF > 2 ? 2 : 4)
-      for (; s < whole; s += 4) {
+      for (; s < whole; s += NW) {
         u32x4 fv[2], fm[NF];
 #pragma unroll
         for (int i = 0; i < 2; ++i) fv[i] = *reinterpret_cast<const u32x4*>(vr[i] + 32 * s + 8 * q);
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a, bool vec_v, b
           for (int i = 0; i < 2; ++i) acc[i][f] = mfma16(fm[f], fv[i], acc[i][f]);
       }
     }
-    for (; s < s1; s += 4) {
+    for (; s < s1; s += NW) {
       u32x4 fv[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) fv[i] = load8(vr[i], 32 * s + 8 * q, a.len, vec_v);
@@ -117,12 +117,15 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a, bool vec_v, b
       for (int f = 0; f < NF; ++f)
         *reinterpret_cast<f32x4*>(&red[wv][16 * i + c16][16 * f + 4 * q]) = acc[i][f];
     __syncthreads();
-    for (int e = tid; e < kShrinkRows * a.rp; e += 256) {
+    for (int e = tid; e < kShrinkRows * a.rp; e += NW * 64) {
       const int tl = e / a.rp, p = e % a.rp;
       if (!((in >> tl) & 1u)) continue;
       const int64_t t = t0 + tl;
       float v = 0.0f;
-      if (p < a.rank) v = (red[0][tl][p] + red[1][tl][p]) + (red[2][tl][p] + red[3][tl][p]);
+      if (p < a.rank) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) v += red[w][tl][p];
+      }
       if (gridDim.y > 1) {
         if (p < a.rank) a.sums[(int64_t(blockIdx.y) * a.n + t) * a.rank + p] = v;
       } else {
@@ -132,7 +135,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a, bool vec_v, b
   }
   // rows without an adapter
   if (blockIdx.y == 0 && a.H)
-    for (int e = tid; e < kShrinkRows * a.rank; e += 256) {
+    for (int e = tid; e < kShrinkRows * a.rank; e += NW * 64) {
       const int tl = e / a.rank;
       if (((none >> tl) & 1u) && t0 + tl < a.n) a.H[(t0 + tl) * a.rank + e % a.rank] = 0.0f;
     }
@@ -189,10 +192,10 @@ gptq_status launch_shrink(const ShrinkArgs& a, hipStream_t st) {
   }
   const int shares = shrink_shares(a.n, a.len);
   const dim3 grid(ceil_div(a.n, kShrinkRows), shares);
-  if (a.rank <= 16) shrink_kernel<1><<<grid, 256, 0, st>>>(a, vv, vm);
-  else if (a.rank <= 32) shrink_kernel<2><<<grid, 256, 0, st>>>(a, vv, vm);
-  else if (a.rank <= 64) shrink_kernel<4><<<grid, 256, 0, st>>>(a, vv, vm);
-  else shrink_kernel<8><<<grid, 256, 0, st>>>(a, vv, vm);
+  if (a.rank <= 16) shrink_kernel<1, 8><<<grid, 512, 0, st>>>(a, vv, vm);
+  else if (a.rank <= 32) shrink_kernel<2, 8><<<grid, 512, 0, st>>>(a, vv, vm);
+  else if (a.rank <= 64) shrink_kernel<4, 8><<<grid, 512, 0, st>>>(a, vv, vm);
+  else shrink_kernel<8, 4><<<grid, 256, 0, st>>>(a, vv, vm);
   GPTQ_CHECK_LAUNCH();
   if (shares > 1) {
     shrink_sum_kernel<<<ceil_div(a.n * a.rp, 256), 256, 0, st>>>(a, shares);
@@ -371,13 +374,23 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs args) {
       }
 }
 
-// The shares' sums, four values a thread, in their order.
+// The shares' sums in their order, four neighbouring values a thread (16-byte
+// loads where a result's length is a multiple of four).
 __global__ __launch_bounds__(256) void outer_sum_kernel(OuterArgs args, int count, unsigned blocks0) {
   const bool second = blockIdx.x >= blocks0;
   const OuterSide& a = args.side[second ? 1 : 0];
   const int64_t e = (int64_t(blockIdx.x - (second ? blocks0 : 0)) * 256 + threadIdx.x) * 4;
   const int64_t per = int64_t(args.rank) * a.len;
   if (e >= per * count) return;
+  if (per % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0) {
+    const float* s = a.sums + e / per * a.shares * per + e % per;
+    f32x4 v = *reinterpret_cast<const f32x4*>(s);
+#pragma unroll 8
+    for (int i = 1; i < a.shares; ++i) v += *reinterpret_cast<const f32x4*>(s + i * per);
+    f32x4* o = reinterpret_cast<f32x4*>(a.out + e);
+    *o = args.accumulate ? *o + v : v;
+    return;
+  }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     if (e + u >= per * count) break;

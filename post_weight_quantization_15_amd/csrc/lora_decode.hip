@@ -4,7 +4,7 @@
 //
 // hidden_kernel: H[t][p] = X[t] . A_a[p], one wave per value (fp32, exact
 //   bf16 products in pairs); the rows of A are the traffic.
-// decode_kernel: a workgroup of eight waves owns 16 output rows; the waves
+// decode_kernel: a workgroup of 4 to 16 waves owns 16 output rows; the waves
 //   share the input dimension in chunks of 128 columns.  In a chunk lane
 //   (j, q) loads the 32 codes of row j, columns 32 q .. 32 q + 31, in one
 //   load (16 rows x 64 bytes at 4 bits), four register swaps turn them so that
@@ -24,7 +24,6 @@ namespace gptq {
 namespace {
 
 constexpr int kDecodeRows = 16;            // output rows per workgroup
-constexpr int kDecodeWaves = 8;
 constexpr int kDecodeMaxGroups = 768;      // 96 KB of grids in LDS
 
 // ---------------------------------------------------------------------------
@@ -58,14 +57,15 @@ struct DecodeArgs {
   int64_t ldx, n;
   Packed w;
   int64_t words;
-  const float* H;
+  float* H;
+  const uint16_t* A;
   const uint16_t* B;
   const float* alpha;
   const int32_t* row;
   int n_adapters, rank;
   void* Y;
   int64_t ldy;
-  int out_bf16;
+  int out_bf16, fused;
 };
 
 // Eight codes in nibbles as four bf16 pairs 16 + k, in order.
@@ -160,13 +160,15 @@ __device__ inline void turn4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d)
   d = v[1];
 }
 
-// grid.y: passes of 64 rows.
-template <int BITS, int NT>
-__global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a, bool vec_x,
-                                                                   bool vec_w) {
+// NW waves share the input dimension; grid.y: passes of 64 rows.  FUSED (one
+// row): every workgroup forms the hidden values itself, from L2.
+template <int BITS, int NT, int NW>
+__global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(DecodeArgs a, bool vec_x,
+                                                                   bool vec_w, bool vec_a) {
   constexpr int kW = BITS == 8 ? 8 : BITS;      // words of 32 codes
   extern __shared__ __attribute__((aligned(16))) float grid[];   // [ng][16 rows] (Delta, zz)
-  __shared__ float red[kDecodeWaves][NT][16][17];
+  __shared__ float red[NW][NT][16][17];
+  __shared__ float hid[kMaxRank];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, c16 = lane & 15;
@@ -182,7 +184,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
   // ahead of their use; whole ones (of aligned rows) in wide loads without
   // a condition among them, the last one of the row piece by piece.
   // Activation rows past n read row n - 1: their sums are not stored.
-  constexpr int kAhead = NT == 1 ? (BITS == 8 ? 3 : 4) : NT == 2 ? 2 : 1;
+  constexpr int kAhead = NT == 1 ? 2 : 1;
   uint32_t codes[kAhead][kW];
   u32x4 x[kAhead][NT][4];
   int ga[kAhead], gb[kAhead];              // group ids of columns 2 lane, 2 lane + 1
@@ -229,11 +231,50 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
   };
 #pragma unroll
   for (int u = 0; u < kAhead; ++u)
-    if (wv + kDecodeWaves * u < chunks)
-      load_chunk(wv + kDecodeWaves * u, codes[u], x[u], ga[u], gb[u]);
+    if (wv + NW * u < chunks)
+      load_chunk(wv + NW * u, codes[u], x[u], ga[u], gb[u]);
 
+  if (NT == 1 && a.fused) {
+    const int id = a.row[0];
+    const bool some = id >= 0 && id < a.n_adapters;
+    for (int p = wv; p < a.rank; p += NW) {
+      float s = 0.0f;
+      if (some) s = dot_wave(a.X, a.A + (int64_t(id) * a.rank + p) * w.d, w.d, vec_x && vec_a, lane);
+      if (lane == 0) {
+        hid[p] = s;
+        if (a.H && blockIdx.x == 0) a.H[p] = s;
+      }
+    }
+    __syncthreads();
+  }
+  // The adapter's part of the outputs this thread will write (NT = 1: the first
+  // 256 threads one each): its loads ride along with those above.
+  constexpr int kOuts = (NT * 256 + NW * 64 - 1) / (NW * 64);
+  float part_y[kOuts];
+#pragma unroll
+  for (int o = 0; o < kOuts; ++o) {
+    const int e = tid + o * NW * 64;
+    const int64_t t = tb + (e >> 4), j = j0 + (e & 15);
+    part_y[o] = 0.0f;
+    if (e >= NT * 256 || t >= a.n || j >= w.m) continue;
+    const int id = a.row[t];
+    if (id < 0 || id >= a.n_adapters) continue;
+    const uint16_t* b = a.B + (int64_t(id) * w.m + j) * a.rank;
+    const float* h = a.fused ? hid : a.H + t * a.rank;
+    float s = 0.0f;
+    int p = 0;
+    if (a.rank % 8 == 0 && reinterpret_cast<uintptr_t>(a.B) % 16 == 0)
+      for (; p < a.rank; p += 8) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(b + p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          s = fmaf(h[p + i], bf16_f32((v[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), s);
+      }
+    for (; p < a.rank; ++p) s = fmaf(h[p], bf16_f32(b[p]), s);
+    part_y[o] = a.alpha[id] * s;
+  }
   constexpr bool kMagic = BITS != 8;
-  for (int e = tid; e < ng * kDecodeRows; e += kDecodeWaves * 64) {
+  for (int e = tid; e < ng * kDecodeRows; e += NW * 64) {
     const int r = e / ng, g = e % ng;
     const int64_t at = min<int64_t>(j0 + r, w.m - 1) * ng + g;
     grid[(g * kDecodeRows + r) * 2] = step_at(w, at);
@@ -246,10 +287,10 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const u32x4 ones = u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  for (int cb = wv; cb < chunks; cb += kDecodeWaves * kAhead) {
+  for (int cb = wv; cb < chunks; cb += NW * kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int ch = cb + kDecodeWaves * u;
+      const int ch = cb + NW * u;
       if (ch >= chunks) break;
       const int64_t k0 = int64_t(ch) * 128;
       Run<BITS> run[4];
@@ -264,11 +305,35 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 #pragma unroll
           for (int h = 0; h < (BITS == 8 ? 2 : 1); ++h) run[s].w[h] ^= top_bits<BITS>();
       }
+      // The chunk's groups: one, one per step, or steps that mix them.  Decided
+      // once a chunk, so that its four steps' chains run side by side.
+      const int G0 = __builtin_amdgcn_readlane(ga[u], 0), G1 = __builtin_amdgcn_readlane(ga[u], 16),
+                G2 = __builtin_amdgcn_readlane(ga[u], 32), G3 = __builtin_amdgcn_readlane(ga[u], 48);
+      const int own = q == 0 ? G0 : q == 1 ? G1 : q == 2 ? G2 : G3;
+      const uint64_t diff = __ballot(ga[u] != own || gb[u] != own);
+      if (!diff && G0 == G1 && G1 == G2 && G2 == G3) {
+        const int gi = min(max(G0, 0), ng - 1);
+        const float dl = grid[(gi * kDecodeRows + c16) * 2];
+        const float zz = grid[(gi * kDecodeRows + c16) * 2 + 1] + (kMagic ? 16.0f : 0.0f);
+        u32x4 m[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) m[s] = run_operand<BITS>(run[s]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          f32x4 P = f32x4{0.f, 0.f, 0.f, 0.f}, Xs = P;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            P = mfma16(x[u][i][s], m[s], P);
+            Xs = mfma16(x[u][i][s], ones, Xs);
+          }
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(dl, fmaf(-zz, Xs[v], P[v]), acc[i][v]);
+        }
+      } else {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         if (k0 + 32 * s >= w.d) break;
-        const int G = __builtin_amdgcn_readlane(ga[u], 16 * s);
-        const uint64_t diff = __ballot(ga[u] != G || gb[u] != G);
+        const int G = s == 0 ? G0 : s == 1 ? G1 : s == 2 ? G2 : G3;
         if (!((diff >> (16 * s)) & 0xFFFFu)) {
           const u32x4 m = run_operand<BITS>(run[s]);
           const int gi = min(max(G, 0), ng - 1);
@@ -300,7 +365,8 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
             for (int h = 0; h < 3; ++h) acc[i] = mfma16(x[u][i][s], part[h], acc[i]);
         }
       }
-      const int next = ch + kDecodeWaves * kAhead;
+      }
+      const int next = ch + NW * kAhead;
       if (next < chunks) load_chunk(next, codes[u], x[u], ga[u], gb[u]);
     }
   }
@@ -310,40 +376,45 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(DecodeArgs a,
 #pragma unroll
     for (int v = 0; v < 4; ++v) red[wv][i][4 * q + v][c16] = acc[i][v];
   __syncthreads();
-  for (int e = tid; e < NT * 256; e += kDecodeWaves * 64) {
+#pragma unroll
+  for (int o = 0; o < kOuts; ++o) {
+    const int e = tid + o * NW * 64;
     const int64_t t = tb + (e >> 4), j = j0 + (e & 15);
-    if (t >= a.n || j >= w.m) continue;
+    if (e >= NT * 256 || t >= a.n || j >= w.m) continue;
     float y = 0.0f;
 #pragma unroll
-    for (int v = 0; v < kDecodeWaves; ++v) y += red[v][e >> 8][(e >> 4) & 15][e & 15];
-    const int id = a.row[t];
-    if (id >= 0 && id < a.n_adapters) {
-      const uint16_t* b = a.B + (int64_t(id) * w.m + j) * a.rank;
-      const float* h = a.H + t * a.rank;
-      float s = 0.0f;
-      int p = 0;
-      if (a.rank % 8 == 0 && reinterpret_cast<uintptr_t>(a.B) % 16 == 0)
-        for (; p < a.rank; p += 8) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(b + p);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            s = fmaf(h[p + i], bf16_f32((v[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), s);
-        }
-      for (; p < a.rank; ++p) s = fmaf(h[p], bf16_f32(b[p]), s);
-      y = fmaf(a.alpha[id], s, y);
-    }
+    for (int v = 0; v < NW; ++v) y += red[v][e >> 8][(e >> 4) & 15][e & 15];
+    y += part_y[o];
     if (a.out_bf16) static_cast<uint16_t*>(a.Y)[t * a.ldy + j] = f32_bf16(y);
     else static_cast<float*>(a.Y)[t * a.ldy + j] = y;
   }
 }
 
-template <int BITS>
-void launch_bits(const DecodeArgs& a, bool vx, bool vw, hipStream_t st) {
+template <int BITS, int NT, int NW>
+void launch_waves(const DecodeArgs& a, bool vx, bool vw, bool va, hipStream_t st) {
   const dim3 grid(ceil_div(a.w.m, kDecodeRows), ceil_div(a.n, 64));
   const size_t lds = size_t(a.w.ng) * kDecodeRows * 8;
-  if (a.n <= 16) decode_kernel<BITS, 1><<<grid, kDecodeWaves * 64, lds, st>>>(a, vx, vw);
-  else if (a.n <= 32) decode_kernel<BITS, 2><<<grid, kDecodeWaves * 64, lds, st>>>(a, vx, vw);
-  else decode_kernel<BITS, 4><<<grid, kDecodeWaves * 64, lds, st>>>(a, vx, vw);
+  decode_kernel<BITS, NT, NW><<<grid, NW * 64, lds, st>>>(a, vx, vw, va);
+}
+
+// Waves per workgroup: the more the fewer workgroups there are, so that a CU
+// has about 16 waves' loads in flight and the workgroups run in one round
+// (11008 rows, 16 tokens: 688 workgroups of eight waves took two rounds).
+template <int BITS, int NT>
+void launch_rows(const DecodeArgs& a, bool vx, bool vw, bool va, hipStream_t st) {
+  const int64_t wgs = int64_t(ceil_div(a.w.m, kDecodeRows)) * ceil_div(a.n, 64);
+  const int64_t chunks = (a.w.d + 127) / 128;
+  if constexpr (NT < 4)
+    if (wgs <= 256 && chunks >= 16) return launch_waves<BITS, NT, 16>(a, vx, vw, va, st);
+  if (wgs <= 512 && chunks >= 8) return launch_waves<BITS, NT, 8>(a, vx, vw, va, st);
+  launch_waves<BITS, NT, 4>(a, vx, vw, va, st);
+}
+
+template <int BITS>
+void launch_bits(const DecodeArgs& a, bool vx, bool vw, bool va, hipStream_t st) {
+  if (a.n <= 16) launch_rows<BITS, 1>(a, vx, vw, va, st);
+  else if (a.n <= 32) launch_rows<BITS, 2>(a, vx, vw, va, st);
+  else launch_rows<BITS, 4>(a, vx, vw, va, st);
 }
 
 }  // namespace
@@ -355,20 +426,26 @@ gptq_status launch_lora_decode(const uint16_t* X, int64_t ldx, int64_t n, const 
                                int64_t ldy, hipStream_t st) {
   const bool vx = ldx % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;
   const bool va = w.d % 8 == 0 && reinterpret_cast<uintptr_t>(ad.A) % 16 == 0;
-  const HiddenArgs h{X, ldx, w.d, static_cast<const uint16_t*>(ad.A), ad.row, ad.n_adapters,
-                     ad.rank, H};
-  hidden_kernel<<<dim3(ceil_div(ad.rank, 4), unsigned(n)), 256, 0, st>>>(h, vx, va);
-  GPTQ_CHECK_LAUNCH();
+  // One row of a small adapter: a second launch costs more than forming the
+  // hidden values in every workgroup.
+  const int fused = n == 1 && ad.rank * w.d <= (int64_t(1) << 17);
+  if (!fused) {
+    const HiddenArgs h{X, ldx, w.d, static_cast<const uint16_t*>(ad.A), ad.row, ad.n_adapters,
+                       ad.rank, H};
+    hidden_kernel<<<dim3(ceil_div(ad.rank, 4), unsigned(n)), 256, 0, st>>>(h, vx, va);
+    GPTQ_CHECK_LAUNCH();
+  }
   const int64_t words = (w.d * w.bits + 31) / 32;
   const int bytes = w.bits == 2 ? 8 : w.bits == 3 ? 4 : 16;
   const bool vw = words * 4 % bytes == 0 && reinterpret_cast<uintptr_t>(w.qw) % bytes == 0;
-  const DecodeArgs a{X, ldx, n, w, words, H, static_cast<const uint16_t*>(ad.B), ad.alpha, ad.row,
-                     ad.n_adapters, ad.rank, Y, ldy, out_bf16};
+  const DecodeArgs a{X, ldx, n, w, words, H, static_cast<const uint16_t*>(ad.A),
+                     static_cast<const uint16_t*>(ad.B), ad.alpha, ad.row, ad.n_adapters, ad.rank,
+                     Y, ldy, out_bf16, fused};
   switch (w.bits) {
-    case 2: launch_bits<2>(a, vx, vw, st); break;
-    case 3: launch_bits<3>(a, vx, vw, st); break;
-    case 4: launch_bits<4>(a, vx, vw, st); break;
-    default: launch_bits<8>(a, vx, vw, st); break;
+    case 2: launch_bits<2>(a, vx, vw, va, st); break;
+    case 3: launch_bits<3>(a, vx, vw, va, st); break;
+    case 4: launch_bits<4>(a, vx, vw, va, st); break;
+    default: launch_bits<8>(a, vx, vw, va, st); break;
   }
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;

@@ -47,11 +47,18 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
   if (tid == 0) ident = d % block == 0;
   __syncthreads();
   bool inc = true;
-#pragma unroll 4
-  for (int c = tid; c < d; c += kPlanThreads) {
-    const int g = min(max(g_idx[c], 0), ng - 1);
-    of[c] = static_cast<uint16_t>(g);
-    atomicAdd(&cnt[g], 1);
+  for (int c0 = 0; c0 < d; c0 += 8 * kPlanThreads) {        // eight loads at a time
+    int v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = g_idx[min(c0 + kPlanThreads * i + tid, d - 1)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + kPlanThreads * i + tid;
+      if (c >= d) break;
+      const int g = min(max(v[i], 0), ng - 1);
+      of[c] = static_cast<uint16_t>(g);
+      atomicAdd(&cnt[g], 1);
+    }
   }
   __syncthreads();
   for (int c = tid + 1; c < d; c += kPlanThreads) inc = inc && of[c] >= of[c - 1];
