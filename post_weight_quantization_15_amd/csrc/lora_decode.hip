@@ -23,7 +23,7 @@
 namespace gptq {
 namespace {
 
-constexpr int kDecodeRows = 16;            // output rows per workgroup
+constexpr int kWideFrom = 400;             // workgroups of 16 rows from which 32 are taken
 constexpr int kDecodeMaxGroups = 768;      // 96 KB of grids in LDS
 
 // ---------------------------------------------------------------------------
@@ -160,13 +160,15 @@ __device__ inline void turn4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d)
   d = v[1];
 }
 
+// NJ x 16 output rows a workgroup (the activations' operands serve all of them),
 // NW waves share the input dimension; grid.y: passes of 64 rows.  FUSED (one
 // row): every workgroup forms the hidden values itself, from L2.
-template <int BITS, int NT, int NW>
+template <int BITS, int NT, int NW, int NJ>
 __global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(DecodeArgs a, bool vec_x,
                                                                    bool vec_w, bool vec_a) {
   constexpr int kW = BITS == 8 ? 8 : BITS;      // words of 32 codes
-  extern __shared__ __attribute__((aligned(16))) float grid[];   // [ng][16 rows] (Delta, zz)
+  constexpr int kRows = NJ * 16;
+  extern __shared__ __attribute__((aligned(16))) float grid[];   // [ng][kRows] (Delta, zz)
   __shared__ float red[NW][NT][16][17];
   __shared__ float hid[kMaxRank];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -174,41 +176,46 @@ __global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(Decode
   const int q = lane >> 4, c16 = lane & 15;
   const Packed& w = a.w;
   const int64_t tb = int64_t(blockIdx.y) * 64;
-  const int64_t j0 = int64_t(blockIdx.x) * kDecodeRows;
-  const int64_t jr = min<int64_t>(j0 + c16, w.m - 1);
+  const int64_t j0 = int64_t(blockIdx.x) * kRows;
   const int ng = static_cast<int>(w.ng);
   const int chunks = static_cast<int>((w.d + 127) / 128);
-  const uint32_t* wrow = w.qw + jr * a.words;
+  const uint32_t* wrow[NJ];
+#pragma unroll
+  for (int f = 0; f < NJ; ++f) wrow[f] = w.qw + min<int64_t>(j0 + 16 * f + c16, w.m - 1) * a.words;
 
   // A chunk's codes, activations and group ids.  Chunks are loaded kAhead
   // ahead of their use; whole ones (of aligned rows) in wide loads without
   // a condition among them, the last one of the row piece by piece.
   // Activation rows past n read row n - 1: their sums are not stored.
   constexpr int kAhead = NT == 1 ? 2 : 1;
-  uint32_t codes[kAhead][kW];
+  uint32_t codes[kAhead][NJ][kW];
   u32x4 x[kAhead][NT][4];
   int ga[kAhead], gb[kAhead];              // group ids of columns 2 lane, 2 lane + 1
   const uint16_t* xr[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) xr[i] = a.X + min<int64_t>(tb + 16 * i + c16, a.n - 1) * a.ldx;
   const int whole = vec_x && vec_w ? static_cast<int>(w.d / 128) : 0;
-  auto load_chunk = [&](int ch, uint32_t* cv, u32x4 (*xv)[4], int& g0, int& g1) {
+  auto load_chunk = [&](int ch, uint32_t (*cv)[kW], u32x4 (*xv)[4], int& g0, int& g1) {
     const int64_t k0 = int64_t(ch) * 128;
     const int64_t at = int64_t(ch) * (4 * kW) + q * kW;     // first word of the lane's 32 codes
     if (ch < whole) {
-      if constexpr (BITS == 2) {
-        const uint2 u = *reinterpret_cast<const uint2*>(wrow + at);
-        cv[0] = u.x;
-        cv[1] = u.y;
-      } else if constexpr (BITS == 3) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) cv[i] = wrow[at + i];
-      } else {
+      for (int f = 0; f < NJ; ++f) {
+        const uint32_t* src = wrow[f] + at;
+        if constexpr (BITS == 2) {
+          const uint2 u = *reinterpret_cast<const uint2*>(src);
+          cv[f][0] = u.x;
+          cv[f][1] = u.y;
+        } else if constexpr (BITS == 3) {
 #pragma unroll
-        for (int h = 0; h < kW / 4; ++h) {
-          const u32x4 u = *reinterpret_cast<const u32x4*>(wrow + at + 4 * h);
+          for (int i = 0; i < 3; ++i) cv[f][i] = src[i];
+        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) cv[4 * h + i] = u[i];
+          for (int h = 0; h < kW / 4; ++h) {
+            const u32x4 u = *reinterpret_cast<const u32x4*>(src + 4 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cv[f][4 * h + i] = u[i];
+          }
         }
       }
 #pragma unroll
@@ -220,7 +227,9 @@ __global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(Decode
       g1 = w.g_idx[k0 + 2 * lane + 1];
     } else {
 #pragma unroll
-      for (int i = 0; i < kW; ++i) cv[i] = at + i < a.words ? wrow[at + i] : 0u;
+      for (int f = 0; f < NJ; ++f)
+#pragma unroll
+        for (int i = 0; i < kW; ++i) cv[f][i] = at + i < a.words ? wrow[f][at + i] : 0u;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -247,16 +256,16 @@ __global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(Decode
     }
     __syncthreads();
   }
-  // The adapter's part of the outputs this thread will write (NT = 1: the first
-  // 256 threads one each): its loads ride along with those above.
-  constexpr int kOuts = (NT * 256 + NW * 64 - 1) / (NW * 64);
+  // The adapter's part of the outputs this thread will write (element e: column
+  // e % 16 of fragment e / (256 NT), row e / 16 % (16 NT)): its loads ride along with those above.
+  constexpr int kOuts = (NT * NJ * 256 + NW * 64 - 1) / (NW * 64);
   float part_y[kOuts];
 #pragma unroll
   for (int o = 0; o < kOuts; ++o) {
     const int e = tid + o * NW * 64;
-    const int64_t t = tb + (e >> 4), j = j0 + (e & 15);
+    const int64_t t = tb + (e >> 4) % (16 * NT), j = j0 + 16 * (e / (256 * NT)) + (e & 15);
     part_y[o] = 0.0f;
-    if (e >= NT * 256 || t >= a.n || j >= w.m) continue;
+    if (e >= NT * NJ * 256 || t >= a.n || j >= w.m) continue;
     const int id = a.row[t];
     if (id < 0 || id >= a.n_adapters) continue;
     const uint16_t* b = a.B + (int64_t(id) * w.m + j) * a.rank;
@@ -274,18 +283,20 @@ __global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(Decode
     part_y[o] = a.alpha[id] * s;
   }
   constexpr bool kMagic = BITS != 8;
-  for (int e = tid; e < ng * kDecodeRows; e += NW * 64) {
+  for (int e = tid; e < ng * kRows; e += NW * 64) {
     const int r = e / ng, g = e % ng;
     const int64_t at = min<int64_t>(j0 + r, w.m - 1) * ng + g;
-    grid[(g * kDecodeRows + r) * 2] = step_at(w, at);
-    grid[(g * kDecodeRows + r) * 2 + 1] =
+    grid[(g * kRows + r) * 2] = step_at(w, at);
+    grid[(g * kRows + r) * 2 + 1] =
         w.sgn ? static_cast<float>(1 << (BITS - 1)) : static_cast<float>(w.zeros[at]);
   }
   __syncthreads();
 
-  f32x4 acc[NT];
+  f32x4 acc[NJ][NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int f = 0; f < NJ; ++f)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const u32x4 ones = u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   for (int cb = wv; cb < chunks; cb += NW * kAhead) {
 #pragma unroll
@@ -293,17 +304,20 @@ __global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(Decode
       const int ch = cb + NW * u;
       if (ch >= chunks) break;
       const int64_t k0 = int64_t(ch) * 128;
-      Run<BITS> run[4];
+      Run<BITS> run[NJ][4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) run[s] = run_of<BITS>(codes[u], s);
+      for (int f = 0; f < NJ; ++f) {
 #pragma unroll
-      for (int h = 0; h < (BITS == 8 ? 2 : 1); ++h)
-        turn4(run[0].w[h], run[1].w[h], run[2].w[h], run[3].w[h]);
-      if (w.sgn) {
+        for (int s = 0; s < 4; ++s) run[f][s] = run_of<BITS>(codes[u][f], s);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int h = 0; h < (BITS == 8 ? 2 : 1); ++h)
+          turn4(run[f][0].w[h], run[f][1].w[h], run[f][2].w[h], run[f][3].w[h]);
+        if (w.sgn) {
 #pragma unroll
-          for (int h = 0; h < (BITS == 8 ? 2 : 1); ++h) run[s].w[h] ^= top_bits<BITS>();
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int h = 0; h < (BITS == 8 ? 2 : 1); ++h) run[f][s].w[h] ^= top_bits<BITS>();
+        }
       }
       // The chunk's groups: one, one per step, or steps that mix them.  Decided
       // once a chunk, so that its four steps' chains run side by side.
@@ -313,101 +327,138 @@ __global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(Decode
       const uint64_t diff = __ballot(ga[u] != own || gb[u] != own);
       if (!diff && G0 == G1 && G1 == G2 && G2 == G3) {
         const int gi = min(max(G0, 0), ng - 1);
-        const float dl = grid[(gi * kDecodeRows + c16) * 2];
-        const float zz = grid[(gi * kDecodeRows + c16) * 2 + 1] + (kMagic ? 16.0f : 0.0f);
-        u32x4 m[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) m[s] = run_operand<BITS>(run[s]);
+        // sums of the activations: the same for every fragment of rows
+        f32x4 Xs[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          f32x4 P = f32x4{0.f, 0.f, 0.f, 0.f}, Xs = P;
+          Xs[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            P = mfma16(x[u][i][s], m[s], P);
-            Xs = mfma16(x[u][i][s], ones, Xs);
+          for (int s = 0; s < 4; ++s) Xs[i] = mfma16(x[u][i][s], ones, Xs[i]);
+        }
+#pragma unroll
+        for (int f = 0; f < NJ; ++f) {
+          const float2 gr = *reinterpret_cast<const float2*>(&grid[(gi * kRows + 16 * f + c16) * 2]);
+          const float zz = gr.y + (kMagic ? 16.0f : 0.0f);
+          u32x4 m[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) m[s] = run_operand<BITS>(run[f][s]);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            f32x4 P = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) P = mfma16(x[u][i][s], m[s], P);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              acc[f][i][v] = fmaf(gr.x, fmaf(-zz, Xs[i][v], P[v]), acc[f][i][v]);
           }
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(dl, fmaf(-zz, Xs[v], P[v]), acc[i][v]);
         }
       } else {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (k0 + 32 * s >= w.d) break;
-        const int G = s == 0 ? G0 : s == 1 ? G1 : s == 2 ? G2 : G3;
-        if (!((diff >> (16 * s)) & 0xFFFFu)) {
-          const u32x4 m = run_operand<BITS>(run[s]);
-          const int gi = min(max(G, 0), ng - 1);
-          const float dl = grid[(gi * kDecodeRows + c16) * 2];
-          const float zz = grid[(gi * kDecodeRows + c16) * 2 + 1] + (kMagic ? 16.0f : 0.0f);
+        for (int s = 0; s < 4; ++s) {
+          if (k0 + 32 * s >= w.d) break;
+          const int G = s == 0 ? G0 : s == 1 ? G1 : s == 2 ? G2 : G3;
+          const f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (!((diff >> (16 * s)) & 0xFFFFu)) {
+            const int gi = min(max(G, 0), ng - 1);
+            f32x4 Xs[NT];
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
-            const f32x4 P = mfma16(x[u][i][s], m, z), Xs = mfma16(x[u][i][s], ones, z);
+            for (int i = 0; i < NT; ++i) Xs[i] = mfma16(x[u][i][s], ones, z);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(dl, fmaf(-zz, Xs[v], P[v]), acc[i][v]);
+            for (int f = 0; f < NJ; ++f) {
+              const u32x4 m = run_operand<BITS>(run[f][s]);
+              const float2 gr = *reinterpret_cast<const float2*>(&grid[(gi * kRows + 16 * f + c16) * 2]);
+              const float zz = gr.y + (kMagic ? 16.0f : 0.0f);
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                const f32x4 P = mfma16(x[u][i][s], m, z);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  acc[f][i][v] = fmaf(gr.x, fmaf(-zz, Xs[i][v], P[v]), acc[f][i][v]);
+              }
+            }
+          } else {
+            int g8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int src = 16 * s + 4 * q + (i >> 1);
+              g8[i] = min(max(__shfl(i & 1 ? gb[u] : ga[u], src), 0), ng - 1);
+            }
+#pragma unroll
+            for (int f = 0; f < NJ; ++f) {
+              u32x4 part[3] = {};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 gr =
+                    *reinterpret_cast<const float2*>(&grid[(g8[i] * kRows + 16 * f + c16) * 2]);
+                uint16_t p[3];
+                split3(gr.x * (static_cast<float>(run_code<BITS>(run[f][s], i)) - gr.y), p);
+#pragma unroll
+                for (int h = 0; h < 3; ++h) part[h][i >> 1] |= uint32_t(p[h]) << (16 * (i & 1));
+              }
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int h = 0; h < 3; ++h) acc[f][i] = mfma16(x[u][i][s], part[h], acc[f][i]);
+            }
           }
-        } else {
-          u32x4 part[3] = {};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int src = 16 * s + 4 * q + (i >> 1);
-            const int g = min(max(__shfl(i & 1 ? gb[u] : ga[u], src), 0), ng - 1);
-            const float dl = grid[(g * kDecodeRows + c16) * 2];
-            const float zz = grid[(g * kDecodeRows + c16) * 2 + 1];
-            uint16_t p[3];
-            split3(dl * (static_cast<float>(run_code<BITS>(run[s], i)) - zz), p);
-#pragma unroll
-            for (int h = 0; h < 3; ++h) part[h][i >> 1] |= uint32_t(p[h]) << (16 * (i & 1));
-          }
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int h = 0; h < 3; ++h) acc[i] = mfma16(x[u][i][s], part[h], acc[i]);
         }
-      }
       }
       const int next = ch + NW * kAhead;
       if (next < chunks) load_chunk(next, codes[u], x[u], ga[u], gb[u]);
     }
   }
-  // ---- the waves' shares, in their order, and the adapter's part
+  // ---- the waves' shares, in their order, and the adapter's part; one
+  //      fragment of rows at a time
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int f = 0; f < NJ; ++f) {
+    if (f) __syncthreads();
 #pragma unroll
-    for (int v = 0; v < 4; ++v) red[wv][i][4 * q + v][c16] = acc[i][v];
-  __syncthreads();
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-  for (int o = 0; o < kOuts; ++o) {
-    const int e = tid + o * NW * 64;
-    const int64_t t = tb + (e >> 4), j = j0 + (e & 15);
-    if (e >= NT * 256 || t >= a.n || j >= w.m) continue;
-    float y = 0.0f;
+      for (int v = 0; v < 4; ++v) red[wv][i][4 * q + v][c16] = acc[f][i][v];
+    __syncthreads();
 #pragma unroll
-    for (int v = 0; v < NW; ++v) y += red[v][e >> 8][(e >> 4) & 15][e & 15];
-    y += part_y[o];
-    if (a.out_bf16) static_cast<uint16_t*>(a.Y)[t * a.ldy + j] = f32_bf16(y);
-    else static_cast<float*>(a.Y)[t * a.ldy + j] = y;
+    for (int o = 0; o < kOuts; ++o) {
+      const int e = tid + o * NW * 64;
+      if (e / (256 * NT) != f) continue;
+      const int64_t t = tb + (e >> 4) % (16 * NT), j = j0 + 16 * f + (e & 15);
+      if (t >= a.n || j >= w.m) continue;
+      float y = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NW; ++v) y += red[v][(e >> 8) % NT][(e >> 4) & 15][e & 15];
+      y += part_y[o];
+      if (a.out_bf16) static_cast<uint16_t*>(a.Y)[t * a.ldy + j] = f32_bf16(y);
+      else static_cast<float*>(a.Y)[t * a.ldy + j] = y;
+    }
   }
 }
 
-template <int BITS, int NT, int NW>
+template <int BITS, int NT, int NW, int NJ>
 void launch_waves(const DecodeArgs& a, bool vx, bool vw, bool va, hipStream_t st) {
-  const dim3 grid(ceil_div(a.w.m, kDecodeRows), ceil_div(a.n, 64));
-  const size_t lds = size_t(a.w.ng) * kDecodeRows * 8;
-  decode_kernel<BITS, NT, NW><<<grid, NW * 64, lds, st>>>(a, vx, vw, va);
+  const dim3 grid(ceil_div(a.w.m, 16 * NJ), ceil_div(a.n, 64));
+  const size_t lds = size_t(a.w.ng) * NJ * 16 * 8;
+  decode_kernel<BITS, NT, NW, NJ><<<grid, NW * 64, lds, st>>>(a, vx, vw, va);
 }
 
-// Waves per workgroup: the more the fewer workgroups there are, so that a CU
-// has about 16 waves' loads in flight and the workgroups run in one round
-// (11008 rows, 16 tokens: 688 workgroups of eight waves took two rounds).
+// Workgroups and their waves: about 16 waves a CU, so that their loads keep
+// memory busy; from 33 activation rows on 32 output rows where there are
+// enough of them (each activation operand, by then the larger stream, serves
+// twice the output rows: 128 tokens, 4096 x 4096, 48 -> 33 us; with fewer
+// activation rows the registers cost more than it saves).
 template <int BITS, int NT>
 void launch_rows(const DecodeArgs& a, bool vx, bool vw, bool va, hipStream_t st) {
-  const int64_t wgs = int64_t(ceil_div(a.w.m, kDecodeRows)) * ceil_div(a.n, 64);
+  const int64_t wgs = int64_t(ceil_div(a.w.m, 16)) * ceil_div(a.n, 64);
   const int64_t chunks = (a.w.d + 127) / 128;
+  if constexpr (NT == 4) {
+    if (wgs >= kWideFrom && a.w.ng <= kDecodeMaxGroups / 2) {
+      if (chunks >= 8) return launch_waves<BITS, NT, 8, 2>(a, vx, vw, va, st);
+      return launch_waves<BITS, NT, 4, 2>(a, vx, vw, va, st);
+    }
+  }
   if constexpr (NT < 4)
-    if (wgs <= 256 && chunks >= 16) return launch_waves<BITS, NT, 16>(a, vx, vw, va, st);
-  if (wgs <= 512 && chunks >= 8) return launch_waves<BITS, NT, 8>(a, vx, vw, va, st);
-  launch_waves<BITS, NT, 4>(a, vx, vw, va, st);
+    if (wgs <= 256 && chunks >= 16) return launch_waves<BITS, NT, 16, 1>(a, vx, vw, va, st);
+  if (wgs <= 512 && chunks >= 8) return launch_waves<BITS, NT, 8, 1>(a, vx, vw, va, st);
+  launch_waves<BITS, NT, 4, 1>(a, vx, vw, va, st);
 }
 
 template <int BITS>
