@@ -24,6 +24,18 @@
 // student and teacher agree.  Cells are exponentiated in fp32 and summed in
 // fp32 per thread (at most 128 terms), in fp64 across threads, in a fixed
 // order: results are the same bits from run to run.
+//
+// Bound by memory where workgroups share a CU, so that one's loads and stores
+// run beside another's exponentials: loss and gradient of 4096 bf16 rows of
+// 64000 cells take 218 us, 4.8 TB/s of the 4.9 that a copy reaches.  A row of
+// 128000 takes a CU's whole register file but for what the code needs, so its
+// loads wait for the row before: 499 us, 4.2 TB/s (with every wave at the
+// known ids, a barrier per sum of theirs and a maximum in fp32 it was 696).
+// Few rows are bound by the chain of one row: 14 us for 24 rows of 32000.
+// Loading the next row into registers that the stores free was tried: its
+// registers spill, 2.1 ms.
+#include <type_traits>
+
 #include "common.h"
 
 namespace gptq {
@@ -105,12 +117,16 @@ struct DistillArgs {
   int64_t ldd;
 };
 
-// Sum (or maximum) over the workgroup, the same value in every thread.
-template <int THREADS, class T, class F>
-__device__ inline T block_all(T v, T* red, F f) {
+// Sum (or maximum) over a wave / the workgroup, the same value in every thread.
+template <class T, class F>
+__device__ inline T wave_all(T v, F f) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v = f(v, __shfl_xor(v, o));
-  __syncthreads();                       // red is free
+  return v;
+}
+template <int THREADS, class T, class F>
+__device__ inline T block_all(T v, T* red, F f) {
+  v = wave_all(v, f);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   T r = red[0];
@@ -124,136 +140,116 @@ __device__ inline T sum2(T a, T b) { return a + b; }
 // NaN stays: a row with a NaN cell has a NaN loss
 __device__ inline float fmax_nan(float a, float b) { return (a > b || a != a) ? a : b; }
 
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
 enum { kLoss = 0, kFused = 1, kBackward = 2 };
 
+// fp64 exponential and logarithm, out of line: inlined, their constants are
+// hoisted over the rows into registers that the row's cells need.
+__device__ __attribute__((noinline)) double dexp(double x) { return exp(x); }
+__device__ __attribute__((noinline)) double dlog(double x) { return log(x); }
+
 // NV vectors of 16 bytes per thread held in registers; NV = 0: the row is
-// streamed (and read again for the gradient).
+// streamed (and read again for the gradient).  The first wave alone sees to the
+// known ids, the others wait for it at two barriers only.
 template <int DT, int THREADS, int NV, int MODE>
 __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
   using T = typename Cell<DT>::type;
   using DTag = std::integral_constant<int, DT>;
   constexpr int E = Cell<DT>::kPer;
+  constexpr double kLn2 = 0.693147180559945309417;
   extern __shared__ uint32_t mask[];     // one bit per cell, aligned as the vectors are
   __shared__ double p_s[kMaxK];          // teacher's probability of entry i (0: padding)
   __shared__ float z_s[kMaxK];           // student's logit of entry i
   __shared__ double redd[THREADS / 64];
-  __shared__ float redf[THREADS / 64];
+  __shared__ float redf[THREADS / 64], redg[THREADS / 64];
   __shared__ int dup;
-  const int tid = threadIdx.x;
+  __shared__ double sh_lse, sh_factor;
+  __shared__ float sh_coef, sh_refc;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const bool first = tid < 64;           // the wave of the known ids
+  const int V = static_cast<int>(a.vocab);
+  const bool tail = a.t_lse != nullptr;
+  const float cf = static_cast<float>(a.inv_temp) * kLog2e;
+
+  // A row's body is its whole vectors, 16-byte aligned; the cells before and
+  // after them (fewer than a vector each) are `edge`, one a thread.
+  auto head_of = [&](const T* p) {
+    const int h = static_cast<int>((E - (reinterpret_cast<uintptr_t>(p) / sizeof(T)) % E) % E);
+    return min(h, V);
+  };
+  // the thread's edge cell, -1: none
+  auto edge_of = [&](int head, int nvec) {
+    const int last = head + nvec * E;
+    return tid < head ? tid : tid >= E && tid - E < V - last ? last + tid - E : -1;
+  };
+  auto load_vec = [&](const T* body, int v) { return *reinterpret_cast<const u32x4*>(body + v * E); };
   const int64_t row = blockIdx.x;
   const T* src = static_cast<const T*>(a.logits) + row * a.ldl;
   T* dst = a.dlogits ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
-  const int V = static_cast<int>(a.vocab);
   const int32_t* ids = a.t_idx + row * a.k;
   const float* tl = a.t_logits + row * a.k;
   const float w = a.weight ? a.weight[row] : 1.0f;
-  // vector v covers cells v E - off .. + E - 1, 16-byte aligned in logits
-  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) / sizeof(T)) % E);
-  const int nvec = (V + off + E - 1) / E;
-  // the gradient's row has its vectors at the same places
-  const bool same = dst && (reinterpret_cast<uintptr_t>(dst) / sizeof(T)) % E == unsigned(off);
-
-  auto store_vec = [&](int e0, const u32x4& v) {
-    if (same && e0 >= 0 && e0 + E <= V) {
-      *reinterpret_cast<u32x4*>(dst + e0) = v;
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (e0 + i < 0 || e0 + i >= V) continue;
-        if (DT == GPTQ_F32)
-          reinterpret_cast<uint32_t*>(dst)[e0 + i] = v[i % 4];
-        else
-          reinterpret_cast<uint16_t*>(dst)[e0 + i] =
-              static_cast<uint16_t>(v[(i >> 1) % 4] >> (16 * (i & 1)));
-      }
-    }
-  };
   if (w == 0.0f) {       // a row that does not count: nothing of it is read
     if (MODE != kBackward && tid == 0) {
       a.loss[row] = 0.0f;
       if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
     }
     if (MODE != kLoss)
-      for (int v = tid; v < nvec; v += THREADS) store_vec(v * E - off, u32x4{0u, 0u, 0u, 0u});
+      for (int c = tid; c < V; c += THREADS) dst[c] = T(0);
     return;
   }
-  const bool tail = a.t_lse != nullptr;
-  // ---- the cells, a vector partly outside the row filled with -inf
-  auto load_vec = [&](int e0) {
-    u32x4 v;
-    if (e0 >= 0 && e0 + E <= V) {
-      v = *reinterpret_cast<const u32x4*>(src + e0);
-    } else {
-      constexpr uint32_t f = DT == GPTQ_F32 ? Cell<DT>::kNegInf
-                                            : Cell<DT>::kNegInf | (Cell<DT>::kNegInf << 16);
-      v = u32x4{f, f, f, f};
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (e0 + i >= 0 && e0 + i < V) {
-          const T c = src[e0 + i];
-          uint32_t bits;
-          if (DT == GPTQ_F32) bits = __builtin_bit_cast(uint32_t, static_cast<float>(c));
-          else bits = static_cast<uint32_t>(c);
-          set_bits<DT>(v, i, bits);
-        }
-    }
-    return v;
-  };
+  const int head = head_of(src), nvec = (V - head) / E;
+  const int edge = edge_of(head, nvec);
+  // the gradient's row has its vectors at the same places
+  const bool same = dst && head_of(dst) == head;
   u32x4 cell[NV > 0 ? NV : 1];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = tid + THREADS * i;
-    if (v < nvec) cell[i] = load_vec(v * E - off);
-  }
-  // ---- the teacher's side
-  for (int i = tid; i < (nvec * E + 31) / 32; i += THREADS) mask[i] = 0u;
+  for (int i = 0; i < NV; ++i)
+    if (tid + THREADS * i < nvec) cell[i] = load_vec(src + head, tid + THREADS * i);
+  // ---- the teacher's side (first wave)
+  // mask bits: the body's cells in order, then from `ebase` on the edges'
+  const int ebase = (nvec * E + 31) / 32 * 32;
+  for (int i = tid; i <= ebase / 32; i += THREADS) mask[i] = 0u;
   if (tid == 0) dup = 0;
   __syncthreads();
-  float tm = -INFINITY;
-  for (int i = tid; i < a.k; i += THREADS) {
-    const int32_t id = ids[i];
-    if (id < 0 || id >= V) continue;
-    const unsigned b = unsigned(id + off);
-    if ((atomicOr(&mask[b >> 5], 1u << (b & 31)) >> (b & 31)) & 1u) dup = 1;
-    z_s[i] = cell_to_f32(src[id], DTag());
-    tm = fmax_nan(tm, tl[i]);
+  double t_norm = 0.0, p_sum = 0.0, p_rest = 0.0;
+  if (first) {
+    float tm = -INFINITY;
+    for (int i = lane; i < a.k; i += 64) {
+      const int32_t id = ids[i];
+      if (id < 0 || id >= V) continue;
+      const int in = id - head;
+      const unsigned b = unsigned(in < 0 ? ebase + id : in < nvec * E ? in : ebase + E + in - nvec * E);
+      if ((atomicOr(&mask[b >> 5], 1u << (b & 31)) >> (b & 31)) & 1u) dup = 1;
+      z_s[i] = cell_to_f32(src[id], DTag());
+      tm = fmax_nan(tm, tl[i]);
+    }
+    if (tail) {
+      t_norm = static_cast<double>(a.t_lse[row]);
+    } else {
+      tm = wave_all(tm, fmax_nan);
+      double ts = 0.0;
+      if (tm != -INFINITY)
+        for (int i = lane; i < a.k; i += 64) {
+          const int32_t id = ids[i];
+          if (id < 0 || id >= V) continue;
+          ts += dexp((double(tl[i]) - double(tm)) * a.inv_temp);
+        }
+      ts = wave_all(ts, sum2<double>);
+      t_norm = double(tm) * a.inv_temp + dlog(ts);     // -inf where nothing is known
+    }
+    for (int i = lane; i < a.k; i += 64) {
+      const int32_t id = ids[i];
+      double p = 0.0;
+      if (id >= 0 && id < V && tl[i] != -INFINITY) p = dexp(double(tl[i]) * a.inv_temp - t_norm);
+      p_s[i] = p;
+      p_sum += p;
+    }
+    p_sum = wave_all(p_sum, sum2<double>);
+    if (tail) p_rest = p_sum >= 1.0 ? 0.0 : 1.0 - p_sum;   // NaN stays
   }
-  double t_norm;
-  if (tail) {
-    t_norm = static_cast<double>(a.t_lse[row]);
-    __syncthreads();
-  } else {
-    tm = block_all<THREADS>(tm, redf, fmax_nan);
-    double ts = 0.0;
-    if (tm != -INFINITY)
-      for (int i = tid; i < a.k; i += THREADS) {
-        const int32_t id = ids[i];
-        if (id < 0 || id >= V) continue;
-        ts += exp((double(tl[i]) - double(tm)) * a.inv_temp);
-      }
-    ts = block_all<THREADS>(ts, redd, sum2<double>);
-    t_norm = double(tm) * a.inv_temp + log(ts);     // -inf where nothing is known
-  }
-  // probabilities; entries of one id more than once (dup) count each, and
-  // the first of them stands for the id where the student's mass is summed
-  auto first_of_id = [&](int i) {
-    if (!dup) return true;
-    for (int j = 0; j < i; ++j)
-      if (ids[j] == ids[i]) return false;
-    return true;
-  };
-  double p_sum = 0.0;
-  for (int i = tid; i < a.k; i += THREADS) {
-    const int32_t id = ids[i];
-    double p = 0.0;
-    if (id >= 0 && id < V && tl[i] != -INFINITY) p = exp(double(tl[i]) * a.inv_temp - t_norm);
-    p_s[i] = p;
-    p_sum += p;
-  }
-  p_sum = block_all<THREADS>(p_sum, redd, sum2<double>);
-  double p_rest = 0.0;
-  if (tail) p_rest = p_sum >= 1.0 ? 0.0 : 1.0 - p_sum;   // NaN stays
-  // ---- the student's side
+  if (tail) __syncthreads();           // the mask is whole
   // with a class for the rest, the cells of S leave the registers here
   auto take_out = [&](u32x4& v, int vi) {
     const uint32_t byte = E == 8 ? reinterpret_cast<const uint8_t*>(mask)[vi]
@@ -264,136 +260,222 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
         if ((byte >> i) & 1u) set_bits<DT>(v, i, Cell<DT>::kNegInf);
     }
   };
-  const float cf = static_cast<float>(a.inv_temp) * kLog2e;
-  double lse, lse_rest;
-  float ref = 0.0f;                      // the gradient's exponentials are of (logit - ref) / T
-  if (MODE == kBackward) {
-    lse = double(a.stats[2 * row]);
-    lse_rest = double(a.stats[2 * row + 1]);
-  } else {
-    float mx = -INFINITY;
-    float sum = 0.0f;
+  float ez = edge >= 0 ? cell_to_f32(src[edge], DTag()) : -INFINITY;   // the edge cell
+  if (tail && edge >= 0 && ((mask[ebase / 32] >> tid) & 1u)) ez = -INFINITY;
+  // ---- the student's side: maximum, then sum of 2^(cf z - refc), refc = cf
+  //      max as rounded (its rounding is put back per row, below)
+  float mx = -INFINITY, refc = 0.0f;
+  double sum = 0.0;
+  if (MODE != kBackward) {
+    float part = 0.0f;
     if (NV > 0) {
+      float m = -INFINITY;
+      if (E == 8) {
+        // 16-bit cells order like integers as long as one is positive
+        s16x2 m2 = s16x2{short(0x8000), short(0x8000)};
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = tid + THREADS * i;
-        if (v >= nvec) break;
-        if (tail) take_out(cell[i], v);
+        for (int i = 0; i < NV; ++i) {
+          if (tid + THREADS * i >= nvec) break;
+          if (tail) take_out(cell[i], tid + THREADS * i);
 #pragma unroll
-        for (int e = 0; e < E; ++e) mx = fmax_nan(mx, get_cell<DT>(cell[i], e));
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t word = cell[i][e];
+            m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(s16x2, word));
+          }
+        }
+        const short top = m2[0] > m2[1] ? m2[0] : m2[1];
+        const short own = max(top, static_cast<short>(ez == -INFINITY ? short(0x8000) : short(to_bits<DT>(ez))));
+        m = block_all<THREADS>(static_cast<float>(own), redf, [](float x, float y) { return x > y ? x : y; });
+        if (m >= 0.0f) {
+          mx = cell_to_f32(static_cast<T>(static_cast<int>(m)), DTag());
+        } else {                       // no positive cell (log-probabilities)
+          float neg = ez;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (tid + THREADS * i >= nvec) break;
+#pragma unroll
+            for (int e = 0; e < E; ++e) neg = fmax_nan(neg, get_cell<DT>(cell[i], e));
+          }
+          mx = block_all<THREADS>(neg, redg, fmax_nan);
+        }
+      } else {
+        m = ez;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (tid + THREADS * i >= nvec) break;
+          if (tail) take_out(cell[i], tid + THREADS * i);
+#pragma unroll
+          for (int e = 0; e < E; ++e) m = fmax_nan(m, get_cell<DT>(cell[i], e));
+        }
+        mx = block_all<THREADS>(m, redf, fmax_nan);
       }
-      mx = block_all<THREADS>(mx, redf, fmax_nan);
       // all cells -inf: nothing to exponentiate (the sum stays 0)
       if (mx != -INFINITY) {
+        refc = mx * cf;
+        if (edge >= 0) part = __builtin_amdgcn_exp2f(fmaf(ez, cf, -refc));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           if (tid + THREADS * i >= nvec) break;
 #pragma unroll
           for (int e = 0; e < E; ++e)
-            sum += __builtin_amdgcn_exp2f((get_cell<DT>(cell[i], e) - mx) * cf);
+            part += __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(cell[i], e), cf, -refc));
         }
       }
     } else {
-      float run = -INFINITY;
+      float run = ez;
+      if (run != -INFINITY) part = __builtin_amdgcn_exp2f(fmaf(run, cf, -(run * cf)));
       for (int v = tid; v < nvec; v += THREADS) {
-        u32x4 c = load_vec(v * E - off);
+        u32x4 c = load_vec(src + head, v);
         if (tail) take_out(c, v);
         float m8 = run;
 #pragma unroll
         for (int e = 0; e < E; ++e) m8 = fmax_nan(m8, get_cell<DT>(c, e));
         if (m8 == -INFINITY) continue;
-        if (m8 != run) sum *= __builtin_amdgcn_exp2f((run - m8) * cf);
+        if (m8 != run) part *= __builtin_amdgcn_exp2f(run * cf - m8 * cf);
         run = m8;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          sum += __builtin_amdgcn_exp2f((get_cell<DT>(c, e) - run) * cf);
+          part += __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, e), cf, -(run * cf)));
       }
       mx = block_all<THREADS>(run, redf, fmax_nan);
-      if (run != -INFINITY) sum *= __builtin_amdgcn_exp2f((run - mx) * cf);
+      if (mx != -INFINITY) refc = mx * cf;
+      if (run != -INFINITY) part *= __builtin_amdgcn_exp2f(run * cf - refc);
     }
-    const double s = block_all<THREADS>(double(sum), redd, sum2<double>);
-    if (!tail) {
-      ref = mx;
-      lse = double(mx) * a.inv_temp + log(s);       // NaN for a row without a finite cell
-      lse_rest = lse;
-    } else {
-      lse_rest = mx == -INFINITY ? -INFINITY : double(mx) * a.inv_temp + log(s);
-      ref = mx == -INFINITY ? 0.0f : mx;
-      // the known ids' share, on the larger of the two maxima
-      float ms = mx;
-      for (int i = tid; i < a.k; i += THREADS) {
-        const int32_t id = ids[i];
-        if (id >= 0 && id < V) ms = fmax_nan(ms, z_s[i]);
-      }
-      const float top = block_all<THREADS>(ms, redf, fmax_nan);
-      double ss = 0.0;
-      for (int i = tid; i < a.k; i += THREADS) {
-        const int32_t id = ids[i];
-        if (id >= 0 && id < V && first_of_id(i)) ss += exp((double(z_s[i]) - double(top)) * a.inv_temp);
-      }
-      ss = block_all<THREADS>(ss, redd, sum2<double>);
-      if (mx != -INFINITY) ss += s * exp((double(mx) - double(top)) * a.inv_temp);
-      lse = double(top) * a.inv_temp + log(ss);
-    }
+    sum = block_all<THREADS>(double(part), redd, sum2<double>);
   }
-  const bool use_rest = tail && !(p_rest <= 0.0) && lse_rest != -INFINITY;
-  if (MODE != kBackward) {
-    double t = 0.0;
-    for (int i = tid; i < a.k; i += THREADS) {
-      const double p = p_s[i];
-      if (p != 0.0)
-        t += p * ((double(tl[i]) * a.inv_temp - t_norm) - (double(z_s[i]) * a.inv_temp - lse));
-    }
-    t = block_all<THREADS>(t, redd, sum2<double>);
-    if (use_rest) t += p_rest * (log(p_rest) - (lse_rest - lse));
-    if (tid == 0) {
-      a.loss[row] = static_cast<float>(double(w) * a.temp * a.temp * t);
-      if (a.stats) {
-        a.stats[2 * row] = static_cast<float>(lse);
-        a.stats[2 * row + 1] = static_cast<float>(lse_rest);
+  // ---- per row, first wave: log-sum-exps, loss, the gradient's factors
+  if (first) {
+    double lse, lse_rest;
+    if (MODE == kBackward) {
+      lse = double(a.stats[2 * row]);
+      lse_rest = double(a.stats[2 * row + 1]);
+    } else {
+      // log of the cells' sum; refc stands for cf mx up to its rounding
+      lse_rest = mx == -INFINITY ? -INFINITY
+                                 : double(mx) * a.inv_temp + dlog(sum) -
+                                       (double(mx) * double(cf) - double(refc)) * kLn2;
+      lse = lse_rest;                  // NaN below for a row without a finite cell
+      if (!tail) {
+        if (mx == -INFINITY) lse = lse_rest = NAN;
+      } else {
+        // the known ids' share, on the larger of the two maxima
+        float ms = mx;
+        for (int i = lane; i < a.k; i += 64) {
+          const int32_t id = ids[i];
+          if (id >= 0 && id < V) ms = fmax_nan(ms, z_s[i]);
+        }
+        const float top = wave_all(ms, fmax_nan);
+        double ss = 0.0;
+        for (int i = lane; i < a.k; i += 64) {
+          const int32_t id = ids[i];
+          if (id < 0 || id >= V) continue;
+          bool one = true;             // an id named twice has its mass once
+          if (dup)
+            for (int j = 0; j < i; ++j) one = one && ids[j] != id;
+          if (one) ss += dexp((double(z_s[i]) - double(top)) * a.inv_temp);
+        }
+        ss = wave_all(ss, sum2<double>);
+        if (mx != -INFINITY) ss += dexp(lse_rest - double(top) * a.inv_temp);
+        lse = double(top) * a.inv_temp + dlog(ss);
       }
+    }
+    const bool use_rest = tail && !(p_rest <= 0.0) && lse_rest != -INFINITY;
+    if (MODE != kBackward) {
+      double t = 0.0;
+      for (int i = lane; i < a.k; i += 64) {
+        const double p = p_s[i];
+        if (p != 0.0)
+          t += p * ((double(tl[i]) * a.inv_temp - t_norm) - (double(z_s[i]) * a.inv_temp - lse));
+      }
+      t = wave_all(t, sum2<double>);
+      if (use_rest) t += p_rest * (dlog(p_rest) - (lse_rest - lse));
+      // a row that knows nothing of the teacher has no loss, whatever it holds
+      if (!tail && p_sum == 0.0) t = 0.0;
+      if (lane == 0) {
+        a.loss[row] = static_cast<float>(double(w) * a.temp * a.temp * t);
+        if (a.stats) {
+          a.stats[2 * row] = static_cast<float>(lse);
+          a.stats[2 * row + 1] = static_cast<float>(lse_rest);
+        }
+      }
+    }
+    if (MODE != kLoss && lane == 0) {
+      // A cell outside S: q_v (1 - p_r / q_r) = dexp(z_v - lse_rest) (q_r - p_r):
+      // no factor overflows where q_r is tiny.  A row that knows nothing of
+      // the teacher has no gradient, as no loss.
+      const double factor = (!tail && p_sum == 0.0)
+                                ? 0.0
+                                : double(w) * a.temp * (MODE == kBackward ? double(a.grad[row]) : 1.0);
+      const double base = tail ? lse_rest : lse;      // the log-sum-exp of those cells
+      double coef = 0.0;
+      float rc = refc;
+      if (base != -INFINITY) {
+        coef = factor * (dexp(base - lse) - (use_rest ? p_rest : 0.0));
+        if (MODE == kBackward) {
+          rc = static_cast<float>(base / kLn2);
+          coef *= exp2(double(rc) - base / kLn2);
+        } else {
+          coef /= sum;
+        }
+      }
+      sh_coef = static_cast<float>(coef);
+      sh_refc = base == -INFINITY ? 0.0f : rc;
+      sh_lse = lse;
+      sh_factor = factor;
     }
   }
   if (MODE == kLoss) return;
-  // ---- the gradient: first every cell as one outside S, q_v (1 - p_r / q_r)
-  // = exp(z_v - lse_rest) (q_r - p_r): no factor overflows where q_r is tiny.
-  // A row that knows nothing of the teacher has no gradient, as no loss.
-  const double factor = (!tail && !(p_sum > 0.0) && p_sum == p_sum)
-                            ? 0.0
-                            : double(w) * a.temp * (MODE == kBackward ? double(a.grad[row]) : 1.0);
-  const double base = tail ? lse_rest : lse;      // the log-sum-exp that ref goes with
-  double coef_d = 0.0;
-  if (base != -INFINITY) {
-    coef_d = factor * (exp(base - lse) - (use_rest ? p_rest : 0.0));
-    if (MODE != kBackward) coef_d *= exp(double(ref) * a.inv_temp - base);
-  }
-  const float coef = static_cast<float>(coef_d);
-  const float base_f = base == -INFINITY ? 0.0f : static_cast<float>(base);
-  const float it = static_cast<float>(a.inv_temp);
+  __syncthreads();
+  // ---- the gradient: first every cell as one outside S ...
+  const float coef = sh_coef, rc = sh_refc;
   auto grad_vec = [&](const u32x4& c) {
-    u32x4 g = u32x4{0u, 0u, 0u, 0u};
+    u32x4 g;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float z = get_cell<DT>(c, e);
-      const float x = MODE == kBackward ? fmaf(z, it, -base_f) * kLog2e : (z - ref) * cf;
-      const uint32_t b = to_bits<DT>(coef * __builtin_amdgcn_exp2f(x));
-      if (DT == GPTQ_F32) g[e % 4] = b;
-      else g[(e >> 1) % 4] |= b << (16 * (e & 1));
+    for (int e = 0; e < 4; ++e) {
+      if (DT == GPTQ_F32) {
+        g[e] = to_bits<DT>(coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, e), cf, -rc)));
+      } else {
+        const uint32_t lo = to_bits<DT>(
+            coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, (2 * e) % E), cf, -rc)));
+        const uint32_t hi = to_bits<DT>(
+            coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, (2 * e + 1) % E), cf, -rc)));
+        g[e] = lo | (hi << 16);
+      }
     }
     return g;
   };
-  if (NV > 0) {
+  if (edge >= 0) {
+    const uint32_t b = to_bits<DT>(
+        coef * __builtin_amdgcn_exp2f(fmaf(cell_to_f32(src[edge], DTag()), cf, -rc)));
+    if (DT == GPTQ_F32) reinterpret_cast<uint32_t*>(dst)[edge] = b;
+    else reinterpret_cast<uint16_t*>(dst)[edge] = static_cast<uint16_t>(b);
+  }
+  if (NV > 0 && same) {
+    u32x4* out = reinterpret_cast<u32x4*>(dst + head);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + THREADS * i;
-      if (v >= nvec) break;
-      store_vec(v * E - off, grad_vec(cell[i]));
+      if (v < nvec) out[v] = grad_vec(cell[i]);
     }
-  } else {
-    for (int v = tid; v < nvec; v += THREADS) store_vec(v * E - off, grad_vec(load_vec(v * E - off)));
+  } else {                             // streamed, or the gradient lies otherwise: read again
+    for (int v = tid; v < nvec; v += THREADS) {
+      const u32x4 g = grad_vec(load_vec(src + head, v));
+      if (same) {
+        *reinterpret_cast<u32x4*>(dst + head + v * E) = g;
+      } else {
+        for (int e = 0; e < E; ++e) {
+          if (DT == GPTQ_F32)
+            reinterpret_cast<uint32_t*>(dst)[head + v * E + e] = g[e % 4];
+          else
+            reinterpret_cast<uint16_t*>(dst)[head + v * E + e] =
+                static_cast<uint16_t>(g[(e >> 1) % 4] >> (16 * (e & 1)));
+        }
+      }
+    }
   }
   // ... then the cells of S over it (entries of one id write the same value)
   __syncthreads();
+  const double lse = sh_lse, factor = sh_factor;
   for (int i = tid; i < a.k; i += THREADS) {
     const int32_t id = ids[i];
     if (id < 0 || id >= V) continue;
@@ -403,7 +485,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
       for (int j = 0; j < a.k; ++j)
         if (ids[j] == id) p += p_s[j];
     }
-    const double g = factor * (exp(double(z_s[i]) * a.inv_temp - lse) - p);
+    const double g = factor * (dexp(double(z_s[i]) * a.inv_temp - lse) - p);
     const uint32_t b = to_bits<DT>(static_cast<float>(g));
     if (DT == GPTQ_F32) reinterpret_cast<uint32_t*>(dst)[id] = b;
     else reinterpret_cast<uint16_t*>(dst)[id] = static_cast<uint16_t>(b);
@@ -414,16 +496,20 @@ template <int DT, int MODE>
 gptq_status launch_mode(const DistillArgs& a, int64_t n, hipStream_t st) {
   constexpr int E = Cell<DT>::kPer;
   const int64_t nvec = (a.vocab + 2 * (E - 1)) / E;            // the most a row can take
-  const size_t lds = size_t((nvec * E + 31) / 32) * 4;
-  const unsigned grid = static_cast<unsigned>(n);
+  const size_t lds = (size_t((nvec * E + 31) / 32) + 2) * 4;
+  // A row takes the fewest threads that hold it, so that several rows share a
+  // CU; where every row has a CU to itself it takes more of them.  32000 bf16
+  // cells: 4096 rows 122 us by 256 threads, 211 by 1024; 256 rows 18.8 and 16.2.
 #define GPTQ_DISTILL(TH, NVV) \
-  distill_kernel<DT, TH, NVV, MODE><<<grid, TH, lds, st>>>(a)
+  distill_kernel<DT, TH, NVV, MODE><<<unsigned(n), TH, lds, st>>>(a)
   if (nvec <= 256 * 4)
     GPTQ_DISTILL(256, 4);
-  else if (nvec <= 1024 * 4)
+  else if (nvec <= 1024 * 4 && n <= 256)
     GPTQ_DISTILL(1024, 4);
+  else if (nvec <= 256 * 16)
+    GPTQ_DISTILL(256, 16);
   else if (nvec <= 1024 * 8)
-    GPTQ_DISTILL(1024, 8);
+    GPTQ_DISTILL(512, 16);
   else if (nvec <= 1024 * 16)
     GPTQ_DISTILL(1024, 16);
   else

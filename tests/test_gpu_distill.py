@@ -286,3 +286,44 @@ def test_gradient_is_the_loss_s_difference(dev):
     real = ((up.double() - down.double()) / 2 * grad).sum(1)
     # two log-sum-exps (all cells, the rest): (1 + 1) 2 s^3 / 6 each side
     assert float(((a - b) / 2 - real).abs().max()) <= 4 * (1 / 8) ** 3 / 6 + 1e-4
+
+
+@pytest.mark.parametrize("case", [(300, 9000, torch.bfloat16), (300, 4100, torch.float32),
+                                  (257, 30001, torch.float16), (2, 40000, torch.bfloat16),
+                                  (3, 20003, torch.float32)],
+                         ids=lambda c: "n%d_V%d_%s" % (c[0], c[1], str(c[2])[6:]))
+def test_many_and_middling_rows(dev, case):
+    """Rows that share a CU, and those of the length between."""
+    n, vocab, dtype = case
+    z, idx, t, t_lse, w = inputs(n, vocab, 5, dtype, 1.0, True, seed=13)
+    w[n // 2] = 0.0
+    check(dev, z, idx, t, t_lse, w, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("vocab", [900, 9000, 140001])
+def test_log_probabilities_as_logits(dev, dtype, vocab):
+    """No cell above 0, some at 0 or -0: the maximum is taken all the same."""
+    z, idx, t, t_lse, w = inputs(4, vocab, 7, dtype, 1.0, True, seed=14)
+    z = (z.double() - torch.logsumexp(z.double(), 1, keepdim=True)).to(dtype)
+    z[1, 11] = -0.0
+    z[2, 5] = 0.0
+    z[2, 6] = -0.0
+    z[3, 1::2] = -float("inf")
+    idx[3] = idx[3] // 2 * 2
+    idx[3] = np.where(np.isin(np.arange(7), np.unique(idx[3], return_index=True)[1]), idx[3], -1)
+    check(dev, z, idx, t, t_lse, w, 1.0)
+
+
+@pytest.mark.parametrize("shift", [1, 3])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_at_another_alignment(dev, shift, dtype):
+    z, idx, t, t_lse, w = inputs(3, 5003, 7, dtype, 1.0, True, seed=15)
+    ix, tt, tl = to(dev, idx), to(dev, t), to(dev, t_lse)
+    want = gq.gptq_distill_loss(z.to(dev), ix, tt, t_lse=tl, want_grad=True)
+    wide = torch.full((4, 5003 + 9), 3.0, dtype=dtype, device=dev)
+    out = wide[:3, shift:shift + 5003]
+    got = gq.gptq_distill_loss(z.to(dev), ix, tt, t_lse=tl, dlogits=out)
+    assert torch.equal(out, want["dlogits"]) and torch.equal(got["loss"], want["loss"])
+    out.zero_()
+    assert float(wide.double().sum()) == 3.0 * (5003 + 9 + 3 * 9)

@@ -457,3 +457,25 @@ def test_bits_of_the_shared_product_alone(dev):
         bound = 2 * (544 + 16) * U * (np.abs(c["X"].cpu().double().numpy()) @ lay.mag.T)
         near(Y, Yd.cpu().double().numpy(), bound, "Y")
         assert not H.any()
+
+
+@pytest.mark.parametrize("case", [
+    (100, 3300, 300, 4, 128, "natural", 7, 16, "random"),    # several passes over the rows,
+    (192, 2200, 1100, 3, 64, "act", 5, 8, "runs"),           # wide passes, short and long sums
+    (129, 6500, 136, 2, -1, "natural", 2, 4, "each"),
+    (70, 50, 2100, 8, 128, "any", 3, 20, "each"),
+    (20, 90, 1602, 4, 2, "natural", 3, 8, "each"),           # more groups than fit beside the rows
+    (3, 40, 1999, 4, 1, "natural", 2, 8, "each"),
+    (90, 3300, 900, 4, 2, "act", 3, 8, "random"),
+    (5, 6, 60000, 4, 128, "act", 2, 16, "each"),             # long rows
+    (200, 70, 60000, 4, 128, "act", 2, 16, "random"),
+], ids=lambda c: "n%d_m%d_d%d_b%d_g%d_%s_L%d_r%d_%s" % c)
+def test_lora_passes_groups_and_long_rows(dev, case):
+    n, m, d, bits, group, order, L, r, kind = case
+    check_lora(dev, Layer(m, d, bits, group, order), n, L, r, kind)
+
+
+@pytest.mark.parametrize("n", [1, 3, 40, 250])
+def test_lora_gradients_of_long_rows(dev, n):
+    check_backward(dev, Layer(70, 40000, 4, 128, "act"), n, 2, 16, "each")
+    check_backward(dev, Layer(9000, 72, 4, 64), n, 2, 16, "each")
