@@ -24,6 +24,7 @@ namespace gptq {
 namespace {
 
 constexpr int kWideFrom = 400;             // workgroups of 16 rows from which 32 are taken
+constexpr int kWiderFrom = 512;            // ... and 64, up to 32 activation rows
 constexpr int kDecodeMaxGroups = 768;      // 96 KB of grids in LDS
 
 // ---------------------------------------------------------------------------
@@ -164,7 +165,7 @@ __device__ inline void turn4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d)
 // NW waves share the input dimension; grid.y: passes of 64 rows.  FUSED (one
 // row): every workgroup forms the hidden values itself, from L2.
 template <int BITS, int NT, int NW, int NJ>
-__global__ __launch_bounds__(NW * 64, NT == 4 ? 2 : 4) void decode_kernel(DecodeArgs a, bool vec_x,
+__global__ __launch_bounds__(NW * 64, NT == 4 || NJ > 1 ? 2 : 4) void decode_kernel(DecodeArgs a, bool vec_x,
                                                                    bool vec_w, bool vec_a) {
   constexpr int kW = BITS == 8 ? 8 : BITS;      // words of 32 codes
   constexpr int kRows = NJ * 16;
@@ -441,10 +442,13 @@ void launch_waves(const DecodeArgs& a, bool vx, bool vw, bool va, hipStream_t st
 }
 
 // Workgroups and their waves: about 16 waves a CU, so that their loads keep
-// memory busy; from 33 activation rows on 32 output rows where there are
-// enough of them (each activation operand, by then the larger stream, serves
-// twice the output rows: 128 tokens, 4096 x 4096, 48 -> 33 us; with fewer
-// activation rows the registers cost more than it saves).
+// memory busy.  The activations are read once a workgroup, and from some 9
+// rows on that stream is the larger one, so where there are enough output rows
+// a workgroup takes 64 of them (32 from 33 activation rows on, whose operands
+// fill the registers): 14336 x 4096, 16 tokens 28.1 -> 22.5 us, 32 tokens 44.6
+// -> 29.6; 28672 x 8192, 16 tokens 81 -> 54; 4096 x 4096, 128 tokens 48 -> 33.
+// With fewer rows the registers cost more than it saves (14336 x 4096, 4
+// tokens 20.4 by 16 output rows, 19.8 by 64; 11008 x 4096 16.7 and 19.4).
 template <int BITS, int NT>
 void launch_rows(const DecodeArgs& a, bool vx, bool vw, bool va, hipStream_t st) {
   const int64_t wgs = int64_t(ceil_div(a.w.m, 16)) * ceil_div(a.n, 64);
@@ -455,6 +459,11 @@ void launch_rows(const DecodeArgs& a, bool vx, bool vw, bool va, hipStream_t st)
       return launch_waves<BITS, NT, 4, 2>(a, vx, vw, va, st);
     }
   }
+  if constexpr (NT <= 2 && BITS != 8)        // 8-bit codes' registers would spill
+    if (a.n > 8 && wgs >= kWiderFrom && a.w.ng <= kDecodeMaxGroups / 4) {
+      if (chunks >= 8 && wgs <= 1024) return launch_waves<BITS, NT, 8, 4>(a, vx, vw, va, st);
+      return launch_waves<BITS, NT, 4, 4>(a, vx, vw, va, st);
+    }
   if constexpr (NT < 4)
     if (wgs <= 256 && chunks >= 16) return launch_waves<BITS, NT, 16, 1>(a, vx, vw, va, st);
   if (wgs <= 512 && chunks >= 8) return launch_waves<BITS, NT, 8, 1>(a, vx, vw, va, st);
@@ -478,8 +487,9 @@ gptq_status launch_lora_decode(const uint16_t* X, int64_t ldx, int64_t n, const 
   const bool vx = ldx % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;
   const bool va = w.d % 8 == 0 && reinterpret_cast<uintptr_t>(ad.A) % 16 == 0;
   // One row of a small adapter: a second launch costs more than forming the
-  // hidden values in every workgroup.
-  const int fused = n == 1 && ad.rank * w.d <= (int64_t(1) << 17);
+  // hidden values in every workgroup, unless there are many (rank 16, 4096 x
+  // 4096: 14.5 us and 15.8; 14336 x 4096: 24 and 17; 28672 x 8192: 79 and 50).
+  const int fused = n == 1 && w.m <= 8192 && ad.rank * w.d <= (int64_t(1) << 17);
   if (!fused) {
     const HiddenArgs h{X, ldx, w.d, static_cast<const uint16_t*>(ad.A), ad.row, ad.n_adapters,
                        ad.rank, H};

@@ -467,6 +467,11 @@ def test_bits_of_the_shared_product_alone(dev):
     (20, 90, 1602, 4, 2, "natural", 3, 8, "each"),           # more groups than fit beside the rows
     (3, 40, 1999, 4, 1, "natural", 2, 8, "each"),
     (90, 3300, 900, 4, 2, "act", 3, 8, "random"),
+    (12, 8210, 1100, 4, 128, "natural", 12, 16, "each"),     # wide layers, few rows
+    (31, 8200, 1300, 3, 128, "act", 3, 5, "random"),
+    (32, 16500, 264, 2, 64, "natural", 2, 8, "each"),
+    (20, 8200, 520, 8, 128, "natural", 2, 8, "each"),
+    (1, 8300, 168, 4, 64, "natural", 2, 16, "one"),
     (5, 6, 60000, 4, 128, "act", 2, 16, "each"),             # long rows
     (200, 70, 60000, 4, 128, "act", 2, 16, "random"),
 ], ids=lambda c: "n%d_m%d_d%d_b%d_g%d_%s_L%d_r%d_%s" % c)
