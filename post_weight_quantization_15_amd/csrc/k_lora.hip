@@ -184,8 +184,11 @@ int shrink_shares(int64_t n, int64_t len) {
 gptq_status launch_shrink(const ShrinkArgs& a, hipStream_t st) {
   const bool vv = a.ldv % 8 == 0 && reinterpret_cast<uintptr_t>(a.V) % 16 == 0;
   const bool vm = a.ldm % 8 == 0 && reinterpret_cast<uintptr_t>(a.M) % 16 == 0;
-  // up to 64 MB of V and M rows in all, mostly from L2
-  if (a.n <= 65535 && a.n * a.rank * a.len <= (int64_t(32) << 20)) {
+  // one wave a value (some 700 elements' time besides the sum's own) while that
+  // takes no longer than the tiles' 12 us; elements loaded one by one take four
+  // times as long: 4096 rows of 512, rank 16: 25 us and 7 by tiles; 203 rows of
+  // 11008, rank 8: 12 us and 24
+  if (a.n <= 65535 && a.n * a.rank * (a.len + 700) * (vv && vm ? 1 : 4) <= (int64_t(40) << 20)) {
     values_kernel<<<dim3(a.rp / 4, unsigned(a.n)), 256, 0, st>>>(a, vv && vm);
     GPTQ_CHECK_LAUNCH();
     return GPTQ_OK;

@@ -722,12 +722,35 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void gemm_kernel(GemmArgs a, unsig
   // ---- the adapters' part: per adapter among the wave's rows one small
   //      product, added to the rows of that adapter alone
   if (LORA) {
+    int ids[kFi];                              // every row's adapter: one wait for all
 #pragma unroll
     for (int i = 0; i < kFi; ++i) {
       const int64_t t = tb + wi + 16 * i + c16;
-      const int id = t < a.n ? a.row[t] : -1;
+      ids[i] = t < a.n ? a.row[t] : -1;
+    }
+    auto part_of = [&](int i) {
+      int row = wi + 16 * i;                   // opaque: no addresses ahead of their use
+      asm volatile("" : "+s"(row));
+      return a.parts + min<int64_t>(tb + row + c16, a.n - 1) * 3 * a.rp + 8 * q;
+    };
+    // the hidden values of the next 16 rows are loaded beside the product of
+    // these, an adapter's factors once for rows that follow each other
+    u32x4 fn[3], fm[kFj];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) fn[p] = *reinterpret_cast<const u32x4*>(part_of(0) + p * a.rp);
+    int held = -1;
+#pragma unroll
+    for (int i = 0; i < kFi; ++i) {
+      const int id = ids[i];
+      u32x4 f0[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) f0[p] = fn[p];
+      if (i + 1 < kFi) {
+        const uint16_t* next = part_of(i + 1);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) fn[p] = *reinterpret_cast<const u32x4*>(next + p * a.rp);
+      }
       uint32_t left = static_cast<uint32_t>(__ballot(id >= 0 && id < a.n_adapters)) & 0xFFFFu;
-      const uint16_t* part = a.parts + min<int64_t>(t, a.n - 1) * 3 * a.rp + 8 * q;
       while (left) {
         const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
         const bool mine = id == ad;
@@ -739,14 +762,26 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void gemm_kernel(GemmArgs a, unsig
         for (int b = 0; b < a.rp; b += 32) {
           u32x4 fa[3];
 #pragma unroll
-          for (int p = 0; p < 3; ++p) fa[p] = *reinterpret_cast<const u32x4*>(part + p * a.rp + b);
+          for (int p = 0; p < 3; ++p) fa[p] = f0[p];
+          if (b) {
+            const uint16_t* part = part_of(i) + b;
 #pragma unroll
-          for (int j = 0; j < kFj; ++j) {
-            const int64_t r = min<int64_t>(jb + wj + 16 * j + c16, a.m - 1);
-            const u32x4 fm = load8(Lm + r * a.rank, b + 8 * q, a.rank, vec_l);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) D[j] = mfma16(fm, fa[p], D[j]);
+            for (int p = 0; p < 3; ++p) fa[p] = *reinterpret_cast<const u32x4*>(part + p * a.rp);
           }
+          if (ad != held || a.rp > 32) {
+            int col = wj;
+            asm volatile("" : "+s"(col));
+#pragma unroll
+            for (int j = 0; j < kFj; ++j) {
+              const int64_t r = min<int64_t>(jb + col + 16 * j + c16, a.m - 1);
+              fm[j] = load8(Lm + r * a.rank, b + 8 * q, a.rank, vec_l);
+            }
+            held = ad;
+          }
+#pragma unroll
+          for (int j = 0; j < kFj; ++j)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) D[j] = mfma16(fm[j], fa[p], D[j]);
         }
 #pragma unroll
         for (int j = 0; j < kFj; ++j)
@@ -756,38 +791,60 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void gemm_kernel(GemmArgs a, unsig
       }
     }
   }
-  // ---- results
+  // ---- results, turned through LDS 16 rows at a time: a lane holds 4 columns
+  //      of a row, 4 lanes a row; stored from there, each of a wave's stores
+  //      would open 16 rows for 32 bytes each
+  constexpr int kCols = TN / WN, kPitch = kCols + 4;
+  constexpr int kTurn = KS > 1 ? (KS - 1) * kWaves * kFi * kFj * 1024 : 0;   // behind the sums
+  static_assert(kTurn + kWaves * 16 * kPitch * 4 <= KS * kRing, "the turned rows fit the rings");
+  if (KS == 1) __syncthreads();                // the last stage is read
+  float* out = reinterpret_cast<float*>(lds_all + kTurn) + wv * (16 * kPitch);
+  const int64_t r0 = jb + wj;
+  const bool wide = vec_y && r0 + kCols <= a.m;
 #pragma unroll
   for (int i = 0; i < kFi; ++i) {
-    const int64_t t = tb + wi + 16 * i + c16;
-    asm volatile("" ::: "memory");           // one row of fragments' addresses at a time
-    if (t >= a.n) continue;
 #pragma unroll
-    for (int j = 0; j < kFj; ++j) {
-      const int64_t r = jb + wj + 16 * j + 4 * q;
-      const f32x4 v = acc[i][j];
-      if (a.out_bf16) {
-        uint16_t* y = static_cast<uint16_t*>(a.Y) + t * a.ldy + r;
-        const uint32_t lo = uint32_t(f32_bf16(v[0])) | (uint32_t(f32_bf16(v[1])) << 16);
-        const uint32_t hi = uint32_t(f32_bf16(v[2])) | (uint32_t(f32_bf16(v[3])) << 16);
-        if (vec_y && r + 4 <= a.m) {
-          *reinterpret_cast<uint2*>(y) = uint2{lo, hi};
-        } else {
+    for (int j = 0; j < kFj; ++j)
+      *reinterpret_cast<f32x4*>(out + c16 * kPitch + 16 * j + 4 * q) = acc[i][j];
+    int row = wi + 16 * i;                     // opaque: these rows' addresses only now
+    asm volatile("s_waitcnt lgkmcnt(0)" : "+s"(row)::"memory");
+    const int64_t t0 = tb + row;
+    if (wide && a.out_bf16) {
+      constexpr int kPer = kCols / 8;          // lanes a row
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (r + e < a.m) y[e] = static_cast<uint16_t>((e < 2 ? lo : hi) >> (16 * (e & 1)));
+      for (int r = lane / kPer; r < 16; r += 64 / kPer) {
+        const int c = 8 * (lane % kPer);
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(out + r * kPitch + c);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(out + r * kPitch + c + 4);
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          v[e] = uint32_t(f32_bf16(lo[2 * e])) | (uint32_t(f32_bf16(lo[2 * e + 1])) << 16);
+          v[e + 2] = uint32_t(f32_bf16(hi[2 * e])) | (uint32_t(f32_bf16(hi[2 * e + 1])) << 16);
         }
-      } else {
-        float* y = static_cast<float*>(a.Y) + t * a.ldy + r;
-        if (vec_y && r + 4 <= a.m) {
-          *reinterpret_cast<f32x4*>(y) = v;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (r + e < a.m) y[e] = v[e];
-        }
+        if (t0 + r < a.n)
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.Y) + (t0 + r) * a.ldy + r0 + c) = v;
       }
+    } else if (wide) {
+      constexpr int kPer = kCols / 4;
+#pragma unroll
+      for (int r = lane / kPer; r < 16; r += 64 / kPer) {
+        const int c = 4 * (lane % kPer);
+        const f32x4 v = *reinterpret_cast<const f32x4*>(out + r * kPitch + c);
+        if (t0 + r < a.n)
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.Y) + (t0 + r) * a.ldy + r0 + c) = v;
+      }
+    } else {
+      const int c = lane % kCols;
+      if (r0 + c < a.m)
+        for (int r = lane / kCols; r < 16 && t0 + r < a.n; r += 64 / kCols) {
+          const float v = out[r * kPitch + c];
+          const int64_t at = (t0 + r) * a.ldy + r0 + c;
+          if (a.out_bf16) static_cast<uint16_t*>(a.Y)[at] = f32_bf16(v);
+          else static_cast<float*>(a.Y)[at] = v;
+        }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next rows' writes
   }
 }
 
@@ -799,7 +856,7 @@ gptq_status launch_tile(const GemmArgs& a, hipStream_t st) {
   const unsigned tj = ceil_div(a.m, TN);
   const unsigned tiles = tj * ceil_div(a.n, TM);
   const int item = a.out_bf16 ? 2 : 4;
-  const int vec_y = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.Y) % (4 * item) == 0;
+  const int vec_y = a.ldy * item % 16 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
   const int vec_l = a.L && a.rank % 8 == 0 && reinterpret_cast<uintptr_t>(a.L) % 16 == 0;
   gemm_kernel<TM, TN, WM, WN, KS, S, FOLD, LORA><<<tiles, WM * WN * KS * 64, lds, st>>>(a, tj, tiles, vec_y, vec_l);
   GPTQ_CHECK_LAUNCH();
