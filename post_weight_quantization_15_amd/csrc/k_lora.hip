@@ -24,7 +24,8 @@ namespace {
 // sums meet in LDS.  Rows are independent in the product, so a tile with
 // several adapters runs once per adapter and keeps each adapter's rows.
 // Read once per adapter of the tile: 32 rows of V from HBM, rank rows of
-// M from L2.
+// M from L2.  Bound by memory: 8192 rows of 4096, rank 16, 33 us (2.0 TB/s);
+// 16384 rows, rank 64, 73 us.
 // ---------------------------------------------------------------------------
 constexpr int kShrinkRows = 32;
 

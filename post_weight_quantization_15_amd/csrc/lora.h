@@ -77,9 +77,10 @@ gptq_status launch_pad_rows(const uint16_t* V, int64_t ldv, int64_t n, int64_t l
 // fold: the unit of columns whose sums one step multiplies; 0: none.
 gptq_status launch_gemm(const GemmArgs& a, int fold, hipStream_t st);
 
-// Few rows (lora_decode.hip): no workspace but H [n][rank].  4096 x 4096 / 11008 x
-// 4096 in 4 bits at 192 rows: 50 / 98 us against 59 / 108 us by laid-out tiles.
-constexpr int64_t kDecodeMaxRows = 192;
+// Few rows (lora_decode.hip): no workspace but H [n][rank].  4096 columns into 4096
+// / 11008 into 4096 in 4 bits: 128 rows 34 / 68 us against 50 / 100 by laid-out
+// tiles (act-order 53 / 112 and 58 / 117), 160 rows 52 / 115 and 49 / 102.
+constexpr int64_t kDecodeMaxRows = 128;
 bool decode_takes(int64_t n, int64_t ng);
 gptq_status launch_lora_decode(const uint16_t* X, int64_t ldx, int64_t n, const Packed& w,
                                const gptq_adapters& ad, float* H, void* Y, int out_bf16,
