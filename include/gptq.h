@@ -386,7 +386,8 @@ gptq_status gptq_lora_backward(const void* dY, gptq_dtype dy_dtype, int64_t n, i
  *   stats and gradient are 0 whatever its logits hold.
  * A logit of -inf has probability 0 (a masked token); one that the teacher
  *   gives probability makes the loss +inf.  NaN, +inf and a row of nothing
- *   but -inf give NaN.
+ *   but -inf give NaN; a row of nothing but the type's lowest value is a row
+ *   of equal logits.
  * loss: fp32 [n].  stats: fp32 [n, 2] or NULL: the log-sum-exp of z over the
  *   vocabulary and over the ids outside S (t_lse NULL: the same), for
  *   gptq_distill_backward.  dlogits: d sum(loss) / d logits in the logits'
@@ -394,7 +395,7 @@ gptq_status gptq_lora_backward(const void* dY, gptq_dtype dy_dtype, int64_t n, i
  *   (same pointer and stride).
  * Cells are exponentiated and summed in fp32 (fp64 across threads), all that
  * is per row or known id in fp64.  Allocates nothing; no workspace.
- * Errors: INVALID_ARG (bad sizes, dtype, temperature not positive and finite,
+ * Errors: INVALID_ARG (bad sizes, dtype, temperature outside 1e-30 .. 1e30,
  *         NULL pointers when n > 0); HIP.
  * ------------------------------------------------------------------------- */
 gptq_status gptq_distill_loss(const void* logits, gptq_dtype dtype, int64_t n,

@@ -202,6 +202,7 @@ gptq_status launch_lora_backward(const uint16_t* dY, int64_t lddy, int64_t n, co
 // gradient where dlogits is given; with grad the gradient alone from stats.
 constexpr int kDistillMaxK = 1024;
 constexpr int64_t kDistillMaxVocab = 262144;
+constexpr float kDistillMinTemp = 1e-30f;   // and its inverse the largest
 gptq_status launch_distill(const void* logits, gptq_dtype dt, int64_t n, int64_t vocab,
                            int64_t ldl, const int32_t* t_idx, const float* t_logits, int64_t k,
                            float temp, const float* t_lse, const float* weight,

@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kMaxK = kDistillMaxK;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kFarLse = 1024.0f;       // from here fp32 stats are off by 2^-14 and more
 
 template <int DT>
 struct Cell;
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
   __shared__ double redd[THREADS / 64];
   __shared__ float redf[THREADS / 64], redg[THREADS / 64];
   __shared__ int dup;
-  __shared__ double sh_lse, sh_factor;
+  __shared__ double sh_top, sh_lse, sh_factor;
   __shared__ float sh_coef, sh_refc;
   const int tid = threadIdx.x, lane = tid & 63;
   const bool first = tid < 64;           // the wave of the known ids
@@ -264,9 +265,22 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
   if (tail && edge >= 0 && ((mask[ebase / 32] >> tid) & 1u)) ez = -INFINITY;
   // ---- the student's side: maximum, then sum of 2^(cf z - refc), refc = cf
   //      max as rounded (its rounding is put back per row, below)
-  float mx = -INFINITY, refc = 0.0f;
+  float mx = -INFINITY, refc = 0.0f, cr = cf;
   double sum = 0.0;
-  if (MODE != kBackward) {
+  // A log-sum-exp far from 0 keeps too little of its sum in the fp32 stats: the
+  // backward pass then forms it again.
+  const bool fresh = MODE != kBackward || !(fabsf(a.stats[2 * row]) < kFarLse);
+  // Where cf mx is so large that its rounding matters, cells are equal or so
+  // far apart that only the maximum counts: a power of two near cf does, whose
+  // product is exact (and finite).
+  auto refer = [&]() {
+    refc = mx * cf;
+    if (!(fabsf(refc) < 0x1p30f) && mx == mx) {
+      cr = ldexpf(1.0f, min(ilogbf(cf), 125 - ilogbf(mx)));
+      refc = mx * cr;
+    }
+  };
+  if (fresh) {
     float part = 0.0f;
     if (NV > 0) {
       float m = -INFINITY;
@@ -311,19 +325,19 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
       }
       // all cells -inf: nothing to exponentiate (the sum stays 0)
       if (mx != -INFINITY) {
-        refc = mx * cf;
-        if (edge >= 0) part = __builtin_amdgcn_exp2f(fmaf(ez, cf, -refc));
+        refer();
+        if (edge >= 0) part = __builtin_amdgcn_exp2f(fmaf(ez, cr, -refc));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           if (tid + THREADS * i >= nvec) break;
 #pragma unroll
           for (int e = 0; e < E; ++e)
-            part += __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(cell[i], e), cf, -refc));
+            part += __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(cell[i], e), cr, -refc));
         }
       }
     } else {
       float run = ez;
-      if (run != -INFINITY) part = __builtin_amdgcn_exp2f(fmaf(run, cf, -(run * cf)));
+      if (run != -INFINITY) part = 1.0f;
       for (int v = tid; v < nvec; v += THREADS) {
         u32x4 c = load_vec(src + head, v);
         if (tail) take_out(c, v);
@@ -331,32 +345,40 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) m8 = fmax_nan(m8, get_cell<DT>(c, e));
         if (m8 == -INFINITY) continue;
-        if (m8 != run) part *= __builtin_amdgcn_exp2f(run * cf - m8 * cf);
+        if (m8 != run) part *= __builtin_amdgcn_exp2f((run - m8) * cf);
         run = m8;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          part += __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, e), cf, -(run * cf)));
+          part += __builtin_amdgcn_exp2f((get_cell<DT>(c, e) - run) * cf);
       }
       mx = block_all<THREADS>(run, redf, fmax_nan);
-      if (mx != -INFINITY) refc = mx * cf;
-      if (run != -INFINITY) part *= __builtin_amdgcn_exp2f(run * cf - refc);
+      if (run != -INFINITY) part *= __builtin_amdgcn_exp2f((run - mx) * cf);
+      if (mx != -INFINITY) refer();
     }
     sum = block_all<THREADS>(double(part), redd, sum2<double>);
+    if (NV == 0 && cr == cf && mx != -INFINITY) sum *= exp2(double(mx) * double(cf) - double(refc));
   }
   // ---- per row, first wave: log-sum-exps, loss, the gradient's factors
   if (first) {
-    double lse, lse_rest;
-    if (MODE == kBackward) {
-      lse = double(a.stats[2 * row]);
-      lse_rest = double(a.stats[2 * row + 1]);
+    // Log-sum-exps as a cell's (mx, or top) share and the rest: lse = top / T +
+    // l_all over the row, mx / T + l_rest over the cells outside S, so that
+    // differences from them are exact however large the logits are.
+    double top = 0.0, l_all, l_rest, between = 0.0;       // between: lse_rest - lse
+    bool rest = true;                                     // the cells outside S have mass
+    if (!fresh) {
+      l_all = double(a.stats[2 * row]);
+      l_rest = double(a.stats[2 * row + 1]);
+      rest = l_rest != -INFINITY;
+      between = l_rest - l_all;
     } else {
-      // log of the cells' sum; refc stands for cf mx up to its rounding
-      lse_rest = mx == -INFINITY ? -INFINITY
-                                 : double(mx) * a.inv_temp + dlog(sum) -
-                                       (double(mx) * double(cf) - double(refc)) * kLn2;
-      lse = lse_rest;                  // NaN below for a row without a finite cell
+      rest = mx != -INFINITY;
+      // refc stands for cf mx up to its rounding
+      l_rest = rest ? dlog(sum) - (cr == cf ? (double(mx) * double(cf) - double(refc)) * kLn2 : 0.0)
+                    : -INFINITY;
       if (!tail) {
-        if (mx == -INFINITY) lse = lse_rest = NAN;
+        top = double(mx);
+        l_all = rest ? l_rest : NAN;     // NaN for a row without a finite cell
+        rest = true;
       } else {
         // the known ids' share, on the larger of the two maxima
         float ms = mx;
@@ -364,63 +386,67 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
           const int32_t id = ids[i];
           if (id >= 0 && id < V) ms = fmax_nan(ms, z_s[i]);
         }
-        const float top = wave_all(ms, fmax_nan);
+        top = double(wave_all(ms, fmax_nan));
         double ss = 0.0;
         for (int i = lane; i < a.k; i += 64) {
           const int32_t id = ids[i];
           if (id < 0 || id >= V) continue;
-          bool one = true;             // an id named twice has its mass once
+          bool one = true;               // an id named twice has its mass once
           if (dup)
             for (int j = 0; j < i; ++j) one = one && ids[j] != id;
-          if (one) ss += dexp((double(z_s[i]) - double(top)) * a.inv_temp);
+          if (one) ss += dexp((double(z_s[i]) - top) * a.inv_temp);
         }
         ss = wave_all(ss, sum2<double>);
-        if (mx != -INFINITY) ss += dexp(lse_rest - double(top) * a.inv_temp);
-        lse = double(top) * a.inv_temp + dlog(ss);
+        const double lead = (double(mx) - top) * a.inv_temp + l_rest;
+        if (rest) ss += dexp(lead);
+        l_all = dlog(ss);
+        between = rest ? lead - l_all : -INFINITY;
       }
     }
-    const bool use_rest = tail && !(p_rest <= 0.0) && lse_rest != -INFINITY;
+    const bool use_rest = tail && !(p_rest <= 0.0) && rest;
     if (MODE != kBackward) {
       double t = 0.0;
       for (int i = lane; i < a.k; i += 64) {
         const double p = p_s[i];
         if (p != 0.0)
-          t += p * ((double(tl[i]) * a.inv_temp - t_norm) - (double(z_s[i]) * a.inv_temp - lse));
+          t += p * ((double(tl[i]) * a.inv_temp - t_norm) - ((double(z_s[i]) - top) * a.inv_temp - l_all));
       }
       t = wave_all(t, sum2<double>);
-      if (use_rest) t += p_rest * (dlog(p_rest) - (lse_rest - lse));
+      if (use_rest) t += p_rest * (dlog(p_rest) - between);
       // a row that knows nothing of the teacher has no loss, whatever it holds
       if (!tail && p_sum == 0.0) t = 0.0;
       if (lane == 0) {
         a.loss[row] = static_cast<float>(double(w) * a.temp * a.temp * t);
         if (a.stats) {
-          a.stats[2 * row] = static_cast<float>(lse);
-          a.stats[2 * row + 1] = static_cast<float>(lse_rest);
+          a.stats[2 * row] = static_cast<float>(top * a.inv_temp + l_all);
+          a.stats[2 * row + 1] = static_cast<float>(tail ? (rest ? double(mx) * a.inv_temp + l_rest : -INFINITY)
+                                                         : top * a.inv_temp + l_all);
         }
       }
     }
     if (MODE != kLoss && lane == 0) {
-      // A cell outside S: q_v (1 - p_r / q_r) = dexp(z_v - lse_rest) (q_r - p_r):
+      // A cell outside S: q_v (1 - p_r / q_r) = exp(z_v - lse_rest) (q_r - p_r):
       // no factor overflows where q_r is tiny.  A row that knows nothing of
       // the teacher has no gradient, as no loss.
       const double factor = (!tail && p_sum == 0.0)
                                 ? 0.0
                                 : double(w) * a.temp * (MODE == kBackward ? double(a.grad[row]) : 1.0);
-      const double base = tail ? lse_rest : lse;      // the log-sum-exp of those cells
       double coef = 0.0;
       float rc = refc;
-      if (base != -INFINITY) {
-        coef = factor * (dexp(base - lse) - (use_rest ? p_rest : 0.0));
-        if (MODE == kBackward) {
-          rc = static_cast<float>(base / kLn2);
-          coef *= exp2(double(rc) - base / kLn2);
-        } else {
+      if (rest) {
+        coef = factor * (dexp(between) - (use_rest ? p_rest : 0.0));
+        if (fresh) {
           coef /= sum;
+        } else {
+          const double base = l_rest / kLn2;
+          rc = static_cast<float>(base);
+          coef *= exp2(double(rc) - base);
         }
       }
       sh_coef = static_cast<float>(coef);
-      sh_refc = base == -INFINITY ? 0.0f : rc;
-      sh_lse = lse;
+      sh_refc = rest ? rc : 0.0f;
+      sh_top = top;
+      sh_lse = l_all;
       sh_factor = factor;
     }
   }
@@ -433,12 +459,12 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (DT == GPTQ_F32) {
-        g[e] = to_bits<DT>(coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, e), cf, -rc)));
+        g[e] = to_bits<DT>(coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, e), cr, -rc)));
       } else {
         const uint32_t lo = to_bits<DT>(
-            coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, (2 * e) % E), cf, -rc)));
+            coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, (2 * e) % E), cr, -rc)));
         const uint32_t hi = to_bits<DT>(
-            coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, (2 * e + 1) % E), cf, -rc)));
+            coef * __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(c, (2 * e + 1) % E), cr, -rc)));
         g[e] = lo | (hi << 16);
       }
     }
@@ -446,7 +472,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
   };
   if (edge >= 0) {
     const uint32_t b = to_bits<DT>(
-        coef * __builtin_amdgcn_exp2f(fmaf(cell_to_f32(src[edge], DTag()), cf, -rc)));
+        coef * __builtin_amdgcn_exp2f(fmaf(cell_to_f32(src[edge], DTag()), cr, -rc)));
     if (DT == GPTQ_F32) reinterpret_cast<uint32_t*>(dst)[edge] = b;
     else reinterpret_cast<uint16_t*>(dst)[edge] = static_cast<uint16_t>(b);
   }
@@ -475,7 +501,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
   }
   // ... then the cells of S over it (entries of one id write the same value)
   __syncthreads();
-  const double lse = sh_lse, factor = sh_factor;
+  const double top_z = sh_top, lse = sh_lse, factor = sh_factor;
   for (int i = tid; i < a.k; i += THREADS) {
     const int32_t id = ids[i];
     if (id < 0 || id >= V) continue;
@@ -485,7 +511,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
       for (int j = 0; j < a.k; ++j)
         if (ids[j] == id) p += p_s[j];
     }
-    const double g = factor * (dexp(double(z_s[i]) * a.inv_temp - lse) - p);
+    const double g = factor * (dexp((double(z_s[i]) - top_z) * a.inv_temp - lse) - p);
     const uint32_t b = to_bits<DT>(static_cast<float>(g));
     if (DT == GPTQ_F32) reinterpret_cast<uint32_t*>(dst)[id] = b;
     else reinterpret_cast<uint16_t*>(dst)[id] = static_cast<uint16_t>(b);

@@ -1,7 +1,5 @@
 // Host side of the adapter products, the transposed dequantizing product and
 // the distillation loss: argument validation and workspace checks.
-#include <cmath>
-
 #include "common.h"
 
 using namespace gptq;
@@ -141,7 +139,7 @@ static bool valid_distill(const void* logits, gptq_dtype dt, int64_t n, int64_t 
                           float temp) {
   if ((dt != GPTQ_BF16 && dt != GPTQ_F16 && dt != GPTQ_F32) || n < 0 || n > (int64_t(1) << 21) ||
       vocab < 1 || vocab > kDistillMaxVocab || ldl < vocab || k < 1 || k > kDistillMaxK ||
-      !(temp > 0.0f) || !std::isfinite(temp))
+      !(temp >= kDistillMinTemp && temp <= 1.0f / kDistillMinTemp))
     return false;
   return n == 0 || (logits && t_idx && t_logits);
 }

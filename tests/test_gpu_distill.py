@@ -327,3 +327,51 @@ def test_gradient_at_another_alignment(dev, shift, dtype):
     assert torch.equal(out, want["dlogits"]) and torch.equal(got["loss"], want["loss"])
     out.zero_()
     assert float(wide.double().sum()) == 3.0 * (5003 + 9 + 3 * 9)
+
+
+@pytest.mark.parametrize("vocab", [900, 9000, 140001])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("far", [2.0 ** 20, 2.0 ** 22, -2.0 ** 22])
+def test_logits_far_from_zero(dev, vocab, tail, far):
+    """Only differences of logits count: whole numbers moved by a large one
+    (exact in fp32) keep the loss and both gradients, within the bounds of the
+    logits that were not moved (the stats of such rows are not relied on)."""
+    z, idx, t, t_lse, w = inputs(3, vocab, 9, torch.float32, 2.0, tail, seed=16, scale=6.0)
+    z = torch.round(z)
+    kw = dict(temperature=2.0, t_lse=to(dev, t_lse), weight=to(dev, w))
+    zg = (z + far).to(dev)
+    got = gq.gptq_distill_loss(zg, to(dev, idx), to(dev, t), want_grad=True, **kw)
+    back = gq.gptq_distill_backward(zg, got["stats"], to(dev, idx), to(dev, t),
+                                    torch.ones(3, device=dev), **kw)
+    loss, grad = orc.distill(z.double().numpy(), idx, t, 2.0, t_lse, w)
+    lb, gb = bounds(z, idx, t, 2.0, t_lse, w)
+    near(got["loss"], loss, lb + U * np.abs(loss), "loss")
+    near(got["dlogits"], grad, gb + half_step(torch.float32, grad), "gradient")
+    near(back, grad, gb + half_step(torch.float32, grad), "backward")
+
+
+@pytest.mark.parametrize("T", [0.5, 1.0, 2.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("vocab", [1000, 16000, 140000])
+def test_a_row_of_nothing_but_the_lowest_value(dev, dtype, T, vocab):
+    """Equal logits, however low: q = 1 / vocab.  A second row of the lowest
+    value but for one cell at half of it: all mass there."""
+    z = torch.full((2, vocab), torch.finfo(dtype).min, dtype=dtype, device=dev)
+    z[1, 7] = torch.finfo(dtype).min / 2
+    ti = torch.tensor([[3, 5], [7, -1]], dtype=torch.int32, device=dev)
+    tt = torch.zeros(2, 2, device=dev)
+    got = gq.gptq_distill_loss(z, ti, tt, temperature=T, want_grad=True)
+    back = gq.gptq_distill_backward(z, got["stats"], ti, tt, torch.ones(2, device=dev), temperature=T)
+    loss = got["loss"].cpu().double()
+    # log 1/2 - log 1/vocab, each log-sum-exp within 140 u and its own rounding
+    want = T * T * np.log(vocab / 2)
+    assert abs(float(loss[0]) - want) <= T * T * 160 * U + U * want
+    assert abs(float(loss[1])) <= T * T * 160 * U
+    for g in (got["dlogits"], back):
+        g = g.cpu().double()
+        q = T / vocab
+        half = float(half_step(dtype, np.array(q))) + 160 * U * q
+        assert float((g[0, 8:] - q).abs().max()) <= half
+        hot = T * (0.5 - 1 / vocab)
+        assert float((g[0, 3] + hot).abs()) <= float(half_step(dtype, np.array(hot))) + 160 * U
+        assert float(g[1].abs().max()) <= T * 160 * U
