@@ -448,12 +448,12 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs a, unsigned nw
 // turn through LDS at the end into whole lines of the result.
 //
 // Reaches 1190 TFLOP/s without a fold on 256 x 256 tiles (8192 rows of 11008
-// into 4096: 621 us), 950 on 256 x 128 (8192 rows of 4096 into 11008: 781 us)
-// and 730 with a fold every 64 columns (256 x 128, two sets of accumulators;
+// into 4096: 621 us; 8192 rows of 4096 into 11008: 695, 781 on 256 x 128) and
+// 730 with a fold every 64 columns (256 x 128, two sets of accumulators;
 // 16384 rows of 4096 into 11008: 2.03 ms), against 1430 of a large library
-// product.  Matrix instructions alone take 474 us of the second, with the
-// barriers 542, with either the copies or the LDS reads about 700: no one of
-// them bounds it, their overlap does.
+// product.  Matrix instructions alone take 474 us of the second on 256 x 128,
+// with the barriers 542, with either the copies or the LDS reads about 700: no
+// one of them bounds it, their overlap does.
 // ---------------------------------------------------------------------------
 constexpr int kBk = 64;
 
@@ -886,7 +886,7 @@ gptq_status launch_fold(const GemmArgs& a, hipStream_t st) {
     const int64_t last = (left + 255) / 256;
     return double((rounds - 1) * per_cu + last) * tm * tn / rate;
   };
-  const double c256 = FOLD == 0 ? cost(256, 256, 1, 1.05) : 1e30, cw = cost(256, 128, 1, 1.0);
+  const double c256 = FOLD == 0 ? cost(256, 256, 1, 1.2) : 1e30, cw = cost(256, 128, 1, 1.0);
   const double c128 = cost(128, 128, 1, 0.75), c64 = cost(64, 64, 3, 0.40), c32 = cost(32, 32, 6, 0.18);
   const double best = std::min(std::min(std::min(c256, cw), std::min(c128, c64)), c32);
   if constexpr (FOLD == 0)
