@@ -9,7 +9,6 @@ namespace gptq {
 inline unsigned ceil_div(int64_t a, int64_t b) { return static_cast<unsigned>((a + b - 1) / b); }
 inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
-
 // ---------------------------------------------------------------------------
 // The products Y[t][j] = sum_k V[t][k] M[j][k] (+ the adapters' part) of
 // lora_gemm.hip.  Both operands are bf16 with k contiguous, rows 16-byte
