@@ -27,8 +27,6 @@ namespace {
 // M from L2.  Bound by memory: 8192 rows of 4096, rank 16, 33 us (2.0 TB/s);
 // 16384 rows, rank 64, 73 us.
 // ---------------------------------------------------------------------------
-constexpr int kShrinkRows = 32;
-
 struct ShrinkArgs {
   const uint16_t* V;
   int64_t ldv, n, len;
@@ -41,6 +39,7 @@ struct ShrinkArgs {
   float* H;                 // [n][rank] or NULL
   uint16_t* parts;          // [n][3 rp]
   float* sums;              // [grid.y][n][rank] when grid.y > 1
+  size_t sums_floats;       // kept for them
 };
 
 // Value q of row t: to H, and alpha times it as parts.
@@ -175,13 +174,6 @@ __global__ __launch_bounds__(256) void shrink_sum_kernel(ShrinkArgs a, int share
   put_hidden(a, t, p, v, a.alpha[id]);
 }
 
-// Shares of k per row tile: enough workgroups for the chip where rows are
-// few, at least 16 steps each.
-int shrink_shares(int64_t n, int64_t len) {
-  const int64_t tiles = (n + kShrinkRows - 1) / kShrinkRows;
-  return tiles >= 128 ? 1 : int(std::max<int64_t>(1, std::min<int64_t>(512 / tiles, (len + 511) / 512)));
-}
-
 gptq_status launch_shrink(const ShrinkArgs& a, hipStream_t st) {
   const bool vv = a.ldv % 8 == 0 && reinterpret_cast<uintptr_t>(a.V) % 16 == 0;
   const bool vm = a.ldm % 8 == 0 && reinterpret_cast<uintptr_t>(a.M) % 16 == 0;
@@ -194,7 +186,7 @@ gptq_status launch_shrink(const ShrinkArgs& a, hipStream_t st) {
     GPTQ_CHECK_LAUNCH();
     return GPTQ_OK;
   }
-  const int shares = shrink_shares(a.n, a.len);
+  const int shares = shrink_shares(a.n, a.len, a.rank, a.sums_floats);
   const dim3 grid(ceil_div(a.n, kShrinkRows), shares);
   if (a.rank <= 16) shrink_kernel<1, 8><<<grid, 512, 0, st>>>(a, vv, vm);
   else if (a.rank <= 32) shrink_kernel<2, 8><<<grid, 512, 0, st>>>(a, vv, vm);
@@ -466,6 +458,7 @@ struct LoraWs {
   float* hidden;
   uint16_t* parts;
   float* sums;
+  size_t sums_floats;
   int32_t* plan;
   uint16_t* M;
   float* scale_t;
@@ -486,8 +479,8 @@ LoraWs carve_lora(Carver& c, int64_t n, int64_t m, int64_t d, int64_t group, int
     return w;
   }
   w.parts = c.take<uint16_t>(size_t(nc) * 3 * parts_rank(rank));
-  const int shares = shrink_shares(nc, d);
-  w.sums = c.take<float>(shares > 1 ? size_t(shares) * nc * rank : 0);
+  w.sums_floats = shrink_floats_chunked(n, d, rank);
+  w.sums = c.take<float>(w.sums_floats);
   const int64_t mpad = round_up(m, 256) + 64, ldp = round_up(d, 64);
   const int lay = layout_of(group);
   const int64_t cols = lay == kByGroups ? plan_cols(d, ng, group) : ldp;
@@ -502,6 +495,7 @@ struct BackWs {
   uint16_t* parts;   // of G
   uint16_t* hparts;  // of alpha H
   float* sums;
+  size_t sums_floats;
   uint16_t* At;      // [count][d][rank]
   uint16_t* Bt;      // [count][rank][mp]
   uint16_t* Wt;      // [d][mp]
@@ -518,8 +512,8 @@ BackWs carve_back(Carver& c, int64_t n, int64_t m, int64_t d, int rank, int coun
   if (count == 0) return w;
   w.parts = c.take<uint16_t>(size_t(n) * 3 * parts_rank(rank));
   w.hparts = c.take<uint16_t>(size_t(n) * 3 * parts_rank(rank));
-  const int shares = shrink_shares(n, m);
-  w.sums = c.take<float>(shares > 1 ? size_t(shares) * n * rank : 0);
+  w.sums_floats = shrink_floats(n, m, rank);
+  w.sums = c.take<float>(w.sums_floats);
   w.At = c.take<uint16_t>(size_t(count) * d * rank);
   w.Bt = c.take<uint16_t>(size_t(count) * rank * mp);
   w.outer[0] = c.take<float>(outer_floats(n, d, rank, count));
@@ -580,7 +574,7 @@ gptq_status launch_lora(const uint16_t* X, int64_t ldx, int64_t n, const Packed&
     const uint16_t* Xc = X + t0 * ldx;
     ShrinkArgs h{Xc, ldx, nc, w.d, static_cast<const uint16_t*>(ad.A), w.d, ad.row + t0,
                  ad.n_adapters, ad.rank, rp, ad.alpha, 0, H ? H + t0 * ad.rank : nullptr, b.parts,
-                 b.sums};
+                 b.sums, b.sums_floats};
     if ((s = launch_shrink(h, st)) != GPTQ_OK) return s;
     g.V = direct ? Xc : nullptr;
     g.ldv = ldx;
@@ -633,7 +627,7 @@ gptq_status launch_lora_backward(const uint16_t* dY, int64_t lddy, int64_t n, co
   if ((s = launch_prepare(pa, st)) != GPTQ_OK) return s;
   if (need_g) {
     const ShrinkArgs h{dY, lddy, n, w.m, b.Bt, mp, ad.row, ad.n_adapters, ad.rank, rp, ad.alpha, 1,
-                       nullptr, b.parts, b.sums};
+                       nullptr, b.parts, b.sums, b.sums_floats};
     if ((s = launch_shrink(h, st)) != GPTQ_OK) return s;
   }
   if (dA || dB) {

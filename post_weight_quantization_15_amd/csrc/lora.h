@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.h"
+#include "lora_sizes.h"
 
 namespace gptq {
 
@@ -35,9 +36,6 @@ struct GemmArgs {
   int out_bf16;
 };
 constexpr int kPlanHeader = 16;   // words before the plan's group list
-
-// Rows of activations handled at once (bounds the reordered copy).
-constexpr int64_t kRowChunk = 16384;
 
 // Columns in group order, every group padded to whole units (64
 // columns where they divide the group size, else 32), and all to whole blocks.

@@ -484,3 +484,42 @@ def test_lora_passes_groups_and_long_rows(dev, case):
 def test_lora_gradients_of_long_rows(dev, n):
     check_backward(dev, Layer(70, 40000, 4, 128, "act"), n, 2, 16, "each")
     check_backward(dev, Layer(9000, 72, 4, 64), n, 2, 16, "each")
+
+
+@pytest.mark.parametrize("case", [
+    (16385, 33, 1100, 4, 128, "natural", 3, 16, "runs"),     # one row in the second chunk
+    (20000, 40, 1152, 4, 128, "natural", 5, 16, "runs"),     # a short one, its k in three shares
+    (20000, 40, 1100, 3, 64, "act", 5, 16, "random"),
+    (20000, 24, 1152, 4, -1, "natural", 2, 33, "runs"),
+    (20000, 24, 1152, 2, 16, "act", 2, 16, "runs"),
+    (36384, 16, 576, 4, 64, "natural", 2, 16, "runs"),       # ... behind two whole ones
+    (32768, 16, 576, 4, 128, "act", 2, 16, "runs"),          # whole chunks alone
+], ids=lambda c: "n%d_m%d_d%d_b%d_g%d_%s_L%d_r%d_%s" % c)
+def test_lora_rows_in_chunks(dev, case):
+    n, m, d, bits, group, order, L, r, kind = case
+    check_lora(dev, Layer(m, d, bits, group, order), n, L, r, kind)
+
+
+def test_rows_in_chunks_stay_in_their_workspace(dev):
+    """The workspace asked for is enough, to the byte: what lies behind it stays,
+    and the result is that of a larger one."""
+    n, m, d, group, r = 20000, 40, 1152, 64, 16
+    c = make_call(dev, n=n, m=m, d=d, r=r)
+    c["packed"] = Layer(m, d, 4, group).on(dev)
+    want = forward(c)
+    need = gq.gptq_lora_workspace_bytes(n, m, d, group, r)
+    ws = torch.full((need + 4096,), 77, dtype=torch.uint8, device=dev)
+    got = forward(c, ws=ws[:need])
+    torch.cuda.synchronize()
+    assert same(got, want) and bool((ws[need:] == 77).all())
+
+
+@pytest.mark.parametrize("case", [
+    (20000, 40, 1152, 4, 128, "natural", 3, 16, "runs"),
+    (16385, 24, 576, 4, -1, "natural", 2, 8, "runs"),
+    (20000, 24, 576, 3, 64, "act", 2, 8, "random"),
+    (32769, 24, 320, 2, 16, "natural", 2, 8, "runs"),
+], ids=lambda c: "n%d_m%d_d%d_b%d_g%d_%s_L%d_r%d_%s" % c)
+def test_lora_gradients_of_rows_in_chunks(dev, case):
+    n, m, d, bits, group, order, L, r, kind = case
+    check_backward(dev, Layer(m, d, bits, group, order), n, L, r, kind)
