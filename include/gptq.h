@@ -374,7 +374,9 @@ gptq_status gptq_lora_backward(const void* dY, gptq_dtype dy_dtype, int64_t n, i
  *   sum_S p), is one more class against the student's q_r = 1 - sum_S q
  *     loss = w T^2 [sum_S p (log p - log q) + p_r (log p_r - log q_r)]
  *     d loss / d logits_v = w T (q_v - p_v) on S, w T q_v (1 - p_r / q_r)
- *     elsewhere; without student mass outside S that class is left out.
+ *     elsewhere.  Where p_r = 0, or the student has no mass outside S (every
+ *     other logit -inf, or none), that class is left out: with P = sum_S p,
+ *     d loss / d logits_v = w T (P q_v - p_v) on S, w T P q_v elsewhere.
  *
  * logits: [n, vocab] of dtype GPTQ_BF16, GPTQ_F16 or GPTQ_F32, row stride ldl
  *   >= vocab; 1 <= vocab <= 262144; n <= 2097152.

@@ -68,7 +68,7 @@ def _lse(z):
 def distill(logits, t_idx, t_logits, temperature=1.0, t_lse=None, weight=None):
     """(loss [n], d sum(loss) / d logits [n, vocab]), the definition row by row:
     T^2 sum p (log p - log q) over the known ids and, with t_lse, the class
-    of all others."""
+    of all others (unless the student has no mass there)."""
     logits = np.asarray(logits, dtype=np.float64)
     n, vocab = logits.shape
     loss, grad = np.zeros(n), np.zeros((n, vocab))
@@ -89,12 +89,16 @@ def distill(logits, t_idx, t_logits, temperature=1.0, t_lse=None, weight=None):
         out = np.ones(vocab, dtype=bool)
         out[known] = False
         lse_rest = _lse(z[out])
-        d = q.copy()
+        # what the target's probabilities add up to: 1, but for a class left out
+        mass = 1.0
+        if t_lse is not None and not (rest > 0 and np.isfinite(lse_rest)):
+            rest, mass = 0.0, p.sum()
+        d = mass * q
         if t_lse is not None and np.isfinite(lse_rest):
             q_rest = np.exp(lse_rest - lse)
             if rest > 0:
                 value += rest * (np.log(rest) - (lse_rest - lse))
-            d[out] = np.exp(z[out] - lse_rest) * (q_rest - rest)
+            d[out] = np.exp(z[out] - lse_rest) * (mass * q_rest - rest)
         d[known] -= p_of
         loss[k] = w * temperature ** 2 * value
         grad[k] = w * temperature * d

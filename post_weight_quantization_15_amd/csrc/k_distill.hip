@@ -9,7 +9,9 @@
 // log-sum-exp is given, its true probabilities exp(t / T - t_lse) with what
 // is left, p_r = 1 - sum p, as one more class against the student's
 // q_r = 1 - sum_S q: the loss gains p_r (log p_r - log q_r) and the cells
-// outside S get w T q_v (1 - p_r / q_r).
+// outside S get w T q_v (1 - p_r / q_r).  Where that class is left out (p_r =
+// 0, or q_r = 0: every cell outside S at -inf) what the probabilities add up
+// to, P = sum_S p, stands before q: w T (P q_v - p_v) on S, w T P q_v elsewhere.
 //
 // One workgroup per row.  The row's cells are read once, 16 bytes a load,
 // and stay in registers as stored (a row of up to 131072 16-bit cells is
@@ -165,7 +167,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
   __shared__ double redd[THREADS / 64];
   __shared__ float redf[THREADS / 64], redg[THREADS / 64];
   __shared__ int dup;
-  __shared__ double sh_top, sh_lse, sh_factor;
+  __shared__ double sh_top, sh_lse, sh_factor, sh_mass;
   __shared__ float sh_coef, sh_refc;
   const int tid = threadIdx.x, lane = tid & 63;
   const bool first = tid < 64;           // the wave of the known ids
@@ -431,10 +433,11 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
       const double factor = (!tail && p_sum == 0.0)
                                 ? 0.0
                                 : double(w) * a.temp * (MODE == kBackward ? double(a.grad[row]) : 1.0);
+      const double mass = tail && !use_rest ? p_sum : 1.0;   // sum of the target's classes
       double coef = 0.0;
       float rc = refc;
       if (rest) {
-        coef = factor * (dexp(between) - (use_rest ? p_rest : 0.0));
+        coef = factor * (mass * dexp(between) - (use_rest ? p_rest : 0.0));
         if (fresh) {
           coef /= sum;
         } else {
@@ -448,6 +451,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
       sh_top = top;
       sh_lse = l_all;
       sh_factor = factor;
+      sh_mass = mass;
     }
   }
   if (MODE == kLoss) return;
@@ -501,7 +505,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
   }
   // ... then the cells of S over it (entries of one id write the same value)
   __syncthreads();
-  const double top_z = sh_top, lse = sh_lse, factor = sh_factor;
+  const double top_z = sh_top, lse = sh_lse, factor = sh_factor, mass = sh_mass;
   for (int i = tid; i < a.k; i += THREADS) {
     const int32_t id = ids[i];
     if (id < 0 || id >= V) continue;
@@ -511,7 +515,7 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
       for (int j = 0; j < a.k; ++j)
         if (ids[j] == id) p += p_s[j];
     }
-    const double g = factor * (dexp((double(z_s[i]) - top_z) * a.inv_temp - lse) - p);
+    const double g = factor * (mass * dexp((double(z_s[i]) - top_z) * a.inv_temp - lse) - p);
     const uint32_t b = to_bits<DT>(static_cast<float>(g));
     if (DT == GPTQ_F32) reinterpret_cast<uint32_t*>(dst)[id] = b;
     else reinterpret_cast<uint16_t*>(dst)[id] = static_cast<uint16_t>(b);

@@ -375,3 +375,60 @@ def test_a_row_of_nothing_but_the_lowest_value(dev, dtype, T, vocab):
         hot = T * (0.5 - 1 / vocab)
         assert float((g[0, 3] + hot).abs()) <= float(half_step(dtype, np.array(hot))) + 160 * U
         assert float(g[1].abs().max()) <= T * 160 * U
+
+
+def without_rest(case, vocab, k, dtype, seed=17):
+    """Rows whose class of all others is left out: every other cell -inf, no
+    other cell, or known probabilities beyond 1."""
+    z, idx, t, _, w = inputs(4, k if case == "whole" else vocab, k, dtype, 1.5, False, seed=seed)
+    if case == "masked":
+        for r in range(4):
+            z[r, np.setdiff1d(np.arange(vocab), idx[r])] = -float("inf")
+    known = np.log(np.exp(t.astype(np.float64) / 1.5).sum(1))
+    off = np.array([0.3, 0.7, 1.5, 3.0]) * (-0.5 if case == "over" else 1)
+    return z, idx, t, (known + off).astype(np.float32), w
+
+
+@pytest.mark.parametrize("case,vocab,k", [("masked", 700, 9), ("masked", 9001, 200), ("masked", 140001, 5),
+                                          ("whole", 0, 1), ("whole", 0, 40), ("whole", 0, 1000),
+                                          ("over", 700, 9), ("over", 20003, 64), ("over", 140001, 5)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32],
+                         ids=["bf16", "f16", "f32"])
+def test_without_the_rest_class(dev, case, vocab, k, dtype):
+    """Held against the oracle; the target's sum P stands before q and the
+    log-sum-exp, and so before their errors."""
+    T = 1.5
+    z, idx, t, t_lse, w = without_rest(case, vocab, k, dtype)
+    kw = dict(temperature=T, t_lse=to(dev, t_lse), weight=to(dev, w))
+    got = gq.gptq_distill_loss(z.to(dev), to(dev, idx), to(dev, t), want_grad=True, **kw)
+    up = np.array([0.5, 1.0, 1.5, 2.0], np.float32)
+    back = gq.gptq_distill_backward(z.to(dev), got["stats"], to(dev, idx), to(dev, t), to(dev, up), **kw)
+    torch.cuda.synchronize()
+    loss, grad = orc.distill(z.double().numpy(), idx, t, T, t_lse, w)
+    lb, gb = bounds(z, idx, t, T, t_lse, w)
+    P = np.maximum(1.0, np.exp(t.astype(np.float64) / T - t_lse[:, None]).sum(1))
+    near(got["loss"], loss, lb * P + U * np.abs(loss), "loss")
+    near(got["dlogits"], grad, gb * P[:, None] + half_step(dtype, grad), "gradient")
+    gb2 = bounds(z, idx, t, T, t_lse, w, stored=True, grad=up)[1]
+    g2 = grad * up[:, None].astype(np.float64)
+    near(back, g2, gb2 * P[:, None] + half_step(dtype, g2), "backward")
+
+
+@pytest.mark.parametrize("case", ["masked", "whole", "over"])
+def test_gradient_without_the_rest_class_is_the_loss_s_difference(dev, case):
+    """As for rows with that class: steps of at most 1/8 on z, 1/12 on z / T, the
+    third derivative of P log-sum-exps at most 2 P (step / T)^3, times T^2 w."""
+    T = 1.5
+    z, idx, t, t_lse, w = without_rest(case, 600, 12, torch.float32)
+    rng = np.random.default_rng(18)
+    step = torch.from_numpy(rng.uniform(-1, 1, size=z.shape).astype(np.float32) / 8)
+    up, down = z + step, z - step
+    kw = dict(temperature=T, t_lse=to(dev, t_lse), weight=to(dev, w))
+    ix, tt = to(dev, idx), to(dev, t)
+    grad = gq.gptq_distill_loss(z.to(dev), ix, tt, want_grad=True, **kw)["dlogits"].cpu().double()
+    a = gq.gptq_distill_loss(up.to(dev), ix, tt, **kw)["loss"].cpu().double()
+    b = gq.gptq_distill_loss(down.to(dev), ix, tt, **kw)["loss"].cpu().double()
+    move = torch.where(torch.isfinite(z), (up.double() - down.double()) / 2, 0.0)
+    P = torch.from_numpy(np.exp(t.astype(np.float64) / T - t_lse[:, None]).sum(1))
+    bound = torch.from_numpy(w).double() * T * T * (2 * P * (1 / 12) ** 3 / 6 + (1 + P) * 1e-5)
+    assert bool((((a - b) / 2 - (move * grad).sum(1)).abs() <= bound).all())

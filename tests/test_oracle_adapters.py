@@ -81,3 +81,37 @@ def test_distill_by_hand():
     loss, grad = orc.distill(z, np.array([[0]]), np.array([[5.0]]), 1.0)
     assert abs(loss[0] - np.log(2.0)) < 1e-15
     assert np.abs(grad[0] - np.array([-0.5, 0.25, 0.25])).max() < 1e-15
+
+
+@pytest.mark.parametrize("case", ["masked", "whole", "over"])
+def test_distill_gradient_without_the_rest_class_is_differences(case):
+    """The class of all others is left out where the student has no mass there
+    (every other cell -inf, or no other cell) and where the known ids' own
+    probabilities reach 1 or more: their sum, not 1, multiplies q."""
+    rng = np.random.default_rng(3)
+    n, vocab, k, T = 3, 7, 4, 1.5
+    z = rng.normal(size=(n, vocab))
+    if case == "whole":
+        z = z[:, :k].copy()
+    idx = np.stack([rng.permutation(z.shape[1])[:k] for _ in range(n)])
+    t = rng.normal(size=(n, k))
+    if case == "masked":
+        for r in range(n):
+            z[r, np.setdiff1d(np.arange(vocab), idx[r])] = -np.inf
+    known = np.log(np.exp(t / T).sum(1))
+    t_lse = known + np.array([0.3, 0.7, 1.5]) * (-1 if case == "over" else 1)
+    w = np.array([1.0, 0.5, 2.0])
+    value = lambda: float(orc.distill(z, idx, t, T, t_lse, w)[0].sum())  # noqa: E731
+    grad = orc.distill(z, idx, t, T, t_lse, w)[1]
+    assert np.abs(grad - differences(value, z)).max() < TOL
+    assert np.abs(grad.sum(1)).max() < 1e-14        # the loss does not see a common shift
+
+
+def test_distill_without_the_rest_class_by_hand():
+    # p = (.4, .2, .1) on all that is not masked: d = q * 0.7 - p
+    z = np.array([[0.3, -0.2, 0.1, -np.inf, -np.inf]])
+    p = np.array([0.4, 0.2, 0.1])
+    grad = orc.distill(z, np.array([[0, 1, 2]]), np.log(p)[None], 1.0, np.array([0.0]))[1]
+    q = np.exp(z[0, :3]) / np.exp(z[0, :3]).sum()
+    assert np.abs(grad[0, :3] - (0.7 * q - p)).max() < 1e-15 and not grad[0, 3:].any()
+    assert np.abs(grad[0, :3] - np.array([-0.1114, -0.0249, 0.1363])).max() < 1e-4
