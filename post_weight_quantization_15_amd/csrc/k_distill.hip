@@ -269,9 +269,11 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
   //      max as rounded (its rounding is put back per row, below)
   float mx = -INFINITY, refc = 0.0f, cr = cf;
   double sum = 0.0;
-  // A log-sum-exp far from 0 keeps too little of its sum in the fp32 stats: the
-  // backward pass then forms it again.
-  const bool fresh = MODE != kBackward || !(fabsf(a.stats[2 * row]) < kFarLse);
+  // A log-sum-exp far from 0 keeps too little of its sum in the fp32 stats (that
+  // of the cells outside S also where they are masked by a low value; there it
+  // may lie beyond fp32): the backward pass then forms both again.
+  const bool fresh = MODE != kBackward || !(fabsf(a.stats[2 * row]) < kFarLse &&
+                                            fabsf(a.stats[2 * row + 1]) < kFarLse);
   // Where cf mx is so large that its rounding matters, cells are equal or so
   // far apart that only the maximum counts: a power of two near cf does, whose
   // product is exact (and finite).
@@ -370,7 +372,6 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
     if (!fresh) {
       l_all = double(a.stats[2 * row]);
       l_rest = double(a.stats[2 * row + 1]);
-      rest = l_rest != -INFINITY;
       between = l_rest - l_all;
     } else {
       rest = mx != -INFINITY;

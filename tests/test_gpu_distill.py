@@ -432,3 +432,57 @@ def test_gradient_without_the_rest_class_is_the_loss_s_difference(dev, case):
     P = torch.from_numpy(np.exp(t.astype(np.float64) / T - t_lse[:, None]).sum(1))
     bound = torch.from_numpy(w).double() * T * T * (2 * P * (1 / 12) ** 3 / 6 + (1 + P) * 1e-5)
     assert bool((((a - b) / 2 - (move * grad).sum(1)).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("vocab", [900, 9000, 140001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32],
+                         ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [0.5, 1.0])
+@pytest.mark.parametrize("low", ["lowest", "far", "half"])
+def test_all_others_far_below_the_known_ids(dev, vocab, dtype, T, low):
+    """The cells outside S at the type's lowest value (a mask that is no -inf),
+    some of them twice as low as the others, or moved down by 2^14: q_r is 0,
+    and the cells get -w T p_r times their softmax among themselves, in both
+    passes.  A cell's exponential is off by (4 R + 8) u, R their own range, the
+    sum by 140 u in all."""
+    n, k = 3, 6
+    rng = np.random.default_rng([19, vocab])
+    idx = np.stack([rng.permutation(vocab)[:k] for _ in range(n)]).astype(np.int32)
+    t = rng.normal(size=(n, k)).astype(np.float32)
+    out = np.ones((n, vocab), bool)
+    out[np.arange(n)[:, None], idx] = False
+    z = torch.zeros(n, vocab, dtype=dtype)
+    own = np.zeros((n, vocab))                       # the cells' logits but for a common part
+    if low == "far":
+        own = rng.integers(0, 2, size=(n, vocab)) * 16.0
+        z[:] = torch.from_numpy(own - 2.0 ** 14).to(dtype)
+        own = (z.double().numpy() + 2.0 ** 14) / T   # bf16 and fp16 keep what they can
+    else:
+        bottom = torch.finfo(dtype).min
+        z[:] = bottom
+        if low == "half":
+            z[:, 1::2] = bottom / 2
+            own[:, 0::2] = -np.inf
+    zs = torch.from_numpy(rng.normal(size=(n, k)).astype(np.float32)).to(dtype)
+    z[torch.arange(n)[:, None], torch.from_numpy(idx).long()] = zs
+    s = t.astype(np.float64) / T
+    t_lse = (np.log(np.exp(s).sum(1)) + np.log(1 / np.array([0.7, 0.5, 0.9]))).astype(np.float32)
+    w = np.array([1.0, 0.5, 0.25], np.float32)
+    kw = dict(temperature=T, t_lse=to(dev, t_lse), weight=to(dev, w))
+    got = gq.gptq_distill_loss(z.to(dev), to(dev, idx), to(dev, t), want_grad=True, **kw)
+    back = gq.gptq_distill_backward(z.to(dev), got["stats"], to(dev, idx), to(dev, t),
+                                    torch.ones(n, device=dev), **kw)
+    torch.cuda.synchronize()
+    p = np.exp(s - t_lse[:, None])
+    q = np.exp(zs.double().numpy() / T)
+    want, bound = np.zeros((n, vocab)), np.zeros((n, vocab))
+    for r in range(n):
+        e = np.where(out[r], np.exp(own[r] - own[r][out[r]].max()), 0.0)
+        R = np.ptp(own[r][out[r] & np.isfinite(own[r])])
+        want[r] = -w[r] * T * (1 - p[r].sum()) * e / e.sum()
+        want[r, idx[r]] = w[r] * T * (q[r] / q[r].sum() - p[r])
+        bound[r] = (4 * R + 160) * U * np.abs(want[r])
+        bound[r, idx[r]] = 160 * U * w[r] * T
+    assert bool(torch.isfinite(got["loss"]).all())
+    near(got["dlogits"], want, bound + half_step(dtype, want), "gradient")
+    near(back, want, bound + half_step(dtype, want), "backward")
