@@ -24,8 +24,9 @@
 // (the teacher's probabilities, the two log-sum-exps, the loss, the
 // gradient on S) is in fp64, because the loss's terms nearly cancel where
 // student and teacher agree.  Cells are exponentiated in fp32 and summed in
-// fp32 per thread (at most 128 terms), in fp64 across threads, in a fixed
-// order: results are the same bits from run to run.
+// fp32 per thread (at most 128 and an edge cell; 16 bytes' worth in longer
+// rows), in fp64 beyond that and across threads, in a fixed order: results
+// are the same bits from run to run.
 //
 // Bound by memory where workgroups share a CU, so that one's loads and stores
 // run beside another's exponentials: loss and gradient of 4096 bf16 rows of
@@ -285,8 +286,9 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
     }
   };
   if (fresh) {
-    float part = 0.0f;
+    double own = 0.0;                  // the thread's cells
     if (NV > 0) {
+      float part = 0.0f;
       float m = -INFINITY;
       if (E == 8) {
         // 16-bit cells order like integers as long as one is positive
@@ -339,9 +341,10 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
             part += __builtin_amdgcn_exp2f(fmaf(get_cell<DT>(cell[i], e), cr, -refc));
         }
       }
+      own = double(part);
     } else {
       float run = ez;
-      if (run != -INFINITY) part = 1.0f;
+      if (run != -INFINITY) own = 1.0;
       for (int v = tid; v < nvec; v += THREADS) {
         u32x4 c = load_vec(src + head, v);
         if (tail) take_out(c, v);
@@ -349,17 +352,19 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) m8 = fmax_nan(m8, get_cell<DT>(c, e));
         if (m8 == -INFINITY) continue;
-        if (m8 != run) part *= __builtin_amdgcn_exp2f((run - m8) * cf);
+        if (m8 != run) own *= double(__builtin_amdgcn_exp2f((run - m8) * cf));
         run = m8;
+        float part = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e)
           part += __builtin_amdgcn_exp2f((get_cell<DT>(c, e) - run) * cf);
+        own += double(part);
       }
       mx = block_all<THREADS>(run, redf, fmax_nan);
-      if (run != -INFINITY) part *= __builtin_amdgcn_exp2f((run - mx) * cf);
+      if (run != -INFINITY) own *= double(__builtin_amdgcn_exp2f((run - mx) * cf));
       if (mx != -INFINITY) refer();
     }
-    sum = block_all<THREADS>(double(part), redd, sum2<double>);
+    sum = block_all<THREADS>(own, redd, sum2<double>);
     if (NV == 0 && cr == cf && mx != -INFINITY) sum *= exp2(double(mx) * double(cf) - double(refc));
   }
   // ---- per row, first wave: log-sum-exps, loss, the gradient's factors

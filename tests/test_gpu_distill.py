@@ -486,3 +486,32 @@ def test_all_others_far_below_the_known_ids(dev, vocab, dtype, T, low):
     assert bool(torch.isfinite(got["loss"]).all())
     near(got["dlogits"], want, bound + half_step(dtype, want), "gradient")
     near(back, want, bound + half_step(dtype, want), "backward")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32],
+                         ids=["bf16", "f16", "f32"])
+def test_long_rows_sums_do_not_drift(dev, dtype):
+    """The longest rows: the first half of the cells at 0, the others with an
+    exponential of 1/2 + 7e-6, of which a running fp32 sum in the hundreds loses
+    all but the half, every time (84 u of a thread's 256 cells).  Summed in
+    fp64 beyond a few cells the row is off by an exponential's (4 R + 8) u, R =
+    log 2, and the few cells' 16 u."""
+    V = 262144
+    T = float(np.float32(-1.0 / np.log(0.5 + 7e-6)))
+    z = torch.zeros(2, V, dtype=dtype, device=dev)
+    z[:, V // 2:] = -1.0
+    ti = torch.tensor([[0, V - 1], [5, -1]], dtype=torch.int32, device=dev)
+    tt = torch.zeros(2, 2, device=dev)
+    got = gq.gptq_distill_loss(z, ti, tt, temperature=T, want_grad=True)
+    lse = np.log(V / 2 * (1.0 + np.exp(-1.0 / T)))
+    loss = T * T * np.array([np.log(0.5) + 0.5 / T + lse, lse])
+    off = (4 * np.log(2) + 24) * U
+    err = np.abs(got["loss"].cpu().double().numpy() - loss)
+    assert (err <= T * T * off + U * loss).all(), err / U
+    grad = np.where(np.arange(V) < V // 2, 1.0, np.exp(-1.0 / T)) * T * np.exp(-lse)
+    g = got["dlogits"].cpu().double().numpy()
+    rest = np.ones(V, bool)
+    rest[[0, 5, V - 1]] = False
+    # the cells' own exponential and the sum's
+    bound = 2 * off * grad + half_step(dtype, grad)
+    assert (np.abs(g - grad)[:, rest] <= bound[rest]).all()
