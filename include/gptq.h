@@ -262,7 +262,8 @@ gptq_status gptq_dequant_matmul(const void* X, gptq_dtype x_dtype, int64_t n,
  *   dX[k][c] = sum_r dY[k][r] * W_hat[r][c]
  *
  * dY: bf16 [n, m], row stride lddy >= m (GPTQ_BF16 only); 0 <= n <= 524280.
- * qweight .. signed_codes: the stored format, as in gptq_dequant_matmul.
+ * qweight .. signed_codes: the stored format, as in gptq_dequant_matmul; a
+ * group id outside [0, n_g) counts as the nearest one.
  * dX: bf16 [n, d], row stride lddx >= d; fully overwritten.
  * W_hat is rounded to bf16 once (by at most 2^-8 of it, as dX itself is when
  * stored); products are exact, sums fp32, rounded to bf16 at the end.
@@ -293,7 +294,7 @@ gptq_status gptq_dequant_matmul_t(const void* dY, gptq_dtype dy_dtype, int64_t n
  * Adapters of a smaller rank are stored with zeros up to `rank`.
  *
  * X: bf16 [n, d], row stride ldx >= d; 0 <= n <= 524280; qweight ..
- * signed_codes: as in gptq_dequant_matmul; H: fp32 [n, rank] contiguous, or
+ * signed_codes: as in gptq_dequant_matmul_t; H: fp32 [n, rank] contiguous, or
  * NULL (gptq_lora_backward needs it); Y: [n, m] of y_dtype GPTQ_F32 or
  * GPTQ_BF16 (rounded once, at the end), row stride ldy >= m.  Both are fully
  * overwritten.

@@ -152,6 +152,10 @@ __device__ inline float dot_wave(const uint16_t* __restrict__ x, const uint16_t*
   return s;
 }
 
+// Group of column c, always one of the row's: an id outside counts as the nearest.
+__device__ inline int group_at(const Packed& w, int64_t c) {
+  return min(max(w.g_idx[c], 0), static_cast<int>(w.ng) - 1);
+}
 // Step Delta and code minus zero of weight (r, c).
 __device__ inline float step_at(const Packed& w, int64_t i) {
   return w.scale_f16 ? static_cast<float>(static_cast<const _Float16*>(w.scales)[i])

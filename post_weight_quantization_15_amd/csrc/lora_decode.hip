@@ -329,12 +329,14 @@ __global__ __launch_bounds__(NW * 64, NT == 4 || NJ > 1 ? 2 : 4) void decode_ker
       }
       // The chunk's groups: one, one per step, or steps that mix them.  Decided
       // once a chunk, so that its four steps' chains run side by side.
-      const int G0 = __builtin_amdgcn_readlane(ga[u], 0), G1 = __builtin_amdgcn_readlane(ga[u], 16),
-                G2 = __builtin_amdgcn_readlane(ga[u], 32), G3 = __builtin_amdgcn_readlane(ga[u], 48);
+      // (Ids outside the row's groups count as the nearest; seen to here, not
+      // at their load, which nothing waits for.)
+      const int ia = min(max(ga[u], 0), ng - 1), ib = min(max(gb[u], 0), ng - 1);
+      const int G0 = __builtin_amdgcn_readlane(ia, 0), G1 = __builtin_amdgcn_readlane(ia, 16),
+                G2 = __builtin_amdgcn_readlane(ia, 32), G3 = __builtin_amdgcn_readlane(ia, 48);
       const int own = q == 0 ? G0 : q == 1 ? G1 : q == 2 ? G2 : G3;
-      const uint64_t diff = __ballot(ga[u] != own || gb[u] != own);
+      const uint64_t diff = __ballot(ia != own || ib != own);
       if (!diff && G0 == G1 && G1 == G2 && G2 == G3) {
-        const int gi = min(max(G0, 0), ng - 1);
         // sums of the activations: the same for every fragment of rows
         f32x4 Xs[NT];
 #pragma unroll
@@ -345,7 +347,7 @@ __global__ __launch_bounds__(NW * 64, NT == 4 || NJ > 1 ? 2 : 4) void decode_ker
         }
 #pragma unroll
         for (int f = 0; f < NJ; ++f) {
-          const float2 gr = *reinterpret_cast<const float2*>(&grid[(gi * kRows + 16 * f + c16) * 2]);
+          const float2 gr = *reinterpret_cast<const float2*>(&grid[(G0 * kRows + 16 * f + c16) * 2]);
           const float zz = gr.y + (kMagic ? 16.0f : 0.0f);
           u32x4 m[4];
 #pragma unroll
@@ -367,14 +369,13 @@ __global__ __launch_bounds__(NW * 64, NT == 4 || NJ > 1 ? 2 : 4) void decode_ker
           const int G = s == 0 ? G0 : s == 1 ? G1 : s == 2 ? G2 : G3;
           const f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
           if (!((diff >> (16 * s)) & 0xFFFFu)) {
-            const int gi = min(max(G, 0), ng - 1);
             f32x4 Xs[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) Xs[i] = mfma16(x[u][i][s], ones, z);
 #pragma unroll
             for (int f = 0; f < NJ; ++f) {
               const u32x4 m = run_operand<BITS>(run[f][s]);
-              const float2 gr = *reinterpret_cast<const float2*>(&grid[(gi * kRows + 16 * f + c16) * 2]);
+              const float2 gr = *reinterpret_cast<const float2*>(&grid[(G * kRows + 16 * f + c16) * 2]);
               const float zz = gr.y + (kMagic ? 16.0f : 0.0f);
 #pragma unroll
               for (int i = 0; i < NT; ++i) {
@@ -389,7 +390,7 @@ __global__ __launch_bounds__(NW * 64, NT == 4 || NJ > 1 ? 2 : 4) void decode_ker
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int src = 16 * s + 4 * q + (i >> 1);
-              g8[i] = min(max(__shfl(i & 1 ? gb[u] : ga[u], src), 0), ng - 1);
+              g8[i] = __shfl(i & 1 ? ib : ia, src);
             }
 #pragma unroll
             for (int f = 0; f < NJ; ++f) {

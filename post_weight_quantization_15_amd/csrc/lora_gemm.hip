@@ -303,7 +303,7 @@ __global__ __launch_bounds__(256) void expand_parts_kernel(Packed w, int64_t wor
   for (int i = 0; i < 8; ++i) {
     const int64_t c = 8 * u + i;
     if (c >= w.d) continue;
-    const int64_t g = j * w.ng + w.g_idx[c];
+    const int64_t g = j * w.ng + group_at(w, c);
     const int k = code_at(w, words, j, c) - (w.sgn ? 0 : w.zeros[g]);
     uint16_t p[3];
     split3(step_at(w, g) * static_cast<float>(k), p);
@@ -338,7 +338,7 @@ __device__ inline void expand_transposed(const Packed& w, int64_t words, uint16_
     bool one = true;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      g[i] = w.g_idx[min<int64_t>(c0 + 8 * run + i, w.d - 1)];
+      g[i] = group_at(w, min<int64_t>(c0 + 8 * run + i, w.d - 1));
       one = one && g[i] == g[0];
     }
     uint32_t out[8];

@@ -523,3 +523,24 @@ def test_rows_in_chunks_stay_in_their_workspace(dev):
 def test_lora_gradients_of_rows_in_chunks(dev, case):
     n, m, d, bits, group, order, L, r, kind = case
     check_backward(dev, Layer(m, d, bits, group, order), n, L, r, kind)
+
+
+@pytest.mark.parametrize("group", [-1, 8, 32, 128])
+@pytest.mark.parametrize("n", [5, 150])
+def test_stray_group_ids_are_the_nearest_group_both_ways(dev, group, n):
+    """Ids outside the row's groups are taken as the nearest one by the forward
+    pass and by both gradients alike, in the same bits as ids given so."""
+    c = make_call(dev, n=n, m=130, d=300)
+    lay = Layer(130, 300, 3, group)
+    ng = lay.scales.shape[1]
+    ids = lay.g_idx.copy()
+    ids[[0, 17, 40]] = [-1, -2 ** 31, -5]
+    ids[[8, 200, 299]] = [ng, 2 ** 31 - 1, ng + 3]
+    got = []
+    for g in (ids, np.clip(ids, 0, ng - 1)):
+        lay.g_idx = g
+        c["packed"] = lay.on(dev)
+        Y, H = forward(c)
+        got.append((Y, H, *backward(c, H), gq.gptq_dequant_matmul_t(c["dY"], *c["packed"])))
+        torch.cuda.synchronize()
+    assert same(*got)
