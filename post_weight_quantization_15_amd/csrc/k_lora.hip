@@ -259,9 +259,11 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs args) {
   __shared__ int wcount[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int kg = lane >> 4, c16 = lane & 15;
-  const bool second = blockIdx.x >= args.side[0].blocks;
+  const unsigned block = flat_block();
+  const bool second = block >= args.side[0].blocks;
   const OuterSide& a = args.side[second ? 1 : 0];
-  const unsigned bx = blockIdx.x - (second ? args.side[0].blocks : 0);
+  const unsigned bx = block - (second ? args.side[0].blocks : 0);
+  if (bx >= a.blocks) return;
   const unsigned tiles = static_cast<unsigned>((a.len + kOuterCols - 1) / kOuterCols);
   const int64_t c0 = int64_t(bx % tiles) * kOuterCols;
   const int share = bx / tiles % a.shares, ad = bx / tiles / a.shares;
@@ -398,8 +400,8 @@ __global__ __launch_bounds__(256) void outer_sum_kernel(OuterArgs args, int coun
 }
 
 __global__ void zero_kernel(float* __restrict__ p, int64_t n) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i < n) p[i] = 0.0f;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256)
+    p[i] = 0.0f;
 }
 
 // Shares of the rows per adapter: enough workgroups, at least 256 rows each,
@@ -428,8 +430,8 @@ gptq_status launch_outer(OuterArgs a, int count, hipStream_t st) {
     o.blocks = ceil_div(o.len, kOuterCols) * o.shares * count;
     if (o.shares > 1) sum_blocks[i] = ceil_div(int64_t(a.rank) * o.len * count, 1024);
   }
-  const unsigned grid = a.side[0].blocks + a.side[1].blocks;
-  if (!grid) return GPTQ_OK;
+  if (!(a.side[0].blocks + a.side[1].blocks)) return GPTQ_OK;
+  const dim3 grid = flat_grid(int64_t(a.side[0].blocks) + a.side[1].blocks);
   if (a.rank <= 16) outer_kernel<1><<<grid, 256, 0, st>>>(a);
   else if (a.rank <= 32) outer_kernel<2><<<grid, 256, 0, st>>>(a);
   else if (a.rank <= 64) outer_kernel<4><<<grid, 256, 0, st>>>(a);
@@ -612,8 +614,9 @@ gptq_status launch_lora_backward(const uint16_t* dY, int64_t lddy, int64_t n, co
   if (n == 0) {
     if (accumulate || !adp || (!dA && !dB)) return GPTQ_OK;
     const int64_t na = int64_t(ad.n_adapters) * ad.rank * w.d, nb = int64_t(ad.n_adapters) * ad.rank * w.m;
-    if (dA) zero_kernel<<<ceil_div(na, 256), 256, 0, st>>>(dA, na);
-    if (dB) zero_kernel<<<ceil_div(nb, 256), 256, 0, st>>>(dB, nb);
+    auto blocks = [](int64_t v) { return unsigned(std::min<int64_t>((v + 255) / 256, 4096)); };
+    if (dA) zero_kernel<<<blocks(na), 256, 0, st>>>(dA, na);
+    if (dB) zero_kernel<<<blocks(nb), 256, 0, st>>>(dB, nb);
     GPTQ_CHECK_LAUNCH();
     return GPTQ_OK;
   }

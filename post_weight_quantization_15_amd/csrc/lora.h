@@ -10,6 +10,15 @@ namespace gptq {
 inline unsigned ceil_div(int64_t a, int64_t b) { return static_cast<unsigned>((a + b - 1) / b); }
 inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
+// A launch holds fewer than 2^32 threads in one dimension (more are cut off
+// without an error), and some launches here have a workgroup for every part
+// of every adapter: those go into two dimensions, and the kernel reads the
+// index off both (flat_block; the last row may run past the end).
+inline dim3 flat_grid(int64_t blocks) {
+  const int64_t y = (blocks + (int64_t(1) << 23) - 1) >> 23;
+  return dim3(ceil_div(blocks, y), unsigned(y));
+}
+
 // ---------------------------------------------------------------------------
 // The products Y[t][j] = sum_k V[t][k] M[j][k] (+ the adapters' part) of
 // lora_gemm.hip.  Both operands are bf16 with k contiguous, rows 16-byte
@@ -85,6 +94,8 @@ gptq_status launch_lora_decode(const uint16_t* X, int64_t ldx, int64_t n, const 
 
 #ifdef __HIPCC__
 namespace {
+
+__device__ inline unsigned flat_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
 
 typedef const void __attribute__((address_space(1)))* gvoid;
 typedef void __attribute__((address_space(3)))* lvoid;

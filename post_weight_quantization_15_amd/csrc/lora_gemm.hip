@@ -401,9 +401,9 @@ __device__ inline void turn_tile(const uint16_t* __restrict__ in, int64_t ny, in
 // alpha H as parts; each by its range of blocks (0: not asked for).
 template <int BITS>
 __global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs a, unsigned nw, unsigned wx,
-                                                      unsigned nb, unsigned nta, unsigned) {
+                                                      unsigned nb, unsigned nta, unsigned nh) {
   __shared__ __attribute__((aligned(16))) char lds[kTurnCols * 36 * 4];
-  unsigned b = blockIdx.x;
+  unsigned b = flat_block();
   if (b < nw) {
     expand_transposed<BITS>(a.w, (a.w.d * BITS + 31) / 32, a.Wt, a.mp, b % wx, b / wx, lds);
     return;
@@ -424,6 +424,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs a, unsigned nw
     return;
   }
   b -= nta;
+  if (b >= nh) return;
   const int64_t e = int64_t(b) * 256 + threadIdx.x;
   const int64_t t = e / a.rp;
   const int p = static_cast<int>(e % a.rp);
@@ -992,8 +993,8 @@ gptq_status launch_prepare(const PrepareArgs& a, hipStream_t st) {
   const unsigned nb = a.Bt ? tr * ceil_div(a.mp, 64) * count : 0;
   const unsigned na = a.At ? tr * ceil_div(a.w.d, 64) * count : 0;
   const unsigned nh = a.hparts ? ceil_div(a.n * a.rp, 256) : 0;
-  const unsigned grid = nw + nb + na + nh;
-  if (!grid) return GPTQ_OK;
+  if (!(nw + nb + na + nh)) return GPTQ_OK;
+  const dim3 grid = flat_grid(int64_t(nw) + nb + na + nh);
   switch (a.w.bits) {
     case 2: prepare_kernel<2><<<grid, 256, 0, st>>>(a, nw, wx, nb, na, nh); break;
     case 3: prepare_kernel<3><<<grid, 256, 0, st>>>(a, nw, wx, nb, na, nh); break;

@@ -544,3 +544,44 @@ def test_stray_group_ids_are_the_nearest_group_both_ways(dev, group, n):
         got.append((Y, H, *backward(c, H), gq.gptq_dequant_matmul_t(c["dY"], *c["packed"])))
         torch.cuda.synchronize()
     assert same(*got)
+
+
+def test_as_many_adapters_as_are_taken(dev):
+    """65535 adapters of a wide layer, three of them with a row: more workgroups
+    than one dimension of a launch holds, for the factors turned, for dA, and for
+    zeros over two ranks without rows."""
+    L, m, d = 65535, 8, 32896
+    lay = Layer(m, d, 4, 128)
+    rng = np.random.default_rng(21)
+    use = [0, 40001, 65534]
+    A = torch.zeros(L, 1, d, dtype=torch.bfloat16, device=dev)
+    B = torch.zeros(L, m, 1, dtype=torch.bfloat16, device=dev)
+    alpha = torch.ones(L, device=dev)
+    a, b, al = adapters(rng, 3, 1, m, d)
+    A[use], B[use], alpha[use] = a.to(dev), b.to(dev), al.to(dev)
+    ids = np.array([65534, 0, -1, 40001, 0])
+    X, dY = bf16(rng, 5, d), bf16(rng, 5, m)
+    H = torch.from_numpy(rng.normal(size=(5, 1)).astype(np.float32))
+    dX, dA, dB = gq.gptq_lora_backward(dY.to(dev), X.to(dev), H.to(dev), *lay.on(dev), A, B,
+                                       torch.from_numpy(ids.astype(np.int32)).to(dev), alpha)
+    torch.cuda.synchronize()
+    few = np.array([2, 0, -1, 1, 0])
+    f = lambda t: t.double().numpy()                     # noqa: E731
+    Xo, Ao, Bo = orc.lora_backward(f(dY), f(X), f(H), lay.W, f(a), f(b), f(al), few)
+    size = orc.lora_backward(*(np.abs(v) for v in (f(dY), f(X), f(H), lay.W, f(a), f(b))), f(al), few)
+    near(dX, Xo, (UB + (m + 17) * U * 2) * size[0] + UB * np.abs(Xo), "dX")
+    near(dA[use], Ao, (m + 36) * U * size[1], "dA")
+    near(dB[use], Bo, 32 * U * size[2], "dB")
+    assert int(dA.count_nonzero()) == int(dA[use].count_nonzero())
+    assert int(dB.count_nonzero()) == int(dB[use].count_nonzero())
+    del A, B, dA, dB
+    A = torch.empty(L, 2, d, dtype=torch.bfloat16, device=dev)
+    B = torch.empty(L, m, 2, dtype=torch.bfloat16, device=dev)
+    dA = torch.ones(L, 2, d, device=dev)
+    none = torch.empty(0, d, dtype=torch.bfloat16, device=dev)
+    gq.gptq_lora_backward(none[:, :m].contiguous(), none, torch.empty(0, 2, device=dev), *lay.on(dev), A, B,
+                          torch.empty(0, dtype=torch.int32, device=dev), alpha, dA=dA)
+    torch.cuda.synchronize()
+    assert not bool(dA.any())
+    del A, B, dA
+    torch.cuda.empty_cache()
