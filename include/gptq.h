@@ -267,7 +267,8 @@ gptq_status gptq_dequant_matmul(const void* X, gptq_dtype x_dtype, int64_t n,
  * dX: bf16 [n, d], row stride lddx >= d; fully overwritten.
  * W_hat is rounded to bf16 once (by at most 2^-8 of it, as dX itself is when
  * stored); products are exact, sums fp32, rounded to bf16 at the end.
- * ws: at least gptq_dequant_matmul_t_workspace_bytes(n, m, d) bytes.
+ * ws: at least gptq_dequant_matmul_t_workspace_bytes(n, m, d) bytes, 16-byte
+ * aligned (else WORKSPACE).
  * Errors: INVALID_ARG (bad sizes, m or d > 65535, dtype, bits, group_size,
  *         NULL pointers when n > 0); WORKSPACE; HIP.
  * ------------------------------------------------------------------------- */
@@ -301,8 +302,8 @@ gptq_status gptq_dequant_matmul_t(const void* dY, gptq_dtype dy_dtype, int64_t n
  * The shared product is gptq_dequant_matmul's: exact codes and activations,
  * fp32 sums per group; H is summed and kept in fp32 and enters its product
  * with B as three bf16 parts, i.e. exactly.
- * ws: at least gptq_lora_workspace_bytes(n, m, d, group_size, rank)
- *     bytes.
+ * ws: at least gptq_lora_workspace_bytes(n, m, d, group_size, rank) bytes,
+ *     16-byte aligned (else WORKSPACE).
  * Errors: INVALID_ARG (bad sizes, m or d > 65535, rank outside 1 .. 128,
  *         n_adapters outside 1 .. 65535, dtype, bits, group_size, NULL
  *         pointers when n > 0); WORKSPACE; HIP.
@@ -344,7 +345,8 @@ gptq_status gptq_lora_matmul(const void* X, gptq_dtype x_dtype, int64_t n, int64
  * row get 0 (nothing added).  G and H enter as three bf16 parts, i.e. exactly;
  * sums fp32, over rows in an order fixed by the sizes and ids alone.  With
  * n = 0 the outputs are written (zeros, unless accumulating).
- * ws: at least gptq_lora_backward_workspace_bytes(...) bytes.
+ * ws: at least gptq_lora_backward_workspace_bytes(...) bytes, 16-byte aligned
+ *     (else WORKSPACE).
  * Errors: as gptq_lora_matmul (a pointer that only an output left NULL would
  *         read may be NULL).
  * ------------------------------------------------------------------------- */

@@ -34,8 +34,9 @@ bool valid_adapters(const gptq_adapters* a) {
          a->rank <= kMaxRank;
 }
 
-bool short_ws(const void* ws, size_t have, size_t need) {
-  return have < need || (need > 0 && !ws);
+// Too small, missing, or not aligned as its parts' 16-byte accesses need.
+bool bad_ws(const void* ws, size_t have, size_t need) {
+  return have < need || (need > 0 && (!ws || reinterpret_cast<uintptr_t>(ws) % 16));
 }
 
 }  // namespace
@@ -58,7 +59,7 @@ gptq_status gptq_dequant_matmul_t(const void* dY, gptq_dtype dy_dtype, int64_t n
                     signed_codes) ||
       lddy < m || lddx < d || (n > 0 && (!dY || !dX)))
     return GPTQ_ERR_INVALID_ARG;
-  if (short_ws(ws, ws_bytes, lora_backward_ws_bytes(n, m, d, 0, 0))) return GPTQ_ERR_WORKSPACE;
+  if (bad_ws(ws, ws_bytes, lora_backward_ws_bytes(n, m, d, 0, 0))) return GPTQ_ERR_WORKSPACE;
   const Packed w = make_packed(m, d, qweight, scales, scale_dtype, zeros, g_idx, bits, group_size,
                                signed_codes);
   return launch_lora_backward(static_cast<const uint16_t*>(dY), lddy, n, nullptr, 0, nullptr, w,
@@ -87,7 +88,7 @@ gptq_status gptq_lora_matmul(const void* X, gptq_dtype x_dtype, int64_t n, int64
     return GPTQ_ERR_INVALID_ARG;
   if (n > 0 && (!X || !Y || !adapters->A || !adapters->B || !adapters->alpha || !adapters->row))
     return GPTQ_ERR_INVALID_ARG;
-  if (short_ws(ws, ws_bytes, lora_ws_bytes(n, m, d, group_size, adapters->rank)))
+  if (bad_ws(ws, ws_bytes, lora_ws_bytes(n, m, d, group_size, adapters->rank)))
     return GPTQ_ERR_WORKSPACE;
   if (n == 0) return GPTQ_OK;
   const Packed w = make_packed(m, d, qweight, scales, scale_dtype, zeros, g_idx, bits, group_size,
@@ -123,7 +124,7 @@ gptq_status gptq_lora_backward(const void* dY, gptq_dtype dy_dtype, int64_t n, i
   if (n > 0 && (!dY || !adapters->alpha || !adapters->row || ((dX || dA) && !adapters->B) ||
                 (dX && !adapters->A) || (dA && !X) || (dB && !H)))
     return GPTQ_ERR_INVALID_ARG;
-  if (short_ws(ws, ws_bytes,
+  if (bad_ws(ws, ws_bytes,
                lora_backward_ws_bytes(n, m, d, adapters->rank, adapters->n_adapters)))
     return GPTQ_ERR_WORKSPACE;
   const Packed w = make_packed(m, d, qweight, scales, scale_dtype, zeros, g_idx, bits, group_size,

@@ -167,3 +167,13 @@ def test_binding_checks_shapes():
         with pytest.raises(TypeError):
             k = dict(c, **{key: bad})
             gq._check_adapters(k["A"], k["B"], k["ids"], k["alpha"], 3, 8, 32, dev)
+
+
+def test_a_workspace_off_its_alignment_is_refused(lib):
+    """The workspace's parts are read and written 16 bytes at a time."""
+    for off in (1, 2, 4, 8):
+        assert lora(lib, ws=FAKE + off) == WS
+        assert backward(lib, ws=FAKE + off) == WS
+        assert back(lib, ws=FAKE + off) == WS
+    # where none is needed it is not looked at
+    assert lora(lib, n=0, ws=FAKE + 4, wsb=0) == gq.GPTQ_OK
