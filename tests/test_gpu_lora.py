@@ -585,3 +585,38 @@ def test_as_many_adapters_as_are_taken(dev):
     assert not bool(dA.any())
     del A, B, dA
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("case", [
+    (1, 70, 768, 4, 1, "natural", 3, 128, "one"),            # as many groups as the grids in LDS hold
+    (16, 50, 1536, 2, 2, "act", 3, 16, "each"),
+    (30, 6500, 1530, 3, 2, "natural", 2, 8, "each"),         # ... one fragment of rows a workgroup
+    (128, 3300, 768, 4, 1, "any", 2, 8, "random"),
+    (100, 3300, 768, 4, 2, "natural", 2, 8, "random"),       # ... two
+    (20, 8300, 384, 4, 2, "natural", 2, 8, "each"),          # ... four
+    (1, 8192, 1024, 4, 128, "natural", 2, 128, "one"),       # the largest fused hidden values
+    (1, 8193, 1024, 4, 128, "natural", 2, 128, "one"),
+], ids=lambda c: "n%d_m%d_d%d_b%d_g%d_%s_L%d_r%d_%s" % c)
+def test_lora_at_the_limits_of_the_few_row_kernel(dev, case):
+    n, m, d, bits, group, order, L, r, kind = case
+    check_lora(dev, Layer(m, d, bits, group, order), n, L, r, kind)
+
+
+def unaligned(t):
+    """The same values one element into a buffer."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    return buf[1:].view(t.shape).copy_(t)
+
+
+@pytest.mark.parametrize("n", [1, 20, 60, 300])
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+def test_operands_at_any_element_s_address(dev, monkeypatch, n, bits):
+    def moved(real):
+        shift = lambda v: unaligned(v) if isinstance(v, torch.Tensor) else v     # noqa: E731
+        return lambda *a, **kw: real(*map(shift, a), **{k: shift(v) for k, v in kw.items()})
+
+    for name in ("gptq_lora_matmul", "gptq_lora_backward"):
+        monkeypatch.setattr(gq, name, moved(getattr(gq, name)))
+    lay = Layer(200, 384, bits, 64)
+    check_lora(dev, lay, n, 3, 16, "each")
+    check_backward(dev, lay, n, 3, 16, "each")
