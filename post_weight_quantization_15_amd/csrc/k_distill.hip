@@ -30,13 +30,17 @@
 //
 // Bound by memory where workgroups share a CU, so that one's loads and stores
 // run beside another's exponentials: loss and gradient of 4096 bf16 rows of
-// 64000 cells take 218 us, 4.8 TB/s of the 4.9 that a copy reaches.  A row of
-// 128000 takes a CU's whole register file but for what the code needs, so its
-// loads wait for the row before: 499 us, 4.2 TB/s (with every wave at the
-// known ids, a barrier per sum of theirs and a maximum in fp32 it was 696).
-// Few rows are bound by the chain of one row: 14 us for 24 rows of 32000.
-// Loading the next row into registers that the stores free was tried: its
-// registers spill, 2.1 ms.
+// 64000 cells take 224 us, 4.7 TB/s of the 4.9 that a copy reaches (254 with a
+// class for the rest).  A row of 128000 takes a CU's whole register file but
+// for what the code needs, so its loads wait for the row before: 510 us, 4.1
+// TB/s (545 to 570 with a class for the rest); with every wave at the known
+// ids, a barrier per sum of theirs and a maximum in fp32 it took four tenths
+// more.  Streamed rows move three lengths for the loss and the gradient: 1024
+// rows of 262144 bf16 cells 316 us, of 128000 fp32 cells 320 (the loss alone
+// 102 and 100, the gradient alone 218 and 226).  Few rows are bound by the
+// chain of one row: 11 us for 24 rows of 32000.  Loading the next row into
+// registers that the stores free was tried: its registers spill, four times
+// the time.
 #include <type_traits>
 
 #include "common.h"

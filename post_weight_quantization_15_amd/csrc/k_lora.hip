@@ -24,8 +24,8 @@ namespace {
 // sums meet in LDS.  Rows are independent in the product, so a tile with
 // several adapters runs once per adapter and keeps each adapter's rows.
 // Read once per adapter of the tile: 32 rows of V from HBM, rank rows of
-// M from L2.  Bound by memory: 8192 rows of 4096, rank 16, 33 us (2.0 TB/s);
-// 16384 rows, rank 64, 73 us.
+// M from L2.  Bound by memory: 8192 rows of 4096, rank 16, 32 us (2.1 TB/s);
+// 16384 rows, rank 64, 72 us.
 // ---------------------------------------------------------------------------
 struct ShrinkArgs {
   const uint16_t* V;
@@ -404,7 +404,7 @@ __global__ void zero_kernel(float* __restrict__ p, int64_t n) {
     p[i] = 0.0f;
 }
 
-// Shares of the rows per adapter: enough workgroups, at least 256 rows each,
+// Shares of the rows per adapter: enough workgroups, more than 128 rows each,
 // and sums of at most 64 (adapter, share) pairs and 256 MB.
 int outer_shares(int64_t n, int64_t len, int rank, int count) {
   int64_t s = 1024 / int64_t(ceil_div(len, kOuterCols));

@@ -19,9 +19,9 @@
 // Delta (code - zero) per column in fp32 and multiplies its three bf16 parts.
 // The grids of the rows lie in LDS for both.
 //
-// One token through 4096 x 4096 in 4 bits takes 10.9 us on the card (9.3 MB,
+// One token through 4096 x 4096 in 4 bits takes 11.0 us on the card (9.3 MB,
 // bound by the chain load - product - sum of one workgroup and its launch), 16
-// tokens through 11008 x 4096 19.9 us (33 MB with the adapters' factors, 1.7
+// tokens through 11008 x 4096 20.0 us (33 MB with the adapters' factors, 1.7
 // TB/s: bound by the activations' operands, which every workgroup reads from
 // L2, and the loads' latency).  Beyond 128 rows, or 768 groups a row, the
 // laid-out product takes over.

@@ -448,13 +448,15 @@ __global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs a, unsigned nw
 // a lane then holds four consecutive j of one activation row, 16 bytes that
 // turn through LDS at the end into whole lines of the result.
 //
-// Reaches 1190 TFLOP/s without a fold on 256 x 256 tiles (8192 rows of 11008
-// into 4096: 621 us; 8192 rows of 4096 into 11008: 695, 781 on 256 x 128) and
-// 730 with a fold every 64 columns (256 x 128, two sets of accumulators;
-// 16384 rows of 4096 into 11008: 2.03 ms), against 1430 of a large library
-// product.  Matrix instructions alone take 474 us of the second on 256 x 128,
-// with the barriers 542, with either the copies or the LDS reads about 700: no
-// one of them bounds it, their overlap does.
+// Reaches 1370 TFLOP/s without a fold on 256 x 256 tiles (8192 rows of 11008
+// into 4096: 539 us; 8192 rows of 4096 into 11008: 586, 1260 TFLOP/s) and 764
+// with a fold every 64 columns (256 x 128, two sets of accumulators; 16384
+// rows of 4096 into 11008: 1.93 ms), against 1430 of a large library product.
+// These are times among calls that have run for a while; in the first some
+// twenty after a pause the card's clock drops, and they are up to a quarter
+// longer.  Measured so, the second took 695, on 256 x 128 tiles 781: matrix
+// instructions alone 474 of it, with the barriers 542, with either the copies
+// or the LDS reads about 700: no one of them bounds it, their overlap does.
 // ---------------------------------------------------------------------------
 constexpr int kBk = 64;
 

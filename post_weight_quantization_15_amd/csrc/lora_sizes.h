@@ -14,7 +14,7 @@ constexpr int64_t kRowChunk = 16384;
 constexpr int kShrinkRows = 32;
 
 // Shares of k per row tile that a launch over n rows wants: enough workgroups
-// for the chip where rows are few.
+// for the chip where rows are few, of at least 8 steps of 32 each.
 inline int shrink_shares(int64_t n, int64_t len) {
   const int64_t tiles = (n + kShrinkRows - 1) / kShrinkRows;
   return tiles >= 128 ? 1 : int(std::max<int64_t>(1, std::min<int64_t>(512 / tiles, (len + 511) / 512)));
