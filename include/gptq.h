@@ -302,6 +302,8 @@ gptq_status gptq_dequant_matmul_t(const void* dY, gptq_dtype dy_dtype, int64_t n
  * The shared product is gptq_dequant_matmul's: exact codes and activations,
  * fp32 sums per group; H is summed and kept in fp32 and enters its product
  * with B as three bf16 parts, i.e. exactly.
+ * An activation that is not finite makes its own row's Y not finite (NaN also
+ * where inf times a weight has a sign), and no other row's.
  * ws: at least gptq_lora_workspace_bytes(n, m, d, group_size, rank) bytes,
  *     16-byte aligned (else WORKSPACE).
  * Errors: INVALID_ARG (bad sizes, m or d > 65535, rank outside 1 .. 128,
