@@ -422,6 +422,57 @@ gptq_status gptq_distill_backward(const void* logits, gptq_dtype dtype, int64_t 
                                   int64_t ldd, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * What rows of logits say about given tokens: how likely each is, how spread
+ * the row's distribution is, and the row's largest logits.  Scores a quantized
+ * model, and makes from a teacher's logits what gptq_distill_loss reads
+ * (top_idx as t_idx, top_logits as t_logits, lse as t_lse).  With z = logits /
+ * T, q = softmax(z):
+ *   logp = log q_token,  entropy = - sum q log q,  lse = log sum exp z,
+ *   top: the k largest logits in descending order, equal ones by lower id.
+ *
+ * logits: [n, vocab] of dtype GPTQ_BF16, GPTQ_F16 or GPTQ_F32, row stride ldl
+ *   >= vocab; 1 <= vocab <= 262144; n <= 2097152.
+ * tokens: int32 [n]; an id outside [0, vocab) asks for none (logp 0); may be
+ *   NULL where logp is.
+ * logp, entropy, lse: fp32 [n], each may be NULL.  stats: fp32 [n, 3] or NULL,
+ *   for the gradient: a logit r of the row, the log of sum exp((x - r) / T),
+ *   and the entropy.
+ * top_logits fp32 [n, k] (the logits themselves, not over T), top_idx int32
+ *   [n, k]: 0 <= k <= 512, k <= vocab; may be NULL where k = 0.
+ * A logit of -inf has probability 0 and is chosen behind all others.  NaN and
+ * +inf make logp, entropy and lse NaN, and so does a row of nothing but -inf
+ * (lse: -inf); a row of nothing but the type's lowest value is a row of equal
+ * logits.  NaN is never among the largest; where fewer than k logits are
+ * numbers the rest of top_idx is -1, of top_logits -inf.
+ * Cells are exponentiated in fp32, summed in fp32 for 32 cells and in fp64
+ * beyond.  Results are the same bits from run to run.  Rows whose logits rise
+ * along the vocabulary take up to some ten times as long for their largest.
+ * ws: at least gptq_token_logprobs_workspace_bytes(n, vocab, k) bytes, 16-byte
+ *   aligned (else WORKSPACE).
+ * Errors: INVALID_ARG (bad sizes, dtype, k, temperature outside 1e-30 .. 1e30,
+ *         NULL pointers when n > 0); WORKSPACE; HIP.
+ * ------------------------------------------------------------------------- */
+size_t gptq_token_logprobs_workspace_bytes(int64_t n, int64_t vocab, int64_t k);
+gptq_status gptq_token_logprobs(const void* logits, gptq_dtype dtype, int64_t n, int64_t vocab,
+                                int64_t ldl, const int32_t* tokens, float temperature,
+                                int64_t k, float* logp, float* entropy, float* lse,
+                                float* stats, float* top_logits, int32_t* top_idx, void* ws,
+                                size_t ws_bytes, void* stream);
+/* The gradient of sum(grad_logp logp + grad_entropy entropy) with respect to
+ * the logits, from the stats of the forward call on the same arguments:
+ *   dlogits_v = [g (1[v = token] - q_v) - h q_v (log q_v + entropy)] / T,
+ * g = grad_logp fp32 [n] or NULL (0), h = grad_entropy fp32 [n] or NULL (0); g
+ * is 0 for a row without a token.  A row whose g and h are both 0 is not read:
+ * its gradient is 0 whatever its logits hold.  dlogits: in the logits' dtype,
+ * row stride ldd >= vocab; it may be the logits' own buffer (same pointer and
+ * stride).  Errors as above; no workspace. */
+gptq_status gptq_token_logprobs_backward(const void* logits, gptq_dtype dtype, int64_t n,
+                                         int64_t vocab, int64_t ldl, const float* stats,
+                                         const int32_t* tokens, float temperature,
+                                         const float* grad_logp, const float* grad_entropy,
+                                         void* dlogits, int64_t ldd, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Layer by layer ([derivation] 3.2 steps 1-2 and 10: capture each layer's
  * inputs, quantize it, verify its reconstruction error, go on to the next;
  * [teardown] "layer-wise quantization").
@@ -470,6 +521,116 @@ gptq_status gptq_quantize_stack(const gptq_stack_layer* layers, int32_t n_layers
                                 const void* X_in, int64_t n_tok, int32_t activation,
                                 void* X_out, double* layer_err, void* ws,
                                 size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Layers and activations in 4-bit floating point (MXFP4): values 0, 1/2, 1,
+ * 3/2, 2, 3, 4, 6 and their negatives (e2m1) in blocks of 32 along a row, a
+ * block's values times one power of two.  The format that the matrix cores
+ * take directly, for layers that need no integer grid and for activations.
+ *
+ * Stored format of a matrix [rows, d], nb = ceil(d / 32):
+ *   codes  uint8 [rows, 16 nb] contiguous, 16-byte aligned: the code (sign,
+ *          two bits of exponent, one of mantissa) of column c in byte c / 2,
+ *          even columns in the lower half; 0 past d;
+ *   scales uint8 [rows, nb] contiguous: 127 + the power of two of each block;
+ *          255: the block is NaN.
+ *
+ * gptq_mx_quantize rounds X [n, d] (bf16, fp16 or fp32, row stride ldx >=
+ * d) to it.  The power of a block is floor(log2 max |x|) - 2, at least -127
+ * (which a block of zeros gets), so that its largest value lies at 4 to 8;
+ * values go to the nearest, halves to the even code, beyond 6 to 6.  A block
+ * with a value that is not finite is NaN as a whole.  hat: the values that
+ * the codes stand for, [n, d] in X's type (exact in it), row stride ldh >= d,
+ * or NULL.  0 <= n <= 524280, d <= 65535.
+ * Errors: INVALID_ARG (bad sizes, dtype, alignment, NULL pointers when n > 0);
+ *         HIP.  Allocates nothing; no workspace.
+ * ------------------------------------------------------------------------- */
+gptq_status gptq_mx_quantize(const void* X, gptq_dtype dtype, int64_t n, int64_t d,
+                                int64_t ldx, uint8_t* codes, uint8_t* scales, void* hat,
+                                int64_t ldh, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The product with such a layer W [m, d]:  Y[k][r] = sum_c X[k][c] W[r][c].
+ *
+ * x_form: GPTQ_MX_BF16: X bf16 [n, d], row stride ldx >= d, as it is;
+ *   GPTQ_MX_ROUND: the same, rounded as gptq_mx_quantize does (the result
+ *   is that of the two calls); GPTQ_MX_CODES: X codes uint8 [n, 16 nb] and
+ *   x_scales [n, nb], as gptq_mx_quantize writes them (ldx ignored), for
+ *   activations that several products share.  x_scales is read only then.
+ * Y: [n, m] of y_dtype GPTQ_F32 or GPTQ_BF16 (rounded once, at the end), row
+ *   stride ldy >= m; fully overwritten.  Any n from 0 to 524280.
+ * Every product is exact, sums are fp32.  Values beyond 2^127 (scale bytes
+ * from 253 on, which no finite input gets) count as infinite with bf16
+ * activations.  A block that is NaN, or an activation that is not finite, makes
+ * its row's (its column's) results NaN or infinite and no others.
+ * ws: at least gptq_mx_matmul_workspace_bytes(n, m, d, x_form) bytes,
+ *   16-byte aligned (else WORKSPACE).
+ * Errors: INVALID_ARG (bad sizes, m or d > 65535, x_form, dtype, alignment,
+ *         NULL pointers when n > 0); WORKSPACE; HIP.
+ * ------------------------------------------------------------------------- */
+typedef enum gptq_mx_input {
+  GPTQ_MX_BF16 = 0, GPTQ_MX_ROUND = 1, GPTQ_MX_CODES = 2
+} gptq_mx_input;
+
+size_t gptq_mx_matmul_workspace_bytes(int64_t n, int64_t m, int64_t d, int32_t x_form);
+gptq_status gptq_mx_matmul(const void* X, int32_t x_form, const uint8_t* x_scales, int64_t n,
+                              int64_t d, int64_t ldx, const uint8_t* codes,
+                              const uint8_t* scales, int64_t m, void* Y, gptq_dtype y_dtype,
+                              int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Its gradient with respect to X as it is (through the frozen layer; for
+ * rounded activations the one of the unrounded product):
+ *   dX[k][c] = sum_r dY[k][r] W[r][c]
+ * dY: bf16 [n, m], row stride lddy >= m; dX: bf16 [n, d], row stride lddx >= d,
+ * fully overwritten.  Products are exact, sums fp32, rounded once at the end.
+ * ws: at least gptq_mx_matmul_t_workspace_bytes(n, m, d) bytes, 16-byte
+ * aligned (else WORKSPACE).  Errors as in gptq_mx_matmul.
+ * ------------------------------------------------------------------------- */
+size_t gptq_mx_matmul_t_workspace_bytes(int64_t n, int64_t m, int64_t d);
+gptq_status gptq_mx_matmul_t(const void* dY, gptq_dtype dy_dtype, int64_t n, int64_t m,
+                                int64_t lddy, const uint8_t* codes, const uint8_t* scales,
+                                int64_t d, void* dX, int64_t lddx, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward block on two such layers [m, d],
+ *   G = X W_gate^T,  U = X W_up^T,  Y = act(G) * U
+ * with both products, the activation (gptq_activation) and the product of the
+ * two in one pass; the block's third layer takes Y through gptq_mx_matmul.
+ * X, x_form, x_scales, d, ldx: as in gptq_mx_matmul.  Y: bf16 [n, m], row
+ * stride ldy >= m, from G and U in fp32.  G, U: bf16 [n, m] with row stride
+ * ldg >= m for gptq_mx_gated_backward, or both NULL.
+ * ws: at least gptq_mx_gated_workspace_bytes(n, m, d, x_form) bytes, 16-byte
+ * aligned (else WORKSPACE).
+ *
+ * Its gradients, from dY bf16 [n, m] (row stride lddy >= m) and the G and U
+ * that the forward call wrote:
+ *   dU = dY act(G),  dG = dY U act'(G),  dX = dG W_gate + dU W_up
+ * (ReLU's slope at 0 is 0; for rounded activations dX is that of the
+ * unrounded product).  dGU: bf16 [n, 2 mp] contiguous, 16-byte aligned, mp =
+ * m rounded up to 64: dG in columns [0, m), dU in [mp, mp + m), zeros between
+ * and behind.  dX: bf16 [n, d], row stride lddx >= d, from dG and dU as rounded
+ * to bf16; or NULL (then neither the layers nor ws are read).
+ * ws: at least gptq_mx_gated_backward_workspace_bytes(n, m, d) bytes,
+ * 16-byte aligned (else WORKSPACE).
+ * Errors: as in gptq_mx_matmul; INVALID_ARG also for a bad activation and
+ *         for G without U.
+ * ------------------------------------------------------------------------- */
+size_t gptq_mx_gated_workspace_bytes(int64_t n, int64_t m, int64_t d, int32_t x_form);
+gptq_status gptq_mx_gated(const void* X, int32_t x_form, const uint8_t* x_scales, int64_t n,
+                             int64_t d, int64_t ldx, const uint8_t* gate_codes,
+                             const uint8_t* gate_scales, const uint8_t* up_codes,
+                             const uint8_t* up_scales, int64_t m, int32_t activation, void* Y,
+                             int64_t ldy, void* G, void* U, int64_t ldg, void* ws,
+                             size_t ws_bytes, void* stream);
+size_t gptq_mx_gated_backward_workspace_bytes(int64_t n, int64_t m, int64_t d);
+gptq_status gptq_mx_gated_backward(const void* dY, gptq_dtype dy_dtype, int64_t n, int64_t m,
+                                      int64_t lddy, const void* G, const void* U, int64_t ldg,
+                                      const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                      const uint8_t* up_codes, const uint8_t* up_scales,
+                                      int64_t d, int32_t activation, void* dX, int64_t lddx,
+                                      void* dGU, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Tracing: per-phase GPU time.  While enabled, each launch group of a phase

@@ -22,6 +22,11 @@ __all__ = [
     "gptq_lora_matmul", "gptq_lora_backward", "gptq_lora_workspace_bytes",
     "gptq_lora_backward_workspace_bytes", "gptq_dequant_matmul_t_workspace_bytes",
     "gptq_distill_loss", "gptq_distill_backward", "gptq_quantize_stack",
+    "gptq_mx_quantize", "gptq_mx_matmul", "gptq_mx_matmul_t", "gptq_mx_gated",
+    "gptq_mx_gated_backward", "gptq_mx_matmul_workspace_bytes",
+    "gptq_mx_matmul_t_workspace_bytes", "gptq_mx_gated_workspace_bytes",
+    "gptq_mx_gated_backward_workspace_bytes", "gptq_token_logprobs",
+    "gptq_token_logprobs_backward", "gptq_token_logprobs_workspace_bytes",
     "gptq_trace_enable", "gptq_trace_read", "TRACE_PHASES",
     "EXPORTED_SYMBOLS", "GRIDS", "ACTIVATIONS", "GPTQ_OK", "GPTQ_ERR_INVALID_ARG", "GPTQ_ERR_NOT_SPD",
     "GPTQ_ERR_WORKSPACE", "GPTQ_ERR_HIP",
@@ -40,6 +45,11 @@ EXPORTED_SYMBOLS = (
     "gptq_trace_read", "gptq_dequant_matmul_t_workspace_bytes", "gptq_dequant_matmul_t",
     "gptq_lora_workspace_bytes", "gptq_lora_matmul", "gptq_lora_backward_workspace_bytes",
     "gptq_lora_backward", "gptq_distill_loss", "gptq_distill_backward",
+    "gptq_mx_quantize", "gptq_mx_matmul_workspace_bytes", "gptq_mx_matmul",
+    "gptq_mx_matmul_t_workspace_bytes", "gptq_mx_matmul_t",
+    "gptq_mx_gated_workspace_bytes", "gptq_mx_gated",
+    "gptq_mx_gated_backward_workspace_bytes", "gptq_mx_gated_backward",
+    "gptq_token_logprobs_workspace_bytes", "gptq_token_logprobs", "gptq_token_logprobs_backward",
 )
 TRACE_PHASES = ("stats", "factor", "chain", "lazy", "other")
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2}
@@ -130,6 +140,35 @@ def load_library():
     lib.gptq_distill_backward.restype = ctypes.c_int
     lib.gptq_distill_backward.argtypes = [vp, dt, i64, i64, i64, vp, vp, vp, i64, f32, vp, vp, vp,
                                           vp, i64, vp]
+    lib.gptq_mx_quantize.restype = ctypes.c_int
+    lib.gptq_mx_quantize.argtypes = [vp, dt, i64, i64, i64, vp, vp, vp, i64, vp]
+    lib.gptq_mx_matmul_workspace_bytes.restype = sz
+    lib.gptq_mx_matmul_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.gptq_mx_matmul.restype = ctypes.c_int
+    lib.gptq_mx_matmul.argtypes = [vp, i32, vp, i64, i64, i64, vp, vp, i64, vp, dt, i64, vp, sz,
+                                      vp]
+    lib.gptq_mx_matmul_t_workspace_bytes.restype = sz
+    lib.gptq_mx_matmul_t_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.gptq_mx_matmul_t.restype = ctypes.c_int
+    lib.gptq_mx_matmul_t.argtypes = [vp, dt, i64, i64, i64, vp, vp, i64, vp, i64, vp, sz, vp]
+    lib.gptq_mx_gated_workspace_bytes.restype = sz
+    lib.gptq_mx_gated_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.gptq_mx_gated.restype = ctypes.c_int
+    lib.gptq_mx_gated.argtypes = [vp, i32, vp, i64, i64, i64, vp, vp, vp, vp, i64, i32, vp, i64,
+                                     vp, vp, i64, vp, sz, vp]
+    lib.gptq_mx_gated_backward_workspace_bytes.restype = sz
+    lib.gptq_mx_gated_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.gptq_mx_gated_backward.restype = ctypes.c_int
+    lib.gptq_mx_gated_backward.argtypes = [vp, dt, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64,
+                                              i32, vp, i64, vp, vp, sz, vp]
+    lib.gptq_token_logprobs_workspace_bytes.restype = sz
+    lib.gptq_token_logprobs_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.gptq_token_logprobs.restype = ctypes.c_int
+    lib.gptq_token_logprobs.argtypes = [vp, dt, i64, i64, i64, vp, f32, i64, vp, vp, vp, vp, vp, vp,
+                                        vp, sz, vp]
+    lib.gptq_token_logprobs_backward.restype = ctypes.c_int
+    lib.gptq_token_logprobs_backward.argtypes = [vp, dt, i64, i64, i64, vp, vp, f32, vp, vp, vp, i64,
+                                                 vp]
     sp = ctypes.POINTER(_StackLayer)
     lib.gptq_stack_workspace_bytes.restype = sz
     lib.gptq_stack_workspace_bytes.argtypes = [sp, i32, i64]
@@ -691,6 +730,267 @@ def gptq_distill_backward(logits: torch.Tensor, stats: torch.Tensor, t_idx: torc
             t_logits.data_ptr(), k, temperature, None if t_lse is None else t_lse.data_ptr(),
             None if weight is None else weight.data_ptr(), grad.data_ptr(), dlogits.data_ptr(), ldd)
     return dlogits
+
+
+# ---------------------------------------------------------------------------
+# Given tokens of rows of logits
+# ---------------------------------------------------------------------------
+
+def gptq_token_logprobs_workspace_bytes(n: int, vocab: int, k: int) -> int:
+    return int(_lib().gptq_token_logprobs_workspace_bytes(n, vocab, k))
+
+
+def gptq_token_logprobs(logits: torch.Tensor, tokens=None, k: int = 0, temperature: float = 1.0,
+                        ws=None) -> dict:
+    """Statistics of the rows of logits [n, vocab] (bfloat16, float16 or
+    float32) at a temperature: {"logp": the log probability of tokens int32
+    [n] (outside [0, vocab): 0; None without tokens), "entropy", "lse": fp32
+    [n], "stats": fp32 [n, 3] (for gptq_token_logprobs_backward), "top_logits":
+    fp32 [n, k], "top_idx": int32 [n, k]: the k largest logits, equal ones by
+    lower id (None with k = 0)}.  top_idx, top_logits and lse are a teacher's
+    t_idx, t_logits and t_lse in gptq_distill_loss."""
+    ldl = _gpu_rows(logits, "logits", None, tuple(_LOGITS))
+    dev = _gpu_device(logits)
+    n, vocab = logits.shape
+    if tokens is not None:
+        _like(tokens, "tokens", torch.int32, (n,), dev)
+    lib = _lib()
+    ws = _enough(ws, lib.gptq_token_logprobs_workspace_bytes(n, vocab, k), dev)
+    out = torch.empty(6 * n, dtype=_F32, device=dev)
+    logp, entropy, lse, stats = out[:n], out[n:2 * n], out[2 * n:3 * n], out[3 * n:].view(n, 3)
+    top = torch.empty(n, k, dtype=_F32, device=dev) if k > 0 else None
+    idx = torch.empty(n, k, dtype=torch.int32, device=dev) if k > 0 else None
+    at = out.data_ptr()
+    _launch(dev, "gptq_token_logprobs", lib.gptq_token_logprobs, logits.data_ptr(),
+            _LOGITS[logits.dtype], n, vocab, ldl, None if tokens is None else tokens.data_ptr(),
+            temperature, k, None if tokens is None else at, at + 4 * n, at + 8 * n, at + 12 * n,
+            None if top is None else top.data_ptr(), None if idx is None else idx.data_ptr(),
+            ws.data_ptr(), ws.numel() * ws.element_size())
+    return dict(logp=None if tokens is None else logp, entropy=entropy, lse=lse, stats=stats,
+                top_logits=top, top_idx=idx)
+
+
+def gptq_token_logprobs_backward(logits: torch.Tensor, stats: torch.Tensor, tokens=None,
+                                 grad_logp=None, grad_entropy=None, temperature: float = 1.0,
+                                 dlogits=None) -> torch.Tensor:
+    """The gradient of sum(grad_logp logp + grad_entropy entropy), both fp32
+    [n] or None, with respect to the logits, in their dtype, from the stats of
+    gptq_token_logprobs on the same arguments; dlogits may be the logits' own
+    tensor."""
+    ldl = _gpu_rows(logits, "logits", None, tuple(_LOGITS))
+    dev = _gpu_device(logits)
+    n, vocab = logits.shape
+    _like(stats, "stats", _F32, (n, 3), dev)
+    if tokens is not None:
+        _like(tokens, "tokens", torch.int32, (n,), dev)
+    elif grad_logp is not None:
+        raise ValueError("grad_logp needs tokens")
+    if grad_logp is not None:
+        _like(grad_logp, "grad_logp", _F32, (n,), dev)
+    if grad_entropy is not None:
+        _like(grad_entropy, "grad_entropy", _F32, (n,), dev)
+    dlogits, ldd = _dlogits(dlogits, logits, dev)
+    _launch(dev, "gptq_token_logprobs_backward", _lib().gptq_token_logprobs_backward,
+            logits.data_ptr(), _LOGITS[logits.dtype], n, vocab, ldl, stats.data_ptr(),
+            None if tokens is None else tokens.data_ptr(), temperature,
+            None if grad_logp is None else grad_logp.data_ptr(),
+            None if grad_entropy is None else grad_entropy.data_ptr(), dlogits.data_ptr(), ldd)
+    return dlogits
+
+
+# ---------------------------------------------------------------------------
+# Layers and activations in 4-bit floating point
+# ---------------------------------------------------------------------------
+
+_MX_BF16, _MX_ROUND, _MX_CODES = range(3)
+
+
+def _check_mx(codes, scales, name, blocks, dev):
+    """Checks a matrix [rows, 32 blocks] in the stored format; returns its rows."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError(f"{name} codes must be [rows, 16 blocks]")
+    rows = codes.shape[0]
+    _like(codes, f"{name} codes", torch.uint8, (rows, 16 * blocks), dev)
+    _like(scales, f"{name} scales", torch.uint8, (rows, blocks), dev)
+    return rows
+
+
+def _mx_input(X, x_scales, quantize_x, blocks):
+    """Checks the activations of a product with layers of `blocks` blocks (None:
+    as X has); returns (form, row stride, scales' pointer, n, d, device)."""
+    if isinstance(X, torch.Tensor) and X.dtype is torch.uint8:
+        if x_scales is None or quantize_x:
+            raise ValueError("X as codes needs x_scales, and is quantized already")
+        dev = _gpu_device(X)
+        n = _check_mx(X, x_scales, "X", blocks, dev)
+        return _MX_CODES, 0, x_scales.data_ptr(), n, 32 * blocks, dev
+    if x_scales is not None:
+        raise ValueError("x_scales belongs to X as codes (uint8)")
+    ldx = _gpu_rows(X, "X")
+    dev = _gpu_device(X)
+    n, d = X.shape
+    if -(-d // 32) != blocks:
+        raise ValueError(f"X has {d} columns, the layer {blocks} blocks of 32")
+    return (_MX_ROUND if quantize_x else _MX_BF16), ldx, None, n, d, dev
+
+
+def gptq_mx_matmul_workspace_bytes(n: int, m: int, d: int, x_form: int) -> int:
+    return int(_lib().gptq_mx_matmul_workspace_bytes(n, m, d, x_form))
+
+
+def gptq_mx_matmul_t_workspace_bytes(n: int, m: int, d: int) -> int:
+    return int(_lib().gptq_mx_matmul_t_workspace_bytes(n, m, d))
+
+
+def gptq_mx_gated_workspace_bytes(n: int, m: int, d: int, x_form: int) -> int:
+    return int(_lib().gptq_mx_gated_workspace_bytes(n, m, d, x_form))
+
+
+def gptq_mx_gated_backward_workspace_bytes(n: int, m: int, d: int) -> int:
+    return int(_lib().gptq_mx_gated_backward_workspace_bytes(n, m, d))
+
+
+def gptq_mx_quantize(X: torch.Tensor, want_hat: bool = False, codes=None, scales=None,
+                        hat=None) -> dict:
+    """X [n, d] (bfloat16, float16 or float32) in 4-bit floating point: {"codes":
+    uint8 [n, 16 ceil(d / 32)], two values a byte, the even column's in the
+    lower half, "scales": uint8 [n, ceil(d / 32)], 127 + the power of two of
+    each block of 32 columns (255: a block with a value that is not finite),
+    and with want_hat (or hat given) "hat": the values that the codes stand
+    for, in X's dtype}."""
+    ldx = _gpu_rows(X, "X", None, tuple(_LOGITS))
+    dev = _gpu_device(X)
+    n, d = X.shape
+    blocks = -(-d // 32)
+    codes = _out(codes, "codes", torch.uint8, (n, 16 * blocks), dev)
+    scales = _out(scales, "scales", torch.uint8, (n, blocks), dev)
+    if want_hat or hat is not None:
+        hat = _out(hat, "hat", X.dtype, (n, d), dev)
+    _launch(dev, "gptq_mx_quantize", _lib().gptq_mx_quantize, X.data_ptr(), _LOGITS[X.dtype],
+            n, d, ldx, codes.data_ptr(), scales.data_ptr(), None if hat is None else hat.data_ptr(),
+            d)
+    out = dict(codes=codes, scales=scales)
+    if hat is not None:
+        out["hat"] = hat
+    return out
+
+
+def gptq_mx_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                      quantize_x: bool = False, x_scales=None, Y=None, out_dtype=torch.float32,
+                      ws=None) -> torch.Tensor:
+    """Y [n, m] = X W^T for a layer W [m, d] as gptq_mx_quantize stores it.
+
+    X is bfloat16 [n, d], taken as it is or (quantize_x) rounded to 4 bits as
+    gptq_mx_quantize does, or the codes of that call with their x_scales.
+    Y is float32 or bfloat16 (out_dtype, or the given Y's)."""
+    if scales.dim() != 2:
+        raise ValueError("scales must be [m, blocks]")
+    form, ldx, xs, n, d, dev = _mx_input(X, x_scales, quantize_x, scales.shape[1])
+    m = _check_mx(codes, scales, "layer", scales.shape[1], dev)
+    if Y is not None:
+        out_dtype = Y.dtype
+    if out_dtype is not _F32 and out_dtype is not _BF16:
+        raise TypeError(f"Y must be float32 or bfloat16, got {out_dtype}")
+    lib = _lib()
+    ws = _enough(ws, lib.gptq_mx_matmul_workspace_bytes(n, m, d, form), dev)
+    Y = _out(Y, "Y", out_dtype, (n, m), dev)
+    _launch(dev, "gptq_mx_matmul", lib.gptq_mx_matmul, X.data_ptr(), form, xs, n, d, ldx,
+            codes.data_ptr(), scales.data_ptr(), m, Y.data_ptr(),
+            GPTQ_F32 if out_dtype is _F32 else GPTQ_BF16, m, ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    return Y
+
+
+def gptq_mx_matmul_t(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, d: int,
+                        dX=None, ws=None) -> torch.Tensor:
+    """dX bf16 [n, d] = dY W for dY bf16 [n, m]: the gradient of
+    gptq_mx_matmul with respect to its activations."""
+    ldy = _gpu_rows(dY, "dY")
+    dev = _gpu_device(dY)
+    n, m = dY.shape
+    if _check_mx(codes, scales, "layer", -(-d // 32), dev) != m:
+        raise ValueError(f"the layer must have {m} rows")
+    lib = _lib()
+    ws = _enough(ws, lib.gptq_mx_matmul_t_workspace_bytes(n, m, d), dev)
+    dX = _out(dX, "dX", _BF16, (n, d), dev)
+    _launch(dev, "gptq_mx_matmul_t", lib.gptq_mx_matmul_t, dY.data_ptr(), GPTQ_BF16, n, m, ldy,
+            codes.data_ptr(), scales.data_ptr(), d, dX.data_ptr(), d, ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    return dX
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def gptq_mx_gated(X: torch.Tensor, gate_codes: torch.Tensor, gate_scales: torch.Tensor,
+                     up_codes: torch.Tensor, up_scales: torch.Tensor, activation: str = "silu",
+                     quantize_x: bool = False, x_scales=None, want_parts: bool = False, Y=None,
+                     ws=None):
+    """Y bf16 [n, m] = act(G) * U with G = X W_gate^T and U = X W_up^T, for two
+    layers [m, d] as gptq_mx_quantize stores them; X, quantize_x and
+    x_scales as in gptq_mx_matmul.  Returns Y, or (Y, G, U) with both
+    factors in bf16 where want_parts is set (gptq_mx_gated_backward needs
+    them)."""
+    act = _activation(activation)
+    if gate_scales.dim() != 2:
+        raise ValueError("gate_scales must be [m, blocks]")
+    blocks = gate_scales.shape[1]
+    form, ldx, xs, n, d, dev = _mx_input(X, x_scales, quantize_x, blocks)
+    m = _check_mx(gate_codes, gate_scales, "gate", blocks, dev)
+    if _check_mx(up_codes, up_scales, "up", blocks, dev) != m:
+        raise ValueError("gate and up must have the same shape")
+    lib = _lib()
+    ws = _enough(ws, lib.gptq_mx_gated_workspace_bytes(n, m, d, form), dev)
+    Y = _out(Y, "Y", _BF16, (n, m), dev)
+    G = U = None
+    if want_parts:
+        G = torch.empty(n, m, dtype=_BF16, device=dev)
+        U = torch.empty(n, m, dtype=_BF16, device=dev)
+    _launch(dev, "gptq_mx_gated", lib.gptq_mx_gated, X.data_ptr(), form, xs, n, d, ldx,
+            gate_codes.data_ptr(), gate_scales.data_ptr(), up_codes.data_ptr(), up_scales.data_ptr(),
+            m, act, Y.data_ptr(), m, None if G is None else G.data_ptr(),
+            None if U is None else U.data_ptr(), m, ws.data_ptr(), ws.numel() * ws.element_size())
+    return (Y, G, U) if want_parts else Y
+
+
+def gptq_mx_gated_backward(dY: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
+                              gate_codes: torch.Tensor, gate_scales: torch.Tensor,
+                              up_codes: torch.Tensor, up_scales: torch.Tensor, d: int,
+                              activation: str = "silu", need_dx: bool = True, dX=None, ws=None):
+    """Gradients of gptq_mx_gated from dY bf16 [n, m] and the G and U it
+    returned: (dX bf16 [n, d] or None, dG, dU bf16 [n, m]: views of one
+    buffer, with a row stride beyond m)."""
+    act = _activation(activation)
+    ldy = _gpu_rows(dY, "dY")
+    dev = _gpu_device(dY)
+    n, m = dY.shape
+    ldg = _gpu_rows(G, "G", m)
+    if _gpu_rows(U, "U", m) != ldg or G.shape != dY.shape or U.shape != dY.shape or \
+            G.device != dev or U.device != dev:
+        raise ValueError(f"G and U must be {tuple(dY.shape)} with one row stride, on {dev}")
+    lib = _lib()
+    if need_dx:
+        blocks = -(-d // 32)
+        if _check_mx(gate_codes, gate_scales, "gate", blocks, dev) != m or \
+                _check_mx(up_codes, up_scales, "up", blocks, dev) != m:
+            raise ValueError(f"gate and up must have {m} rows")
+        ws = _enough(ws, lib.gptq_mx_gated_backward_workspace_bytes(n, m, d), dev)
+        dX = _out(dX, "dX", _BF16, (n, d), dev)
+    else:
+        dX = ws = None
+    mp = -(-m // 64) * 64
+    grads = torch.empty(n, 2 * mp, dtype=_BF16, device=dev)
+    _launch(dev, "gptq_mx_gated_backward", lib.gptq_mx_gated_backward, dY.data_ptr(),
+            GPTQ_BF16, n, m, ldy, G.data_ptr(), U.data_ptr(), ldg,
+            gate_codes.data_ptr() if need_dx else None, gate_scales.data_ptr() if need_dx else None,
+            up_codes.data_ptr() if need_dx else None, up_scales.data_ptr() if need_dx else None, d,
+            act, None if dX is None else dX.data_ptr(), d, grads.data_ptr(),
+            None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size())
+    return dX, grads[:, :m], grads[:, mp:mp + m]
 
 
 def gptq_quantize_stack(Ws, X: torch.Tensor, params, activation: str = "none",

@@ -209,6 +209,20 @@ gptq_status launch_distill(const void* logits, gptq_dtype dt, int64_t n, int64_t
                            const float* grad, float* loss, float* stats, void* dlogits,
                            int64_t ldd, hipStream_t st);
 
+// A row of logits' log probability of a token, entropy, log-sum-exp and k
+// largest (k_tokens.hip), and the gradient; outputs may be NULL but top / idx
+// where k > 0.
+constexpr int kTokensMaxK = 512;
+size_t tokens_ws_bytes(int64_t n, int64_t vocab, int64_t k);
+gptq_status launch_tokens(const void* logits, gptq_dtype dt, int64_t n, int64_t vocab, int64_t ldl,
+                          const int32_t* token, float temp, int64_t k, float* logp, float* entropy,
+                          float* lse, float* stats, float* top, int32_t* idx, void* ws,
+                          hipStream_t st);
+gptq_status launch_tokens_grad(const void* logits, gptq_dtype dt, int64_t n, int64_t vocab,
+                               int64_t ldl, const float* stats, const int32_t* token, float temp,
+                               const float* grad_logp, const float* grad_entropy, void* dlogits,
+                               int64_t ldd, hipStream_t st);
+
 // Tracing (trace.hip): per-phase event pairs on the caller's stream while
 // enabled.  trace_begin returns a token (-1 when off) for trace_end.
 constexpr int kTracePhases = GPTQ_TRACE_PHASES;

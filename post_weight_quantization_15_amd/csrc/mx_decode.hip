@@ -1,0 +1,209 @@
+// The 4-bit floating-point products for few activation rows.
+//
+// Bound by the weights' bytes, and at one token by latency: nothing is laid
+// out, no weight passes through LDS.  A wave takes 16 output rows (or 16 of
+// either layer of a gated block) and a share of k; lane 16 q + r loads the 16
+// bytes that are block 4 s + q of row r, for slabs s of 128 columns, which is
+// the operand that the scaled matrix instruction takes, one block's scale a lane
+// (4-bit activations), or four operands of the bf16 one after a conversion that
+// is exact (bf16 activations; column 32 q + 8 i + v of a slab is then place 8 q
+// + v of product i, in both operands).  Activations to be rounded are rounded
+// on the way: a lane holds a whole block, so its scale needs no exchange.  The
+// waves' sums meet in LDS in the order of k.
+#include "mx.h"
+
+namespace gptq {
+namespace {
+
+struct DecodeArgs {
+  MxInput x;
+  Mx w, up;
+  MxOutput y;
+  bool vec;               // 16-byte loads of bf16 rows are aligned
+};
+
+constexpr int kWaves = 8;
+constexpr int kSlabs = 4;                    // slabs whose loads are under way at once
+
+// FORM: gptq_mx_input; NT: activation rows / 16; JT: 16-row tiles of a wave
+// (GATED: one of each layer).
+template <int FORM, int NT, int JT, bool GATED>
+__global__ __launch_bounds__(kWaves * 64) void mx_decode_kernel(DecodeArgs a) {
+  __shared__ f32x4 sums[kWaves][JT * NT][64];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  constexpr int kRows = GATED ? 16 : 16 * JT;            // output columns of the workgroup
+  const int64_t j0 = int64_t(blockIdx.x) * kRows;
+  const int nb = static_cast<int>(a.w.nb), slabs = (nb + 3) / 4;
+  const int s0 = slabs * wv / kWaves, s1 = slabs * (wv + 1) / kWaves;
+  const uint8_t* wc[JT];
+  const uint8_t* wsc[JT];
+#pragma unroll
+  for (int j = 0; j < JT; ++j) {
+    const Mx& w = GATED && j ? a.up : a.w;
+    const int64_t row = min(j0 + (GATED ? 0 : 16 * j) + r, w.rows - 1);
+    wc[j] = w.codes + row * nb * 16;
+    wsc[j] = w.scales + row * nb;
+  }
+  const char* xp[NT];
+  const uint8_t* xs[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t row = min<int64_t>(16 * t + r, a.x.n - 1);
+    if (FORM == GPTQ_MX_CODES) {
+      xp[t] = static_cast<const char*>(a.x.X) + row * nb * 16;
+      xs[t] = a.x.scales + row * nb;
+    } else {
+      xp[t] = static_cast<const char*>(a.x.X) + row * a.x.ldx * 2;
+    }
+  }
+  f32x4 acc[JT][NT];
+#pragma unroll
+  for (int j = 0; j < JT; ++j)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int kX = FORM == GPTQ_MX_CODES ? 1 : 4;      // 16-byte loads of a block
+  for (int s = s0; s < s1; s += kSlabs) {
+    u32x4 w[kSlabs][JT];
+    uint32_t sc[kSlabs][JT];
+#pragma unroll
+    for (int u = 0; u < kSlabs; ++u) {
+      const int b = 4 * (s + u) + q;
+      // past the share's end or the row's: zeros times 1
+      const bool in = s + u < s1 && b < nb;
+#pragma unroll
+      for (int j = 0; j < JT; ++j) {
+        w[u][j] = u32x4{0u, 0u, 0u, 0u};
+        sc[u][j] = 127u;
+        if (in) {
+          w[u][j] = *reinterpret_cast<const u32x4*>(wc[j] + 16 * b);
+          sc[u][j] = wsc[j][b];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kSlabs; ++u) {
+      if (s + u >= s1) break;
+      const int b = 4 * (s + u) + q;
+      u32x4 x[NT][kX];
+      uint32_t sx[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        sx[t] = 127u;
+        if (FORM == GPTQ_MX_CODES) {
+          x[t][0] = u32x4{0u, 0u, 0u, 0u};
+          if (b < nb) {
+            x[t][0] = *reinterpret_cast<const u32x4*>(xp[t] + 16 * b);
+            sx[t] = xs[t][b];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kX; ++i)
+            x[t][i] = load8(reinterpret_cast<const uint16_t*>(xp[t]), 32 * int64_t(b) + 8 * i, a.x.d,
+                            a.vec);
+        }
+      }
+      if (FORM == GPTQ_MX_ROUND) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int i = 0; i < kX; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = mx_amax2(m, x[t][i][e]);
+          sx[t] = mx_scale_byte(max(m & 0xFFFFu, m >> 16) << 16);
+          const float scale = mx_scale_f32(sx[t]);
+          u32x4 c;
+#pragma unroll
+          for (int i = 0; i < kX; ++i) c[i] = mx_round8(x[t][i], scale);
+          x[t][0] = c;
+        }
+      }
+      if (FORM == GPTQ_MX_BF16) {
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+          const float scale = mx_scale_f32(sc[u][j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const u32x4 f = mx_expand8(w[u][j][i], scale);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[j][t] = mfma16(f, x[t][i % kX], acc[j][t]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            acc[j][t] = mx_mfma(w[u][j], sc[u][j], x[t][0], sx[t], acc[j][t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < JT; ++j)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sums[wv][j * NT + t][lane] = acc[j][t];
+  __syncthreads();
+  // lane 16 q + r holds columns 4 q .. + 3 of activation row r
+  for (int p = wv; p < (GATED ? NT : JT * NT); p += kWaves) {
+    f32x4 v = sums[0][p][lane];
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) v += sums[k][p][lane];
+    const int64_t t = 16 * (p % NT) + r, j = j0 + 16 * (p / NT) + 4 * q;
+    if (t >= a.x.n) continue;
+    if (GATED) {
+      f32x4 u = sums[0][NT + p][lane];
+#pragma unroll
+      for (int k = 1; k < kWaves; ++k) u += sums[k][NT + p][lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (j + e >= a.w.rows) break;
+        static_cast<uint16_t*>(a.y.Y)[t * a.y.ldy + j + e] = f32_bf16(mx_act(v[e], a.y.act) * u[e]);
+        if (a.y.G) {
+          a.y.G[t * a.y.ldg + j + e] = f32_bf16(v[e]);
+          a.y.U[t * a.y.ldg + j + e] = f32_bf16(u[e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (j + e >= a.w.rows) break;
+        if (a.y.out_bf16) static_cast<uint16_t*>(a.y.Y)[t * a.y.ldy + j + e] = f32_bf16(v[e]);
+        else static_cast<float*>(a.y.Y)[t * a.y.ldy + j + e] = v[e];
+      }
+    }
+  }
+}
+
+template <int FORM, int NT>
+gptq_status launch_rows(const DecodeArgs& a, hipStream_t st) {
+  const int64_t m = a.w.rows;
+  if (a.up.codes)
+    mx_decode_kernel<FORM, NT, 2, true><<<ceil_div(m, 16), kWaves * 64, 0, st>>>(a);
+  else
+    mx_decode_kernel<FORM, NT, 1, false><<<ceil_div(m, 16), kWaves * 64, 0, st>>>(a);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+template <int FORM>
+gptq_status launch_form(const DecodeArgs& a, hipStream_t st) {
+  if (a.x.n <= 16) return launch_rows<FORM, 1>(a, st);
+  if (a.x.n <= 32) return launch_rows<FORM, 2>(a, st);
+  return launch_rows<FORM, 4>(a, st);
+}
+
+}  // namespace
+
+gptq_status launch_mx_decode(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y,
+                             hipStream_t st) {
+  if (x.n == 0) return GPTQ_OK;
+  const DecodeArgs a{x, w, up, y, x.ldx % 8 == 0 && reinterpret_cast<uintptr_t>(x.X) % 16 == 0};
+  switch (x.form) {
+    case GPTQ_MX_BF16: return launch_form<GPTQ_MX_BF16>(a, st);
+    case GPTQ_MX_ROUND: return launch_form<GPTQ_MX_ROUND>(a, st);
+    default: return launch_form<GPTQ_MX_CODES>(a, st);
+  }
+}
+
+}  // namespace gptq
