@@ -25,10 +25,12 @@
 namespace gptq {
 namespace {
 
-constexpr int kThreads = 512, kWaves = kThreads / 64;
-constexpr int kGroup = 4;                    // steps between two looks at the candidates
-constexpr int kCap = 8192;                   // candidates in LDS
-constexpr int kByRank = 1024;                // as many are ranked by counting, more sorted
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kLook = 4;                     // steps between two looks at the candidates
+constexpr int kAhead = 3;                    // steps whose loads are under way
+constexpr int kCap = 2048;                   // candidates in LDS (twice as many for k > kThreads)
+constexpr int kByRank = 512;                 // as many are sorted by counting
+constexpr int kBars = 3;                     // 1, 2, 4 waves
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kLn2 = 0.693147180559945309417;
 constexpr float kLowest = -3.402823466e38f;
@@ -71,9 +73,12 @@ __device__ inline uint32_t order_of(float x) {
 __device__ inline float value_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
+// A candidate: value, then lower id first (ids have 18 bits).
+static_assert(kDistillMaxVocab == 1 << 18, "ids have 18 bits");
 __device__ inline uint64_t entry_of(float x, int id) {
-  return uint64_t(order_of(x)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+  return uint64_t(order_of(x)) << 18 | (0x3FFFFu - static_cast<uint32_t>(id));
 }
+__device__ inline uint32_t order_in(uint64_t e) { return static_cast<uint32_t>(e >> 18); }
 
 template <class T, class F>
 __device__ inline T wave_all(T v, F f) {
@@ -82,56 +87,120 @@ __device__ inline T wave_all(T v, F f) {
   return v;
 }
 
-// The k largest of buf[0 .. count), in order, at its front; all threads call it,
-// with buf written and a barrier behind that.  Returns how many there are.
-__device__ __attribute__((noinline)) int select_top(uint64_t* buf, int count, int k) {
-  const int tid = threadIdx.x;
-  if (count <= kByRank) {
-    const uint64_t a0 = tid < count ? buf[tid] : 0u;
-    const uint64_t a1 = tid + kThreads < count ? buf[tid + kThreads] : 0u;
-    int r0 = 0, r1 = 0;
-    if ((tid & ~63) < count) {               // waves without a candidate wait below
-      if (count <= kThreads) {
-#pragma unroll 8
-        for (int i = 0; i < count; ++i) r0 += buf[i] > a0;
-      } else {
-#pragma unroll 8
-        for (int i = 0; i < count; ++i) {
-          const uint64_t v = buf[i];
-          r0 += v > a0;
-          r1 += v > a1;
-        }
-      }
+// What the selections share beside the candidates.
+struct Scratch {
+  int hist[256];
+  uint32_t totals[kWaves];
+  uint64_t prefix;
+  int need, cnt;
+};
+
+// An entry that exactly k of buf[0 .. count) reach, k < count: digit by digit from
+// the top, the digit where the k-th largest lies; done where all of it belong to the k.
+__device__ inline uint64_t kth_entry(const uint64_t* buf, int count, int k, Scratch& sc) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  uint64_t prefix = 0u;
+  int need = k;
+#pragma unroll 1
+  for (int known = 50; ;) {                  // the bits from here up are decided
+    const int shift = max(known - 8, 0);
+    const uint32_t digits = (1u << (known - shift)) - 1u;
+    static_assert(kThreads == 256, "a thread a bin");
+    sc.hist[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < count; i += kThreads) {
+      const uint64_t e = buf[i];
+      if (e >> known == prefix >> known)
+        atomicAdd(&sc.hist[static_cast<uint32_t>(e >> shift) & digits], 1);
     }
     __syncthreads();
-    if (tid < count && r0 < k) buf[r0] = a0;
-    if (tid + kThreads < count && r1 < k) buf[r1] = a1;
+    const int own = sc.hist[tid];
+    int from = own;                          // entries in this bin and above
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_down(from, o);
+      if (lane + o < 64) from += u;
+    }
+    if (lane == 0) sc.totals[wv] = from;
     __syncthreads();
-    return min(count, k);
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w)
+      if (w > wv) from += sc.totals[w];
+    if (from >= need && from - own < need) {
+      sc.prefix = prefix | uint64_t(tid) << shift;
+      // the whole bin: no digit below it matters
+      sc.need = from == need ? 0 : need - (from - own);
+    }
+    __syncthreads();
+    prefix = sc.prefix;
+    need = sc.need;
+    if (need == 0 || shift == 0) return prefix;
+    known = shift;
   }
-  int size = 2 * kByRank;
-  while (size < count) size *= 2;
-  for (int i = count + tid; i < size; i += kThreads) buf[i] = 0u;
+}
+
+// The entries of buf[0 .. count) from `least` up, to its front; all threads call it.
+__device__ inline void keep_from(uint64_t* buf, int count, uint64_t least, Scratch& sc) {
+  const int tid = threadIdx.x;
+  if (tid == 0) sc.cnt = 0;
+  for (int b = 0; b < count; b += kThreads) {
+    const uint64_t e = b + tid < count ? buf[b + tid] : 0u;
+    __syncthreads();                         // these are read: as many places are free
+    if (e >= least && b + tid < count) buf[atomicAdd(&sc.cnt, 1)] = e;
+  }
   __syncthreads();
-  for (int run = 2; run <= size; run *= 2)
-    for (int step = run / 2; step > 0; step /= 2) {
-      for (int p = tid; p < size / 2; p += kThreads) {
-        const int i = 2 * p - (p & (step - 1)), j = i + step;
-        const uint64_t a = buf[i], b = buf[j];
-        if ((a < b) == ((i & run) == 0)) {
-          buf[i] = b;
-          buf[j] = a;
-        }
+}
+
+// buf[0 .. count), count <= kByRank, in descending order.
+__device__ inline void sort_by_rank(uint64_t* buf, int count) {
+  constexpr int kOwn = kByRank / kThreads;
+  const int tid = threadIdx.x;
+  uint64_t own[kOwn];
+  int rank[kOwn];
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j) {
+    own[j] = tid + j * kThreads < count ? buf[tid + j * kThreads] : 0u;
+    rank[j] = 0;
+  }
+  if ((tid & ~63) < count) {                 // waves without an entry wait below
+    if (count <= kThreads) {
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) rank[0] += buf[i] > own[0];
+    } else {
+#pragma unroll 2
+      for (int i = 0; i < count; ++i) {
+        const uint64_t v = buf[i];
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) rank[j] += v > own[j];
       }
-      __syncthreads();
     }
-  return min(count, k);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j)
+    if (tid + j * kThreads < count) buf[rank[j]] = own[j];
+  __syncthreads();
+}
+
+// The lower bound that the (k / p)-th largest of each of `lists` lists (a lane its list's, as an
+// order number; p = parts, and so on) gives for the k-th largest of all: the one that p lists
+// reach.  Lanes' last six bits become their numbers, which makes them different.
+__device__ inline uint32_t reached_by(uint32_t order, int p) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t key = (order & ~63u) | static_cast<uint32_t>(lane);
+  int rank = 0;
+#pragma unroll 8
+  for (int l = 0; l < 64; ++l)
+    rank += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), l)) > key;
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(
+             static_cast<int>(key), __builtin_ctzll(__ballot(rank == p - 1)))) & ~63u;
 }
 
 struct TokenArgs {
   const void* logits;
   int64_t ldl;
   int vocab, k, parts, span;                 // a part: span cells of a row
+  int cap;                                   // candidates that the LDS holds
   double inv_temp;
   const int32_t* token;
   float* logp;
@@ -177,28 +246,40 @@ __device__ inline void finish_row(const TokenArgs& a, int64_t row, double ref, d
 __device__ inline void write_top(const TokenArgs& a, int64_t row, const uint64_t* buf, int have) {
   for (int i = threadIdx.x; i < a.k; i += kThreads) {
     const uint64_t e = i < have ? buf[i] : 0u;
-    const bool some = e >> 32;
-    a.top[row * a.k + i] = some ? value_of(static_cast<uint32_t>(e >> 32)) : -INFINITY;
-    a.idx[row * a.k + i] = some ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(e)) : -1;
+    const bool some = order_in(e);
+    a.top[row * a.k + i] = some ? value_of(order_in(e)) : -INFINITY;
+    a.idx[row * a.k + i] = some ? static_cast<int32_t>(0x3FFFFu - (static_cast<uint32_t>(e) & 0x3FFFFu)) : -1;
   }
 }
 
-// Sums relative to reference r moved to a higher one.
+// Sums relative to a reference moved to one that is higher by `up` (in powers of
+// two); 2^-up from the fp32 exponential of its fraction (2 u).
 __device__ inline void move_sums(double& s, double& t, double up) {
   up = up < 1000.0 ? up : 1000.0;
-  const double f = exp2(-up);
+  const int n = static_cast<int>(up);
+  const double f = ldexp(static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(n - up))), -n);
   t = f * (t - up * s);
   s *= f;
 }
 
+// The lanes' sums, each relative to its own reference, as one of them all.
+__device__ inline void join_sums(double& r, double& s, double& t, float c) {
+  const double most = wave_all(r, [](double x, double y) { return x > y ? x : y; });
+  if (r < most) move_sums(s, t, double(c) * (most - r));
+  r = most;
+  s = wave_all(s, [](double x, double y) { return x + y; });
+  t = wave_all(t, [](double x, double y) { return x + y; });
+}
+
 template <int DT>
-__global__ __launch_bounds__(kThreads, 4) void tokens_kernel(TokenArgs a) {
+__global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
   using T = typename Cells<DT>::type;
   constexpr int E = Cells<DT>::kPer, NV = Cells<DT>::kVec;
   constexpr int kSteps = kThreads * NV;      // vectors of a step
   extern __shared__ __attribute__((aligned(16))) uint64_t buf[];
   __shared__ double red[3][kWaves];
-  __shared__ float bars[kWaves];
+  __shared__ uint32_t bars[kBars][kWaves];
+  __shared__ Scratch sc;
   __shared__ int cnt;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t row = blockIdx.x;
@@ -211,20 +292,21 @@ __global__ __launch_bounds__(kThreads, 4) void tokens_kernel(TokenArgs a) {
   const int edge = tid < head ? tid : tid >= E && tid - E < V - last ? last + tid - E : -1;
   const float c = static_cast<float>(a.inv_temp) * kLog2e;
   const float margin = 40.0f / c;
-  const int steps = (nvec + kSteps - 1) / kSteps;
+  const int steps = max(1, (nvec + kSteps - 1) / kSteps);
   const T* body = src + head;
 
-  u32x4 cur[kGroup][NV], nxt[kGroup][NV];
-  auto load = [&](u32x4 (&v)[kGroup][NV], int step) {
+  // loads run kAhead steps ahead, in registers that move up a step at a time (the loop is
+  // not unrolled: a single row is bound by the fetch of its instructions)
+  u32x4 ring[kAhead][NV];
+  auto load = [&](u32x4 (&v)[NV], int step) {
 #pragma unroll
-    for (int u = 0; u < kGroup; ++u)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int at = (step + u) * kSteps + i * kThreads + tid;
-        if (at < nvec) v[u][i] = *reinterpret_cast<const u32x4*>(body + int64_t(at) * E);
-      }
+    for (int i = 0; i < NV; ++i) {
+      const int at = step * kSteps + i * kThreads + tid;
+      if (at < nvec) v[i] = *reinterpret_cast<const u32x4*>(body + int64_t(at) * E);
+    }
   };
-  load(cur, 0);
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) load(ring[s], s);
   if (tid == 0) cnt = 0;
   float ez = -INFINITY;
   if (edge >= 0) ez = to_f32<DT>(src[edge]);
@@ -238,134 +320,195 @@ __global__ __launch_bounds__(kThreads, 4) void tokens_kernel(TokenArgs a) {
   float bar = -INFINITY;                     // cells from here up are candidates
   float ref = kLowest;
   double s = 0.0, t = 0.0;                   // of this thread, relative to ref
-  // candidates among the vectors of one step (past the buffer's end: counted only)
+  // candidates among the cells of one vector (past the buffer's end: counted only)
   auto push = [&](const u32x4& v, int at) {
+    uint32_t hits = 0u;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float x = cell_of<DT>(v, e);
-      if (x >= bar) {
-        const int p = atomicAdd(&cnt, 1);
-        if (p < kCap) buf[p] = entry_of(x, first + head + at * E + e);
-      }
+    for (int e = 0; e < E; ++e) hits |= cell_of<DT>(v, e) >= bar ? 1u << e : 0u;
+    const u32x4 w = v;
+    while (hits) {
+      const int e = __builtin_ctz(hits);
+      hits &= hits - 1u;
+      const int i = DT == GPTQ_F32 ? e : e >> 1;
+      uint32_t word = w[0];
+      word = i == 1 ? w[1] : word;
+      word = i == 2 ? w[2] : word;
+      word = i == 3 ? w[3] : word;
+      float x = __uint_as_float(word);
+      if (DT == GPTQ_BF16) x = __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
+      if (DT == GPTQ_F16)
+        x = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(word >> (16 * (e & 1)))));
+      const int p = atomicAdd(&cnt, 1);
+      if (p < a.cap) buf[p] = entry_of(x, first + head + at * E + e);
     }
   };
-  // the bar after a selection
-  auto raise = [&]() {
-    if (have >= a.k) bar = value_of(static_cast<uint32_t>(buf[a.k - 1] >> 32) + 1u);
+  int from = 0;                              // first step since the last look
+  float ps = 0.0f, pt = 0.0f;                // of kLook steps
+  auto add_cell = [&](float x) {
+    float d = (x - ref) * c;
+    const float e = __builtin_amdgcn_exp2f(d);
+    d = max3(d, -1000.0f, -1000.0f);         // 0 times -inf
+    ps += e;
+    pt = fmaf(e, d, pt);
   };
 
-  for (int step = 0; step == 0 || step < steps; step += kGroup) {
-    if (step + kGroup < steps) load(nxt, step + kGroup);
-    // ---- the largest cells of each vector
-    float top[kGroup][NV], gm = step == 0 ? ez : -INFINITY;
+#pragma unroll 1
+  for (int step = 0; step < steps; ++step) {
+    u32x4 cur[NV];
 #pragma unroll
-    for (int u = 0; u < kGroup; ++u)
+    for (int i = 0; i < NV; ++i) {
+      cur[i] = ring[0][i];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int at = (step + u) * kSteps + i * kThreads + tid;
-        float m = -INFINITY;
-        if (at < nvec) {
+      for (int u = 0; u + 1 < kAhead; ++u) ring[u][i] = ring[u + 1][i];
+    }
+    load(ring[kAhead - 1], step + kAhead);
+    const int at0 = step * kSteps + tid;
+    // ---- the largest cell of each vector
+    float top[NV], gm = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < E; e += 2) m = max3(m, cell_of<DT>(cur[u][i], e), cell_of<DT>(cur[u][i], e + 1));
-        }
-        top[u][i] = m;
-        gm = fmaxf(gm, m);
+    for (int i = 0; i < NV; ++i) {
+      float m = -INFINITY;
+      if (at0 + i * kThreads < nvec) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) m = max3(m, cell_of<DT>(cur[i], e), cell_of<DT>(cur[i], e + 1));
       }
+      top[i] = m;
+      gm = max3(gm, m, step == 0 ? ez : m);
+    }
     if (__any(gm > ref + margin)) {
       const float up = wave_all(gm, [](float x, float y) { return fmaxf(x, y); });
-      move_sums(s, t, double(c) * (double(up) - double(ref)));
+      s += ps;
+      t += pt;
+      ps = pt = 0.0f;
+      if (step) move_sums(s, t, double(c) * (double(up) - double(ref)));
       ref = up;
     }
     // ---- sums
-    float ps = 0.0f, pt = 0.0f;
-    auto add_cell = [&](float x) {
-      float d = (x - ref) * c;
-      const float e = __builtin_amdgcn_exp2f(d);
-      d = max3(d, -1000.0f, -1000.0f);       // 0 times -inf
-      ps += e;
-      pt = fmaf(e, d, pt);
-    };
     if (step == 0 && edge >= 0) add_cell(ez);
 #pragma unroll
-    for (int u = 0; u < kGroup; ++u)
+    for (int i = 0; i < NV; ++i) {
+      if (at0 + i * kThreads < nvec) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int at = (step + u) * kSteps + i * kThreads + tid;
-        if (at < nvec) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) add_cell(cell_of<DT>(cur[u][i], e));
-        }
-      }
-    s += ps;
-    t += pt;
-    // ---- candidates
-    if (a.k) {
-      if (step == 0) {
-        // this wave's (k / waves)-th largest of the lanes' maxima
-        const int want = (a.k + kWaves - 1) / kWaves;
-        float low = -INFINITY;
-        if (want <= 64) {
-          const uint32_t key = order_of(gm);
-          int rank = 0;
-#pragma unroll
-          for (int l = 0; l < 64; ++l) {
-            const uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), l));
-            rank += o > key || (o == key && l < lane);
-          }
-          const uint64_t at = __ballot(rank == want - 1);
-          const uint32_t pick = static_cast<uint32_t>(
-              __builtin_amdgcn_readlane(static_cast<int>(key), __builtin_ctzll(at)));
-          low = pick ? value_of(pick) : -INFINITY;
-        }
-        if (lane == 0) bars[wv] = low;
-        __syncthreads();
-        bar = bars[0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) bar = fminf(bar, bars[w]);
-      }
-#pragma unroll
-      for (int u = 0; u < kGroup; ++u)
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (top[u][i] >= bar) {
-            const int at = (step + u) * kSteps + i * kThreads + tid;
-            if (at < nvec) push(cur[u][i], at);
-          }
-      __syncthreads();
-      const int found = cnt;
-      __syncthreads();
-      if (found > kCap) {
-        // too many at once: a step at a time, each in room for all its cells
-        for (int u = step; u < min(step + kGroup, steps); ++u) {
-          if (tid == 0) cnt = have;
-          __syncthreads();
-          for (int i = 0; i < NV; ++i) {
-            const int at = u * kSteps + i * kThreads + tid;
-            if (at < nvec) push(*reinterpret_cast<const u32x4*>(body + int64_t(at) * E), at);
-          }
-          __syncthreads();
-          const int now = cnt;
-          __syncthreads();
-          have = select_top(buf, now, a.k);
-          raise();
-          __syncthreads();
-        }
-        if (tid == 0) cnt = have;
-        __syncthreads();
-      } else if (found > a.k + 64 || step + kGroup >= steps) {
-        have = select_top(buf, found, a.k);
-        raise();
-        if (tid == 0) cnt = have;
-        __syncthreads();
-      } else {
-        have = found;
+        for (int e = 0; e < E; ++e) add_cell(cell_of<DT>(cur[i], e));
       }
     }
+    // (without a first bar a step fills the candidates)
+    const bool look = step % kLook == kLook - 1 || step + 1 == steps || (step == 0 && a.k > kThreads);
+    if (look) {
+      s += ps;
+      t += pt;
+      ps = pt = 0.0f;
+    }
+    // ---- candidates
+    if (!a.k) continue;
+    if (step == 0) {
+      // A bar from the lanes' maxima over all cells at hand (this step's and those ahead).
+      // For 1, 2, 4 waves: the (k / waves)-th of each wave, and of these the one that
+      // as many waves reach: at least k cells are as large.  The highest of those
+      // bars holds also where some waves see only masked cells.
+      float most = gm;
 #pragma unroll
-    for (int u = 0; u < kGroup; ++u)
+      for (int u = 0; u + 1 < kAhead; ++u)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) cur[u][i] = nxt[u][i];
+        for (int i = 0; i < NV; ++i)
+          if (at0 + (u + 1) * kSteps + i * kThreads < nvec) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+              most = max3(most, cell_of<DT>(ring[u][i], e), cell_of<DT>(ring[u][i], e + 1));
+          }
+      // last six bits in place of the lane's number, which makes them different
+      const uint32_t key = (order_of(most) & ~63u) | static_cast<uint32_t>(lane);
+      int rank = 0;
+#pragma unroll 8
+      for (int l = 0; l < 64; ++l)
+        rank += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), l)) > key;
+#pragma unroll
+      for (int g = 0; g < kBars; ++g) {
+        const int want = (a.k + (1 << g) - 1) >> g;
+        uint32_t pick = 0u;
+        if (want <= 64)
+          pick = static_cast<uint32_t>(__builtin_amdgcn_readlane(
+                     static_cast<int>(key), __builtin_ctzll(__ballot(rank == want - 1)))) & ~63u;
+        if (lane == 0) bars[g][wv] = pick;
+      }
+      __syncthreads();
+      // lane 8 g + w: wave w's for 2^g waves
+      const bool one = lane < 8 * kBars && (lane & 7) < kWaves;
+      const uint32_t mine = one ? bars[lane >> 3][lane & 7] : 0u;
+      int above = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const uint32_t o = static_cast<uint32_t>(__shfl(static_cast<int>(mine), (lane & ~7) + w));
+        above += o > mine || (o == mine && w < (lane & 7));
+      }
+      const uint32_t best = wave_all(one && above == (1 << (lane >> 3)) - 1 ? mine : 0u,
+                                     [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+      bar = best > order_of(-INFINITY) ? value_of(best) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = at0 + i * kThreads;
+      bool in = top[i] >= bar && at < nvec;
+      if (from == 0) {
+        // many cells may equal the first bar (masked ones): those with k and more of them
+        // before them in their wave are not among the k largest
+        int same = 0;
+        if (in && top[i] == bar) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) same += cell_of<DT>(cur[i], e) == bar;
+        }
+        int before = same;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const int u = __shfl_up(before, o);
+          if (lane >= o) before += u;
+        }
+        if (top[i] == bar && before - same >= a.k) in = false;
+      }
+      if (in) push(cur[i], at);
+    }
+    if (!look) continue;
+    __syncthreads();
+    const int found = cnt;
+    __syncthreads();
+    const bool again = found > a.cap;
+    if (found <= max(2 * a.k + 64, kByRank) && step + 1 < steps) {
+      have = found;
+      from = step + 1;
+      continue;
+    }
+    // too many at once: these steps again in halves, each in room for all its cells
+    int u = again ? 2 * from : 2 * step + 1, now = found;
+#pragma unroll 1
+    do {
+      if (again) {
+        if (tid == 0) cnt = have;
+        __syncthreads();
+        if (tid < kThreads / 2) {
+#pragma unroll 1
+          for (int i = 0; i < NV; ++i) {
+            const int at = (u * NV + i) * (kThreads / 2) + tid;
+            if (at < nvec) push(*reinterpret_cast<const u32x4*>(body + int64_t(at) * E), at);
+          }
+        }
+        __syncthreads();
+        now = cnt;
+        __syncthreads();
+      }
+      have = now;
+      if (now > a.k) {
+        const uint64_t least = kth_entry(buf, now, a.k, sc);
+        keep_from(buf, now, least, sc);
+        have = a.k;
+        // where all of a bin belong to the k, `least` lies at or below the k-th
+        bar = fmaxf(bar, value_of(order_in(least) + ((least & 0x3FFFFu) != 0u)));
+      }
+    } while (++u <= 2 * step + 1);
+    from = step + 1;
+    if (tid == 0) cnt = have;
+    __syncthreads();
   }
+  if (a.k) sort_by_rank(buf, have);
   // ---- the waves' sums, moved to the highest reference
   s = wave_all(s, [](double x, double y) { return x + y; });
   t = wave_all(t, [](double x, double y) { return x + y; });
@@ -375,22 +518,20 @@ __global__ __launch_bounds__(kThreads, 4) void tokens_kernel(TokenArgs a) {
     red[2][wv] = t;
   }
   __syncthreads();
-  if (tid == 0) {
-    double r = kLowest, S = 0.0, Tt = 0.0;
-    for (int w = 0; w < kWaves; ++w) r = red[0][w] > r ? red[0][w] : r;
-    for (int w = 0; w < kWaves; ++w) {
-      double ws = red[1][w], wt = red[2][w];
-      if (red[0][w] < r) move_sums(ws, wt, double(c) * (r - red[0][w]));
-      S += ws;
-      Tt += wt;
-    }
-    if (a.parts == 1) {
-      finish_row<DT>(a, row, r, S, Tt);
-    } else {
-      double* o = a.part_sums + (row * a.parts + part) * 3;
-      o[0] = r;
-      o[1] = S;
-      o[2] = Tt;
+  if (wv == 0) {
+    double r = lane < kWaves ? red[0][lane] : double(kLowest);
+    s = lane < kWaves ? red[1][lane] : 0.0;
+    t = lane < kWaves ? red[2][lane] : 0.0;
+    join_sums(r, s, t, c);
+    if (lane == 0) {
+      if (a.parts == 1) {
+        finish_row<DT>(a, row, r, s, t);
+      } else {
+        double* o = a.part_sums + (row * a.parts + part) * 3;
+        o[0] = r;
+        o[1] = s;
+        o[2] = t;
+      }
     }
   }
   if (a.k) {
@@ -407,17 +548,22 @@ __global__ __launch_bounds__(kThreads, 4) void tokens_kernel(TokenArgs a) {
 template <int DT>
 __global__ __launch_bounds__(kThreads) void tokens_join_kernel(TokenArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint64_t buf[];
+  __shared__ Scratch sc;
   __shared__ int cnt;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   const uint64_t* in = a.part_top + row * a.parts * a.k;
   if (tid == 0) cnt = 0;
-  uint64_t bar = ~uint64_t(0);
+  uint64_t bar = 0u;
   if (a.k) {
-    // every part has (k / parts) entries from its own such entry up
-    const int want = (a.k + a.parts - 1) / a.parts;
-    if ((tid & 63) < a.parts) bar = in[(tid & 63) * a.k + want - 1];
-    bar = wave_all(bar, [](uint64_t x, uint64_t y) { return x < y ? x : y; });
+    // as for a part's first cells: for all parts, a quarter and one
+    uint32_t best = 0u;
+    for (int p = a.parts; p > 0; p = p > 4 ? p >> 2 : p > 1 ? 1 : 0) {
+      const int lane = tid & 63, want = (a.k + p - 1) / p;
+      const uint32_t pick = reached_by(lane < a.parts ? order_in(in[lane * a.k + want - 1]) : 0u, p);
+      best = pick > best ? pick : best;
+    }
+    bar = uint64_t(best) << 18;
   }
   __syncthreads();
   if (a.k) {
@@ -426,22 +572,22 @@ __global__ __launch_bounds__(kThreads) void tokens_join_kernel(TokenArgs a) {
       if (e && e >= bar) buf[atomicAdd(&cnt, 1)] = e;
     }
     __syncthreads();
-    const int found = cnt;
-    const int have = select_top(buf, found, a.k);
+    int have = cnt;
+    __syncthreads();
+    if (have > kByRank || have > a.k) {
+      const uint64_t least = kth_entry(buf, have, a.k, sc);
+      keep_from(buf, have, least, sc);
+      have = a.k;
+    }
+    sort_by_rank(buf, have);
     write_top(a, row, buf, have);
   }
-  if (tid == 0) {
-    const double* p = a.part_sums + row * a.parts * 3;
-    const double c = double(static_cast<float>(a.inv_temp) * kLog2e);
-    double r = kLowest, S = 0.0, Tt = 0.0;
-    for (int w = 0; w < a.parts; ++w) r = p[3 * w] > r ? p[3 * w] : r;
-    for (int w = 0; w < a.parts; ++w) {
-      double ws = p[3 * w + 1], wt = p[3 * w + 2];
-      if (p[3 * w] < r) move_sums(ws, wt, c * (r - p[3 * w]));
-      S += ws;
-      Tt += wt;
-    }
-    finish_row<DT>(a, row, r, S, Tt);
+  if (tid < 64) {                            // at most 64 parts
+    const double* p = a.part_sums + (row * a.parts + tid) * 3;
+    const bool in = tid < a.parts;
+    double r = in ? p[0] : double(kLowest), s = in ? p[1] : 0.0, t = in ? p[2] : 0.0;
+    join_sums(r, s, t, static_cast<float>(a.inv_temp) * kLog2e);
+    if (tid == 0) finish_row<DT>(a, row, r, s, t);
   }
 }
 
@@ -538,10 +684,10 @@ __global__ __launch_bounds__(kGradThreads) void tokens_grad_kernel(TokenGradArgs
   }
 }
 
-// Parts of a row: enough workgroups for the chip where rows are few, of 4096
+// Parts of a row: enough workgroups for the chip where rows are few, of 2048
 // cells (8 a thread) at least, their candidates within the join's LDS.
 int parts_of(int64_t n, int64_t vocab, int64_t k) {
-  int64_t p = std::min<int64_t>(512 / std::max<int64_t>(n, 1), (vocab + 4095) / 4096);
+  int64_t p = std::min<int64_t>(1024 / std::max<int64_t>(n, 1), (vocab + 2047) / 2048);
   p = std::min<int64_t>(p, 64);
   if (k) p = std::min<int64_t>(p, kCap / k);
   return int(std::max<int64_t>(p, 1));
@@ -562,7 +708,7 @@ TokenWs carve_tokens(Carver& c, int64_t n, int64_t vocab, int64_t k) {
 
 template <int DT>
 gptq_status launch_forward(const TokenArgs& a, int64_t n, hipStream_t st) {
-  const size_t lds = a.k ? size_t(kCap) * 8 : 0;
+  const size_t lds = a.k ? size_t(a.cap) * 8 : 0;
   tokens_kernel<DT><<<dim3(unsigned(n), unsigned(a.parts)), kThreads, lds, st>>>(a);
   GPTQ_CHECK_LAUNCH();
   if (a.parts > 1) {
@@ -587,7 +733,8 @@ gptq_status launch_tokens(const void* logits, gptq_dtype dt, int64_t n, int64_t 
   if (n == 0) return GPTQ_OK;
   Carver c(ws);
   const TokenWs w = carve_tokens(c, n, vocab, k);
-  TokenArgs a{logits, ldl, int(vocab), int(k), parts_of(n, vocab, k), 0, 1.0 / double(temp), token,
+  TokenArgs a{logits, ldl, int(vocab), int(k), parts_of(n, vocab, k), 0, k > kThreads ? 2 * kCap : kCap,
+              1.0 / double(temp), token,
               logp, entropy, lse, stats, top, idx, w.sums, w.top};
   a.span = int(round_up((vocab + a.parts - 1) / a.parts, 8));
   a.parts = int((vocab + a.span - 1) / a.span);          // none is empty
