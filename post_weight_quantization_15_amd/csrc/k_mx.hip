@@ -152,22 +152,8 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantizeArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Layouts in bf16 (exact) for the bf16 product
+// Layout in bf16 (exact) for the gradient's product
 // ---------------------------------------------------------------------------
-
-// M[j][k], rows of ldm values (a multiple of 8, at least 32 nb), zeros past 32 nb.
-__global__ __launch_bounds__(256) void mx_expand_kernel(Mx w, uint16_t* __restrict__ M,
-                                                        uint32_t per) {
-  const uint64_t e = uint64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t j = static_cast<int64_t>(e / per);
-  const uint32_t u = static_cast<uint32_t>(e % per);
-  if (j >= w.rows) return;
-  u32x4 v = u32x4{0u, 0u, 0u, 0u};
-  if (u < 4 * w.nb)
-    v = mx_expand8(reinterpret_cast<const uint32_t*>(w.codes)[j * 4 * w.nb + u],
-                   mx_scale_f32(w.scales[j * w.nb + (u >> 2)]));
-  *reinterpret_cast<u32x4*>(M + (j * per + u) * 8) = v;
-}
 
 // Wt[c][j0 + j] = W[j][c] for 64 rows x 128 columns a workgroup, zeros for
 // rows past the matrix.  A thread takes the same eight columns of two
@@ -211,21 +197,8 @@ __global__ __launch_bounds__(256) void mx_turn_kernel(Mx w, Mx up, unsigned by_o
 }
 
 // ---------------------------------------------------------------------------
-// The gated block's elementwise parts
+// The gated block's elementwise gradient
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void mx_gate_kernel(const float* __restrict__ P, int64_t n,
-                                                      int64_t m, MxOutput y) {
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t t = e / m, j = e % m;
-  if (t >= n) return;
-  const float g = P[t * 2 * m + j], u = P[t * 2 * m + m + j];
-  static_cast<uint16_t*>(y.Y)[t * y.ldy + j] = f32_bf16(mx_act(g, y.act) * u);
-  if (y.G) {
-    y.G[t * y.ldg + j] = f32_bf16(g);
-    y.U[t * y.ldg + j] = f32_bf16(u);
-  }
-}
-
 // dGU[t][j] = dY U act'(G), dGU[t][mp + j] = dY act(G); zeros in the padding.
 __global__ __launch_bounds__(256) void mx_gate_grad_kernel(const uint16_t* __restrict__ dY,
                                                            int64_t lddy,
@@ -258,34 +231,6 @@ __global__ __launch_bounds__(256) void mx_gate_grad_kernel(const uint16_t* __res
 bool as_is(const uint16_t* V, int64_t ldv, int64_t len) {
   return ldv % 8 == 0 && reinterpret_cast<uintptr_t>(V) % 16 == 0 && len % 64 == 0 &&
          ldv < (int64_t(1) << 22);
-}
-
-gptq_status launch_expand(const Mx& w, uint16_t* M, int64_t ldm, hipStream_t st) {
-  mx_expand_kernel<<<ceil_div(w.rows * (ldm / 8), 256), 256, 0, st>>>(w, M, uint32_t(ldm / 8));
-  GPTQ_CHECK_LAUNCH();
-  return GPTQ_OK;
-}
-
-struct MatmulWs {
-  uint16_t* M;        // both layers' rows
-  uint16_t* V2;       // the activations, padded (a chunk of rows)
-  uint8_t* codes;     // the activations' codes and scales (a chunk of rows)
-  uint8_t* scales;
-  float* P;           // both factors (a chunk of rows)
-};
-
-MatmulWs carve_matmul(Carver& c, int64_t n, int64_t m, int64_t d, int form, bool gated) {
-  MatmulWs w{};
-  if (n <= kMxDecodeRows) return w;
-  const int64_t nc = std::min<int64_t>(n, kRowChunk), ldp = round_up(d, 64), nb = mx_blocks(d);
-  w.M = c.take<uint16_t>(size_t(gated ? 2 : 1) * m * ldp);
-  w.V2 = c.take<uint16_t>(size_t(nc) * ldp);
-  if (form == GPTQ_MX_ROUND) {
-    w.codes = c.take<uint8_t>(size_t(nc) * nb * 16);
-    w.scales = c.take<uint8_t>(size_t(nc) * nb);
-  }
-  if (gated) w.P = c.take<float>(size_t(nc) * 2 * m);
-  return w;
 }
 
 struct TurnWs {
@@ -331,73 +276,13 @@ gptq_status launch_mx_quantize(const void* X, gptq_dtype dt, int64_t n, int64_t 
 }
 
 size_t mx_matmul_ws_bytes(int64_t n, int64_t m, int64_t d, int form, bool gated) {
-  Carver c(nullptr);
-  carve_matmul(c, n, m, d, form, gated);
-  return c.bytes();
+  return n <= kMxDecodeRows ? 0 : mx_gemm_ws_bytes(n, m, d, form, gated);
 }
 
 gptq_status launch_mx_matmul(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y,
                              void* ws, hipStream_t st) {
-  if (x.n <= kMxDecodeRows) return launch_mx_decode(x, w, up, y, st);
-  const bool gated = up.codes;
-  Carver c(ws);
-  const MatmulWs b = carve_matmul(c, x.n, w.rows, x.d, x.form, gated);
-  const int64_t ldp = round_up(x.d, 64);
-  gptq_status s;
-  if ((s = launch_expand(w, b.M, ldp, st)) != GPTQ_OK) return s;
-  if (gated && (s = launch_expand(up, b.M + w.rows * ldp, ldp, st)) != GPTQ_OK) return s;
-  GemmArgs g{};
-  g.m = w.rows * (gated ? 2 : 1);
-  g.M = b.M;
-  g.ldm = ldp;
-  g.kblocks = g.kwrap = int(ldp / 64);
-  for (int64_t t0 = 0; t0 < x.n; t0 += kRowChunk) {
-    const int64_t nc = std::min<int64_t>(kRowChunk, x.n - t0);
-    const uint16_t* Xc = static_cast<const uint16_t*>(x.X) + t0 * x.ldx;
-    g.V = b.V2;
-    g.ldv = ldp;
-    if (x.form == GPTQ_MX_BF16) {
-      if (as_is(Xc, x.ldx, x.d)) {
-        g.V = Xc;
-        g.ldv = x.ldx;
-      } else if ((s = launch_pad_rows(Xc, x.ldx, nc, x.d, b.V2, ldp, st)) != GPTQ_OK) {
-        return s;
-      }
-    } else {
-      Mx xc{b.codes, b.scales, nc, w.nb};
-      if (x.form == GPTQ_MX_CODES) {
-        xc.codes = static_cast<const uint8_t*>(x.X) + t0 * w.nb * 16;
-        xc.scales = x.scales + t0 * w.nb;
-      } else if ((s = launch_mx_quantize(Xc, GPTQ_BF16, nc, x.d, x.ldx, b.codes, b.scales, nullptr,
-                                         0, st)) != GPTQ_OK) {
-        return s;
-      }
-      if ((s = launch_expand(xc, b.V2, ldp, st)) != GPTQ_OK) return s;
-    }
-    g.n = nc;
-    if (gated) {
-      g.Y = b.P;
-      g.ldy = g.m;
-      g.out_bf16 = 0;
-    } else {
-      g.Y = y.out_bf16 ? static_cast<void*>(static_cast<uint16_t*>(y.Y) + t0 * y.ldy)
-                       : static_cast<void*>(static_cast<float*>(y.Y) + t0 * y.ldy);
-      g.ldy = y.ldy;
-      g.out_bf16 = y.out_bf16;
-    }
-    if ((s = launch_gemm(g, 0, st)) != GPTQ_OK) return s;
-    if (gated) {
-      MxOutput o = y;
-      o.Y = static_cast<uint16_t*>(y.Y) + t0 * y.ldy;
-      if (y.G) {
-        o.G = y.G + t0 * y.ldg;
-        o.U = y.U + t0 * y.ldg;
-      }
-      mx_gate_kernel<<<ceil_div(nc * w.rows, 256), 256, 0, st>>>(b.P, nc, w.rows, o);
-      GPTQ_CHECK_LAUNCH();
-    }
-  }
-  return GPTQ_OK;
+  return x.n <= kMxDecodeRows ? launch_mx_decode(x, w, up, y, st)
+                              : launch_mx_gemm(x, w, up, y, ws, st);
 }
 
 size_t mx_matmul_t_ws_bytes(int64_t n, int64_t m, int64_t d, bool gated) {

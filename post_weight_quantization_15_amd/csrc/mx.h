@@ -61,6 +61,11 @@ constexpr int64_t kMxDecodeRows = 64;
 gptq_status launch_mx_decode(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y,
                              hipStream_t st);
 
+// Many rows (mx_gemm.hip).
+size_t mx_gemm_ws_bytes(int64_t n, int64_t m, int64_t d, int form, bool gated);
+gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y, void* ws,
+                           hipStream_t st);
+
 #ifdef __HIPCC__
 namespace {
 
