@@ -10,35 +10,39 @@ namespace gptq {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Layout, one launch: every operand's scale bytes as [block of 256 columns][row]
-// [8], so that a tile's for one step are contiguous; and the activations in 4
-// bits, rounded or copied, with zeros up to whole 256 columns.
+// Layout, one launch: every operand's scale bytes as [step][row][kPer], kPer blocks of
+// 32 columns a step, so that a tile's for one step are contiguous; and the
+// activations in 4 bits, rounded or copied, with zeros up to whole steps.
 // ---------------------------------------------------------------------------
+constexpr int kPer = 8;
+
 struct LayArgs {
   MxInput x;
   Mx w, up;
-  int64_t nbp;               // blocks of 32 padded to 8
+  int64_t nbp;               // blocks of 32 padded to whole steps
   int64_t npad, mpad;        // rows of the scales' layout
   uint8_t* xcodes;           // [n][16 nbp], or NULL (bf16; codes used as they lie)
-  uint8_t* xscale;           // [nbp / 8][npad][8], or NULL
-  uint8_t* wscale;           // [nbp / 8][mpad][8], then the other layer's
+  uint8_t* xscale;           // [nbp / kPer][npad][kPer], or NULL
+  uint8_t* wscale;           // [nbp / kPer][mpad][kPer], then the other layer's
   uint32_t runs;             // runs of 512 columns of a row
   unsigned blocks_x, blocks_xs, blocks_w;
   bool vec;
 };
 
-// Thread e: the eight scale bytes of one row and step; 127 (1) past the row's blocks.
+// Thread e: the scale bytes of one row and step; 127 (1) past the row's blocks.
 __device__ inline void lay_scales(const uint8_t* __restrict__ scales, int64_t rows, int64_t nb,
                                   int64_t pad, int64_t steps, uint8_t* __restrict__ out, int64_t e) {
   const int64_t step = e / pad, row = e % pad;
   if (step >= steps || row >= rows) return;
-  uint32_t v[2] = {0u, 0u};
+  uint32_t v[kPer / 4] = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t b = 8 * step + i;
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t b = kPer * step + i;
     v[i >> 2] |= (b < nb ? uint32_t(scales[row * nb + b]) : 127u) << (8 * (i & 3));
   }
-  reinterpret_cast<uint2*>(out)[step * pad + row] = make_uint2(v[0], v[1]);
+#pragma unroll
+  for (int i = 0; i < kPer / 4; ++i)
+    reinterpret_cast<uint32_t*>(out)[(step * pad + row) * (kPer / 4) + i] = v[i];
 }
 
 __global__ __launch_bounds__(256) void mx_lay_kernel(LayArgs a) {
@@ -67,35 +71,39 @@ __global__ __launch_bounds__(256) void mx_lay_kernel(LayArgs a) {
     const uint32_t byte = mx_scale_byte(m << 16);
     *out = byte == 255u ? 0u : mx_round8(v, mx_scale_f32(byte));
     if ((lane & 3) == 0)
-      a.xscale[((blk >> 3) * a.npad + row) * 8 + (blk & 7)] = static_cast<uint8_t>(byte);
+      a.xscale[(blk / kPer * a.npad + row) * kPer + blk % kPer] = static_cast<uint8_t>(byte);
     return;
   }
   b -= a.blocks_x;
   if (b < a.blocks_xs) {
-    lay_scales(a.x.scales, a.x.n, a.w.nb, a.npad, a.nbp / 8, a.xscale, int64_t(b) * 256 + tid);
+    lay_scales(a.x.scales, a.x.n, a.w.nb, a.npad, a.nbp / kPer, a.xscale, int64_t(b) * 256 + tid);
     return;
   }
   b -= a.blocks_xs;
   const bool second = b >= a.blocks_w;
   const Mx& w = second ? a.up : a.w;
-  lay_scales(w.scales, w.rows, w.nb, a.mpad, a.nbp / 8,
+  lay_scales(w.scales, w.rows, w.nb, a.mpad, a.nbp / kPer,
              a.wscale + (second ? a.nbp * a.mpad : 0), int64_t(b - (second ? a.blocks_w : 0)) * 256 + tid);
 }
 
 // ---------------------------------------------------------------------------
 // The product.  A workgroup of WM x WN waves owns TM activation rows x TN weight
-// rows; k goes by in blocks of 128 bytes of an activation row (256 4-bit or 64
-// bf16 values) through a ring of S stages in LDS, copied by global_load_lds (no
-// registers), one barrier per block.  KS shares of k, each with its own waves
-// and ring, where tiles are few and small.
-// In LDS a row of 128 bytes has its eight 16-byte units at c ^ ((r / 2) % 8):
-// copies (8 rows of 8 units) and fragment reads (16 rows, one unit each) pass
-// without bank conflicts.  Lane 16 q + r reads unit 2 q + s of its row in half s of
-// a block: 32 4-bit values, or 8 bf16 ones.  For bf16 a block of a weight
-// row is 32 bytes, of which the lane takes bytes 8 q .. + 7 (values 16 q .. + 15, those
-// of its activation units); rows with bit 3 set have their halves swapped, which
-// spreads a read over the banks.  Weights are the matrix instruction's first
-// operand: a lane then holds four consecutive columns of one activation row.
+// rows; k goes by in blocks of 128 bytes of an activation row (256 4-bit or 64 bf16
+// values) through a ring of S stages in LDS, copied by global_load_lds (no
+// registers), one barrier per block.  KS shares of k, each with its own waves and
+// ring, where tiles are few and small.
+// A wave reads the operands of its next half block into the registers that the
+// products of this one have freed.  With three stages, at the barrier of block kb block
+// kb + 1 has landed too, and no product waits behind a barrier for LDS; three stages of
+// 4-bit operands do not fit beside tiles of 256 x 256 (stages of half the length do: with
+// twice the barriers they take 231 us where these take 209, 8192 rows of 4096 into 11008).
+// In LDS a row has its 16-byte units at c ^ unit_swap(r): copies and fragment reads (16
+// rows, one unit each) pass without bank conflicts.  Lane 16 q + r reads unit q +
+// 4 s of its row in half s of a block: 32 4-bit values, or 8 bf16 ones.  With bf16 a
+// block of a weight row is 32 bytes, of which the lane takes word q + 4 s; rows with bit 3
+// set have their halves swapped, which spreads a read over the banks.  Weights are
+// the matrix instruction's first operand: a lane then holds four consecutive columns
+// of one activation row.
 // GATED: 16 rows of the gate's layer and 16 of the other in turn, so that a lane
 // holds both factors of a result.
 // ---------------------------------------------------------------------------
@@ -113,8 +121,13 @@ struct GemmMx {
 
 enum { kBf16 = 0, kFour = 1 };
 
+// A 16-byte read passes in four parts of 16 lanes, of which the first takes
+// rows 0 .. 3 and 12 .. 15 of one quarter of the wave with rows 4 .. 11 of the next, whose
+// unit differs in bit 0.
+constexpr int kRow = 128;    // bytes of an activation row and block
+__device__ inline int unit_swap(int r) { return (r >> 1) & 7; }
 __device__ inline uint32_t unit_at(int r, int c) {
-  return static_cast<uint32_t>(r * 128 + ((c ^ ((r >> 1) & 7)) << 4));
+  return static_cast<uint32_t>(r * kRow + ((c ^ unit_swap(r)) << 4));
 }
 
 template <int FORM, int TM, int TN, int WM, int WN, int KS, int S, bool GATED>
@@ -122,18 +135,23 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
                                                                   unsigned tiles, int vec_y) {
   constexpr int kWaves = WM * WN;                        // of one share of k
   constexpr int kFi = TM / WM / 16, kFj = TN / WN / 16;  // fragments of a wave
-  constexpr int kWRow = FORM == kFour ? 128 : 32;        // bytes of a weight row and block
-  constexpr int kLoadsX = TM / 8 / kWaves;               // copies of a wave and block
-  constexpr int kLoadsW = FORM == kFour ? TN / 8 / kWaves : 1;
-  constexpr int kLanesW = FORM == kFour ? 64 : TN * 2 / kWaves;
+  constexpr int kWRow = FORM == kFour ? kRow : 32;       // bytes of a weight row and block
+  constexpr int kCopyRows = 1024 / kRow;                 // rows of a wave's copy
+  constexpr int kLoadsX = TM / kCopyRows / kWaves;       // copies of a wave and block
+  constexpr int kLanesX = TM * kRow / 16 / kWaves >= 64 ? 64 : TM * kRow / 16 / kWaves;
+  constexpr int kUnitsW = TN * kWRow / 16 / kWaves;      // 16-byte units of a wave and block
+  constexpr int kLoadsW = kUnitsW > 64 ? kUnitsW / 64 : 1, kLanesW = kUnitsW > 64 ? 64 : kUnitsW;
   constexpr int kSRows = FORM == kFour ? TM + TN : TN;   // rows with scales
-  constexpr int kLanesS = kSRows / 2 / kWaves;
-  static_assert(TM % (8 * kWaves) == 0 && kLanesS >= 1 && kLanesS <= 64 && kLanesW <= 64 &&
-                (FORM != kFour || TN % (8 * kWaves) == 0), "copies divide evenly");
+  constexpr int kRowsS = 16 / kPer;                      // of them in 16 bytes
+  constexpr int kLanesS = kSRows / kRowsS / kWaves;
+  static_assert(TM % (kCopyRows * kWaves) == 0 && kLanesX == 64 && kLanesS >= 1 && kLanesS <= 64 &&
+                    kUnitsW % kLanesW == 0 && kSRows % (kRowsS * kWaves) == 0 && 16 % kRowsS == 0,
+                "copies divide evenly");
   static_assert(!GATED || (TN / WN) % 32 == 0, "a wave has both factors");
+  constexpr bool kEarly = S >= 3;                        // the next block has landed, too
   constexpr int kCopies = kLoadsX + kLoadsW + 1;
-  constexpr int kOffW = TM * 128, kOffS = kOffW + TN * kWRow;
-  constexpr int kStage = kOffS + kSRows * 8;
+  constexpr int kOffW = TM * kRow, kOffS = kOffW + TN * kWRow;
+  constexpr int kStage = kOffS + kSRows * kPer;
   constexpr int kRing = S * kStage;
   extern __shared__ __attribute__((aligned(16))) char lds_all[];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -165,34 +183,38 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
   uint32_t offx[kLoadsX];
 #pragma unroll
   for (int i = 0; i < kLoadsX; ++i) {
-    const int r = 8 * (kLoadsX * wv + i) + (lane >> 3);
-    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    const int r = kCopyRows * (kLoadsX * wv + i) + lane / (kRow / 16);
+    const int c = (lane % (kRow / 16)) ^ unit_swap(r);
     offx[i] = static_cast<uint32_t>((min<int64_t>(tb + r, a.n - 1) - tb) * a.ldx + 16 * c);
   }
-  // weights: 4-bit as the activations; bf16: 32 rows of two units a copy
-  const char* pw[kLoadsW];
+  // weights: units in the order of the stage.  4-bit: a copy's rows are of one layer; bf16: a
+  // lane's own pointer
+  constexpr int kUnits = kWRow / 16;
+  const char* pw = nullptr;
+  uint32_t offw[kLoadsW];
   int cw[kLoadsW];                           // the lane's unit of a block
 #pragma unroll
   for (int i = 0; i < kLoadsW; ++i) {
-    const int r = FORM == kFour ? 8 * (kLoadsW * wv + i) + (lane >> 3)
-                                : (kLanesW * wv + min(lane, kLanesW - 1)) >> 1;
-    cw[i] = FORM == kFour ? (lane & 7) ^ ((r >> 1) & 7) : (lane & 1) ^ ((r >> 3) & 1);
-    pw[i] = reinterpret_cast<const char*>(a.W[w_layer(r)]) + min<int64_t>(jb + w_row(r), a.m - 1) * ldw +
-            16 * cw[i];
+    const int u = kUnitsW * wv + 64 * i + min(lane, kLanesW - 1), r = u / kUnits;
+    cw[i] = (u % kUnits) ^ (FORM == kFour ? unit_swap(r) : (r >> 3) & 1);
+    offw[i] = static_cast<uint32_t>((min<int64_t>(jb + w_row(r), a.m - 1) - jb) * ldw + 16 * cw[i]);
+    if (FORM == kBf16) pw = reinterpret_cast<const char*>(a.W[w_layer(r)]) + jb * ldw + offw[i];
   }
-  // scales: 16 bytes are two rows'
+  const char* wbase[2] = {reinterpret_cast<const char*>(a.W[0]) + jb * ldw,
+                          reinterpret_cast<const char*>(a.W[1]) + jb * ldw};
+  // scales: 16 bytes are kRowsS rows'
   const char* ps;
   int64_t step_s;
   {
-    int r = 2 * (kLanesS * wv + min(lane, kLanesS - 1));
+    int r = kRowsS * (kLanesS * wv + min(lane, kLanesS - 1));
     if (FORM == kFour && r < TM) {
-      ps = reinterpret_cast<const char*>(a.xs) + (tb + r) * 8;
-      step_s = a.npad * 8;
+      ps = reinterpret_cast<const char*>(a.xs) + (tb + r) * kPer;
+      step_s = a.npad * kPer;
     } else {
       if (FORM == kFour) r -= TM;
-      step_s = a.mpad * 8;
-      ps = reinterpret_cast<const char*>(a.ws) + (jb + w_row(r)) * 8 +
-           (w_layer(r) ? step_s * ((a.nb + 7) / 8) : 0);
+      step_s = a.mpad * kPer;
+      ps = reinterpret_cast<const char*>(a.ws) + (jb + w_row(r)) * kPer +
+           (w_layer(r) ? step_s * ((a.nb + kPer - 1) / kPer) : 0);
     }
   }
   // copies of block kb into its stage (past the end: the last block again, into a
@@ -202,98 +224,112 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
     const int k = __builtin_amdgcn_readfirstlane(max(min(kb0 + kb, kb1 - 1), 0));
 #pragma unroll
     for (int i = 0; i < kLoadsX; ++i) {
-      const char* base = xbase + int64_t(k) * 128;
+      const char* base = xbase + int64_t(k) * kRow;
       uint32_t o = offx[i];                  // opaque: a scalar base and a 32-bit offset
       asm volatile("" : "+s"(base), "+v"(o));
-      __builtin_amdgcn_global_load_lds((gvoid)(base + o), (lvoid)(st + 8 * (kLoadsX * wv + i) * 128),
+      __builtin_amdgcn_global_load_lds((gvoid)(base + o), (lvoid)(st + 1024 * (kLoadsX * wv + i)),
                                        16, 0, 0);
     }
-    constexpr int kUnits = kWRow / 16;
 #pragma unroll
     for (int i = 0; i < kLoadsW; ++i) {
       // units past the row's last: that one again (the activations are 0 there)
-      const int over = max(kUnits * k + cw[i] - (a.nb - 1), 0);
-      const char* p = pw[i] + int64_t(k) * kWRow - 16 * over;
-      char* to = st + kOffW + (FORM == kFour ? 8 * (kLoadsW * wv + i) * 128 : kLanesW * wv * 16);
+      const int over = kUnits * (k + 1) > a.nb ? 16 * max(kUnits * k + cw[i] - (a.nb - 1), 0) : 0;
+      const char* p;
+      if (FORM == kFour) {
+        const char* base = wbase[w_layer((kUnitsW * wv + 64 * i) / kUnits)] + int64_t(k) * kWRow;
+        uint32_t o = offw[i] - over;
+        asm volatile("" : "+s"(base), "+v"(o));
+        p = base + o;
+      } else {
+        p = pw + (k * kWRow - over);
+      }
       if (kLanesW == 64 || lane < kLanesW)
-        __builtin_amdgcn_global_load_lds((gvoid)p, (lvoid)to, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((gvoid)p, (lvoid)(st + kOffW + 16 * (kUnitsW * wv + 64 * i)),
+                                         16, 0, 0);
     }
     const char* p = ps + (FORM == kFour ? k : k >> 2) * step_s;
     if (kLanesS == 64 || lane < kLanesS)
       __builtin_amdgcn_global_load_lds((gvoid)p, (lvoid)(st + kOffS + kLanesS * wv * 16), 16, 0, 0);
   };
-  const uint32_t ox = unit_at(wi + c16, 2 * q);
-  const uint32_t ow = kOffW + (FORM == kFour ? unit_at(wj + c16, 2 * q)
-                                             : uint32_t((wj + c16) * 32 + ((8 * q) ^ ((c16 & 8) << 1))));
-  const uint32_t osx = kOffS + (wi + c16) * 8 + 2 * q;
-  const uint32_t osw = kOffS + ((FORM == kFour ? TM : 0) + wj + c16) * 8 + (FORM == kFour ? 2 * q : q >> 1);
+  const uint32_t ox = unit_at(wi + c16, q);
+  const uint32_t ow = kOffW + (FORM == kFour ? unit_at(wj + c16, q)
+                                             : uint32_t((wj + c16) * 32 + 4 * q + ((c16 & 8) << 1)));
+  const uint32_t osx = kOffS + (wi + c16) * kPer + q;      // and q + 4, the second half's
+  const uint32_t osw = kOffS + ((FORM == kFour ? TM : 0) + wj + c16) * kPer + (FORM == kFour ? q : 0);
   f32x4 acc[kFi][kFj];
 #pragma unroll
   for (int i = 0; i < kFi; ++i)
 #pragma unroll
     for (int j = 0; j < kFj; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // the operands in work, and the weights of the step behind it
+  u32x4 fx[kFi], fw[kFj], nw[kFj];
+  uint32_t sx[kFi], sw[kFj], tw[kFj];        // 4-bit: scales
+  auto read_x = [&](int kb, int s, int i) {
+    const char* st = lds + (kb % S) * kStage;
+    fx[i] = *reinterpret_cast<const u32x4*>(st + (ox ^ (64 * s)) + 16 * kRow * i);
+    if (FORM == kFour) sx[i] = *reinterpret_cast<const uint8_t*>(st + osx + 4 * s + 16 * kPer * i);
+  };
+  auto read_w = [&](int kb, int s) {
+    const char* st = lds + (kb % S) * kStage;
+#pragma unroll
+    for (int j = 0; j < kFj; ++j) {
+      if (FORM == kFour) {
+        nw[j] = *reinterpret_cast<const u32x4*>(st + (ow ^ (64 * s)) + 16 * kRow * j);
+        tw[j] = *reinterpret_cast<const uint8_t*>(st + osw + 4 * s + 16 * kPer * j);
+      } else {
+        const uint32_t raw = *reinterpret_cast<const uint32_t*>(st + (ow ^ (16 * s)) + 512 * j);
+        // the block's place in its 256 columns
+        const uint32_t byte = *reinterpret_cast<const uint8_t*>(st + osw + 2 * ((kb0 + kb) & 3) + s + 128 * j);
+        nw[j] = mx_expand8(raw, mx_scale_f32(byte));
+      }
+    }
+  };
+  auto next_w = [&]() {
+#pragma unroll
+    for (int j = 0; j < kFj; ++j) {
+      fw[j] = nw[j];
+      if (FORM == kFour) sw[j] = tw[j];
+    }
+  };
+  auto read_first = [&](int kb) {
+    read_w(kb, 0);
+    next_w();
+#pragma unroll
+    for (int i = 0; i < kFi; ++i) read_x(kb, 0, i);
+  };
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
-  for (int kb = 0; kb < turns; ++kb) {
+  if (kEarly) {
     wait_vmcnt<(S - 2) * kCopies>();
-    // LDS reads of the stage that is filled next are done as well
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
+    read_first(0);
+  }
+  for (int kb = 0; kb < turns; ++kb) {
+    // block kb (kEarly: kb + 1) has landed for all; the stage of block kb - 1 is read (its last
+    // reads were waited for before their products)
+    wait_vmcnt<(kEarly ? S - 3 : 0) * kCopies>();
+    asm volatile("s_barrier" ::: "memory");
+    const bool done = KS > 1 && kb >= kb1 - kb0;
+    if (!kEarly && !done) read_first(kb);
     fetch(kb + S - 1);
-    if (KS > 1 && kb >= kb1 - kb0) continue;
-    const char* st = lds + (kb % S) * kStage;
-    if constexpr (FORM == kFour) {
-      uint32_t sx[kFi], sw[kFj];             // both halves' scales
+    if (done) continue;
 #pragma unroll
-      for (int i = 0; i < kFi; ++i) sx[i] = *reinterpret_cast<const uint16_t*>(st + osx + 128 * i);
+    for (int s = 0; s < 2; ++s) {
+      const int kn = s ? kb + 1 : kb, sn = 1 - s;
+      const bool more = kEarly || s == 0;
+      if (more) read_w(kn, sn);
 #pragma unroll
-      for (int j = 0; j < kFj; ++j) sw[j] = *reinterpret_cast<const uint16_t*>(st + osw + 128 * j);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        i32x8 fx[kFi], fw[kFj];
-#pragma unroll
-        for (int i = 0; i < kFi; ++i) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(st + (ox ^ (16 * s)) + 2048 * i);
-          fx[i] = i32x8{int(v[0]), int(v[1]), int(v[2]), int(v[3]), 0, 0, 0, 0};
-        }
+      for (int i = 0; i < kFi; ++i) {
 #pragma unroll
         for (int j = 0; j < kFj; ++j) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(st + (ow ^ (16 * s)) + 2048 * j);
-          fw[j] = i32x8{int(v[0]), int(v[1]), int(v[2]), int(v[3]), 0, 0, 0, 0};
+          if (FORM == kFour)
+            acc[i][j] = mx_mfma(fw[j], sw[j], fx[i], sx[i], acc[i][j]);
+          else
+            acc[i][j] = mfma16(fw[j], fx[i], acc[i][j]);
         }
-#pragma unroll
-        for (int j = 0; j < kFj; ++j)
-#pragma unroll
-          for (int i = 0; i < kFi; ++i) {
-            if (s == 0)
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  fw[j], fx[i], acc[i][j], 4, 4, 0, int(sw[j]), 0, int(sx[i]));
-            else
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  fw[j], fx[i], acc[i][j], 4, 4, 1, int(sw[j]), 1, int(sx[i]));
-          }
+        if (more) read_x(kn, sn, i);
       }
-    } else {
-      uint2 raw[kFj];
-      float sc[kFj];
-      const int sb = 2 * ((kb0 + kb) & 3);   // the block's place in its 256 columns
-#pragma unroll
-      for (int j = 0; j < kFj; ++j) {
-        raw[j] = *reinterpret_cast<const uint2*>(st + ow + 512 * j);
-        sc[j] = mx_scale_f32(*reinterpret_cast<const uint8_t*>(st + osw + sb + 128 * j));
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        u32x4 fx[kFi];
-#pragma unroll
-        for (int i = 0; i < kFi; ++i)
-          fx[i] = *reinterpret_cast<const u32x4*>(st + (ox ^ (16 * s)) + 2048 * i);
-#pragma unroll
-        for (int j = 0; j < kFj; ++j) {
-          const u32x4 fw = mx_expand8(s ? raw[j].y : raw[j].x, sc[j]);
-#pragma unroll
-          for (int i = 0; i < kFi; ++i) acc[i][j] = mfma16(fw, fx[i], acc[i][j]);
-        }
-      }
+      if (more) next_w();
     }
   }
   wait_vmcnt<0>();
@@ -395,8 +431,8 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
 
 template <int FORM, int TM, int TN, int WM, int WN, int KS, int S, bool GATED>
 gptq_status launch_tile(const GemmMx& a, hipStream_t st) {
-  constexpr int lds = KS * S * (TM * 128 + TN * (FORM == kFour ? 128 : 32) +
-                                (FORM == kFour ? TM + TN : TN) * 8);
+  constexpr int lds = KS * S * (FORM == kFour ? (TM + TN) * (kRow + kPer)
+                                              : TM * kRow + TN * (32 + kPer));
   static_assert(lds <= 160 * 1024, "the ring fits the LDS");
   const unsigned tj = ceil_div(a.m, GATED ? TN / 2 : TN);
   const unsigned tiles = tj * ceil_div(a.n, TM);
@@ -425,8 +461,8 @@ gptq_status launch_form(const GemmMx& a, hipStream_t st) {
   const double best = std::min(c256, std::min(c128, c64));
   constexpr int S = FORM == kFour ? 2 : 3;
   if (best == c256) return launch_tile<FORM, 256, 256, 2, 4, 1, S, GATED>(a, st);
-  if (best == c128) return launch_tile<FORM, 128, 128, 2, 2, 2, 2, GATED>(a, st);
-  return launch_tile<FORM, 64, 64, 2, 2, 4, 2, GATED>(a, st);
+  if (best == c128) return launch_tile<FORM, 128, 128, 2, 2, 2, S, GATED>(a, st);
+  return launch_tile<FORM, 64, 64, 2, 2, 4, S, GATED>(a, st);
 }
 
 bool as_is(const void* X, int64_t ldx, int64_t d) {
@@ -442,7 +478,7 @@ struct GemmWs {
 };
 
 GemmWs carve(Carver& c, int64_t n, int64_t m, int64_t d, int form, bool gated) {
-  const int64_t nc = std::min<int64_t>(n, kRowChunk), nbp = round_up(mx_blocks(d), 8);
+  const int64_t nc = std::min<int64_t>(n, kRowChunk), nbp = round_up(mx_blocks(d), kPer);
   GemmWs w{};
   w.wscale = c.take<uint8_t>(size_t(gated ? 2 : 1) * nbp * round_up(m, 256));
   if (form == GPTQ_MX_BF16) {
@@ -467,7 +503,7 @@ gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const Mx
   const bool gated = up.codes;
   Carver c(ws);
   const GemmWs b = carve(c, x.n, w.rows, x.d, x.form, gated);
-  const int64_t m = w.rows, nb = w.nb, nbp = round_up(nb, 8), mpad = round_up(m, 256);
+  const int64_t m = w.rows, nb = w.nb, nbp = round_up(nb, kPer), mpad = round_up(m, 256);
   for (int64_t t0 = 0; t0 < x.n; t0 += kRowChunk) {
     const int64_t nc = std::min<int64_t>(kRowChunk, x.n - t0), npad = round_up(nc, 256);
     GemmMx g{};
@@ -503,14 +539,14 @@ gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const Mx
       g.xs = b.xscale;
       g.npad = npad;
       g.ldx = nbp * 16;
-      g.kblocks = int(nbp / 8);
+      g.kblocks = int(nbp / kPer);
       l.xscale = b.xscale;
       g.X = reinterpret_cast<const char*>(b.xcodes);
       l.xcodes = b.xcodes;
       if (x.form == GPTQ_MX_CODES) {
         l.x.X = static_cast<const uint8_t*>(x.X) + t0 * nb * 16;
         l.x.scales = x.scales + t0 * nb;
-        l.blocks_xs = ceil_div(npad * (nbp / 8), 256);
+        l.blocks_xs = ceil_div(npad * (nbp / kPer), 256);
         if (nb == nbp) {                     // whole blocks: used as they lie
           g.X = static_cast<const char*>(l.x.X);
           l.xcodes = nullptr;
@@ -521,7 +557,7 @@ gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const Mx
       }
       if (l.xcodes) l.blocks_x = ceil_div(nc * l.runs, 4);
     }
-    if (t0 == 0) l.blocks_w = ceil_div(mpad * (nbp / 8), 256);
+    if (t0 == 0) l.blocks_w = ceil_div(mpad * (nbp / kPer), 256);
     const unsigned grid = l.blocks_x + l.blocks_xs + l.blocks_w * (gated ? 2 : 1);
     if (grid) {
       mx_lay_kernel<<<grid, 256, 0, st>>>(l);
