@@ -113,9 +113,14 @@ struct GemmMx {
   const uint8_t* xs;         // scales' layout (4-bit)
   int64_t npad;
   const uint8_t* W[2];       // codes [m][16 nb]
-  const uint8_t* ws;         // scales' layout, the second layer's behind
+  const uint8_t* S[2];       // their scales, as stored (s_rows) or in the layout
   int64_t mpad, m;
-  int nb, kblocks;
+  int nb, kblocks, s_rows;
+  // the sum over k in `splits` parts by workgroups of their own: fp32 [splits][n][ldp], the second
+  // factor's columns from ldp / 2 on
+  int splits;
+  float* part;
+  int64_t ldp;
   MxOutput y;
 };
 
@@ -131,7 +136,7 @@ __device__ inline uint32_t unit_at(int r, int c) {
 }
 
 template <int FORM, int TM, int TN, int WM, int WN, int KS, int S, bool GATED>
-__global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsigned tiles_j,
+__global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void mx_gemm_kernel(GemmMx a, unsigned tiles_j,
                                                                   unsigned tiles, int vec_y) {
   constexpr int kWaves = WM * WN;                        // of one share of k
   constexpr int kFi = TM / WM / 16, kFj = TN / WN / 16;  // fragments of a wave
@@ -142,12 +147,16 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
   constexpr int kUnitsW = TN * kWRow / 16 / kWaves;      // 16-byte units of a wave and block
   constexpr int kLoadsW = kUnitsW > 64 ? kUnitsW / 64 : 1, kLanesW = kUnitsW > 64 ? 64 : kUnitsW;
   constexpr int kSRows = FORM == kFour ? TM + TN : TN;   // rows with scales
-  constexpr int kRowsS = 16 / kPer;                      // of them in 16 bytes
-  constexpr int kLanesS = kSRows / kRowsS / kWaves;
+  // copied 16 bytes a lane (two rows), bf16: 4 (half a row), which the stored scales' alignment allows
+  constexpr int kBytesS = FORM == kFour ? 16 : 4;
+  constexpr int kLanesS = kSRows * kPer / kBytesS / kWaves;
   static_assert(TM % (kCopyRows * kWaves) == 0 && kLanesX == 64 && kLanesS >= 1 && kLanesS <= 64 &&
-                    kUnitsW % kLanesW == 0 && kSRows % (kRowsS * kWaves) == 0 && 16 % kRowsS == 0,
+                    kUnitsW % kLanesW == 0 && kSRows * kPer % (kBytesS * kWaves) == 0,
                 "copies divide evenly");
   static_assert(!GATED || (TN / WN) % 32 == 0, "a wave has both factors");
+  // copies one at a time behind the products of the first half block (two waves a SIMD: 423 us
+  // where all at once take 443, 8192 x 4096 -> 8192; smaller tiles need them earlier)
+  constexpr bool kSpread = FORM == kBf16 && TM * TN == 256 * 256;
   constexpr bool kEarly = S >= 3;                        // the next block has landed, too
   constexpr int kCopies = kLoadsX + kLoadsW + 1;
   constexpr int kOffW = TM * kRow, kOffS = kOffW + TN * kWRow;
@@ -162,7 +171,8 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
   // Each XCD (workgroups b, b + 8, ...) walks a contiguous range of tiles, in bands of
   // kBand activation tiles, so that its L2 takes in the fewest rows per step.
   constexpr unsigned kBand = 4;
-  unsigned tile = blockIdx.x;
+  const unsigned split = blockIdx.x / tiles;
+  unsigned tile = blockIdx.x % tiles;
   const unsigned per = tiles / 8;
   if (tile < 8 * per) tile = (tile % 8) * per + tile / 8;
   const unsigned tiles_t = tiles / tiles_j, band = tile / (kBand * tiles_j);
@@ -173,8 +183,9 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
   const int wi = (wv % WM) * (TM / WM), wj = (wv / WM) * (TN / WN);
 
   // this share's blocks; all shares turn as often as the longest
-  const int kb0 = a.kblocks * kg / KS, kb1 = a.kblocks * (kg + 1) / KS;
-  const int turns = (a.kblocks + KS - 1) / KS;
+  const int share = split * KS + kg, shares = a.splits * KS;
+  const int kb0 = a.kblocks * share / shares, kb1 = a.kblocks * (share + 1) / shares;
+  const int turns = (a.kblocks + shares - 1) / shares;
   // tile row r of the weights: its layer and row
   auto w_layer = [&](int r) { return GATED ? (r >> 4) & 1 : 0; };
   auto w_row = [&](int r) { return GATED ? (r >> 5) * 16 + (r & 15) : r; };
@@ -192,64 +203,85 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
   constexpr int kUnits = kWRow / 16;
   const char* pw = nullptr;
   uint32_t offw[kLoadsW];
-  int cw[kLoadsW];                           // the lane's unit of a block
+  // the lane's unit of a block in copy i
+  auto unit_w = [&](int i) {
+    const int u = kUnitsW * wv + 64 * i + min(lane, kLanesW - 1), r = u / kUnits;
+    return (u % kUnits) ^ (FORM == kFour ? unit_swap(r) : (r >> 3) & 1);
+  };
 #pragma unroll
   for (int i = 0; i < kLoadsW; ++i) {
     const int u = kUnitsW * wv + 64 * i + min(lane, kLanesW - 1), r = u / kUnits;
-    cw[i] = (u % kUnits) ^ (FORM == kFour ? unit_swap(r) : (r >> 3) & 1);
-    offw[i] = static_cast<uint32_t>((min<int64_t>(jb + w_row(r), a.m - 1) - jb) * ldw + 16 * cw[i]);
+    offw[i] = static_cast<uint32_t>((min<int64_t>(jb + w_row(r), a.m - 1) - jb) * ldw + 16 * unit_w(i));
     if (FORM == kBf16) pw = reinterpret_cast<const char*>(a.W[w_layer(r)]) + jb * ldw + offw[i];
   }
   const char* wbase[2] = {reinterpret_cast<const char*>(a.W[0]) + jb * ldw,
                           reinterpret_cast<const char*>(a.W[1]) + jb * ldw};
-  // scales: 16 bytes are kRowsS rows'
   const char* ps;
   int64_t step_s;
+  const int half_s = lane & 1;               // bf16: the lane's half of a row
   {
-    int r = kRowsS * (kLanesS * wv + min(lane, kLanesS - 1));
+    const int u = kLanesS * wv + min(lane, kLanesS - 1);
+    int r = FORM == kFour ? 2 * u : u >> 1;
     if (FORM == kFour && r < TM) {
       ps = reinterpret_cast<const char*>(a.xs) + (tb + r) * kPer;
       step_s = a.npad * kPer;
     } else {
       if (FORM == kFour) r -= TM;
-      step_s = a.mpad * kPer;
-      ps = reinterpret_cast<const char*>(a.ws) + (jb + w_row(r)) * kPer +
-           (w_layer(r) ? step_s * ((a.nb + kPer - 1) / kPer) : 0);
+      const int64_t row = jb + w_row(r);
+      if (a.s_rows) {                        // as stored
+        ps = reinterpret_cast<const char*>(a.S[w_layer(r)]) + min<int64_t>(row, a.m - 1) * a.nb;
+        step_s = kPer;
+      } else {
+        ps = reinterpret_cast<const char*>(a.S[w_layer(r)]) + row * kPer;
+        step_s = a.mpad * kPer;
+      }
+      if (FORM == kBf16) ps += 4 * half_s;
     }
   }
-  // copies of block kb into its stage (past the end: the last block again, into a
-  // stage nobody reads any more, so that every block counts alike)
-  auto fetch = [&](int kb) {
+  // copy p (of kCopies) of block kb into its stage (past the end: of the last block again,
+  // into a stage nobody reads any more, so that every block counts alike)
+  auto copy = [&](int kb, int p) {
     char* st = lds + (kb % S) * kStage;
     const int k = __builtin_amdgcn_readfirstlane(max(min(kb0 + kb, kb1 - 1), 0));
-#pragma unroll
-    for (int i = 0; i < kLoadsX; ++i) {
+    if (p < kLoadsX) {
+      const int i = p;
       const char* base = xbase + int64_t(k) * kRow;
       uint32_t o = offx[i];                  // opaque: a scalar base and a 32-bit offset
       asm volatile("" : "+s"(base), "+v"(o));
       __builtin_amdgcn_global_load_lds((gvoid)(base + o), (lvoid)(st + 1024 * (kLoadsX * wv + i)),
                                        16, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kLoadsW; ++i) {
+    } else if (p < kLoadsX + kLoadsW) {
+      const int i = p - kLoadsX;
       // units past the row's last: that one again (the activations are 0 there)
-      const int over = kUnits * (k + 1) > a.nb ? 16 * max(kUnits * k + cw[i] - (a.nb - 1), 0) : 0;
-      const char* p;
+      int over = 0;
+      if (kUnits * (k + 1) > a.nb) over = 16 * max(kUnits * k + unit_w(i) - (a.nb - 1), 0);
+      const char* from;
       if (FORM == kFour) {
         const char* base = wbase[w_layer((kUnitsW * wv + 64 * i) / kUnits)] + int64_t(k) * kWRow;
         uint32_t o = offw[i] - over;
         asm volatile("" : "+s"(base), "+v"(o));
-        p = base + o;
+        from = base + o;
       } else {
-        p = pw + (k * kWRow - over);
+        from = pw + (k * kWRow - over);
       }
       if (kLanesW == 64 || lane < kLanesW)
-        __builtin_amdgcn_global_load_lds((gvoid)p, (lvoid)(st + kOffW + 16 * (kUnitsW * wv + 64 * i)),
+        __builtin_amdgcn_global_load_lds((gvoid)from, (lvoid)(st + kOffW + 16 * (kUnitsW * wv + 64 * i)),
                                          16, 0, 0);
+    } else {
+      const int step = FORM == kFour ? k : k >> 2;
+      const char* from = ps + step * step_s;
+      // past the stored row's last four: those again (the activations are 0 there)
+      if (FORM == kBf16 && a.s_rows && kPer * (step + 1) > a.nb && half_s) from -= 4;
+      char* to = st + kOffS + kLanesS * wv * kBytesS;
+      if (kLanesS == 64 || lane < kLanesS) {
+        if constexpr (FORM == kFour) __builtin_amdgcn_global_load_lds((gvoid)from, (lvoid)to, 16, 0, 0);
+        else __builtin_amdgcn_global_load_lds((gvoid)from, (lvoid)to, 4, 0, 0);
+      }
     }
-    const char* p = ps + (FORM == kFour ? k : k >> 2) * step_s;
-    if (kLanesS == 64 || lane < kLanesS)
-      __builtin_amdgcn_global_load_lds((gvoid)p, (lvoid)(st + kOffS + kLanesS * wv * 16), 16, 0, 0);
+  };
+  auto fetch = [&](int kb) {
+#pragma unroll
+    for (int p = 0; p < kCopies; ++p) copy(kb, p);
   };
   const uint32_t ox = unit_at(wi + c16, q);
   const uint32_t ow = kOffW + (FORM == kFour ? unit_at(wj + c16, q)
@@ -269,6 +301,7 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
     fx[i] = *reinterpret_cast<const u32x4*>(st + (ox ^ (64 * s)) + 16 * kRow * i);
     if (FORM == kFour) sx[i] = *reinterpret_cast<const uint8_t*>(st + osx + 4 * s + 16 * kPer * i);
   };
+  uint32_t raw[kFj];                         // bf16: the next step's weights as stored, and scales
   auto read_w = [&](int kb, int s) {
     const char* st = lds + (kb % S) * kStage;
 #pragma unroll
@@ -277,12 +310,14 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
         nw[j] = *reinterpret_cast<const u32x4*>(st + (ow ^ (64 * s)) + 16 * kRow * j);
         tw[j] = *reinterpret_cast<const uint8_t*>(st + osw + 4 * s + 16 * kPer * j);
       } else {
-        const uint32_t raw = *reinterpret_cast<const uint32_t*>(st + (ow ^ (16 * s)) + 512 * j);
+        raw[j] = *reinterpret_cast<const uint32_t*>(st + (ow ^ (16 * s)) + 512 * j);
         // the block's place in its 256 columns
-        const uint32_t byte = *reinterpret_cast<const uint8_t*>(st + osw + 2 * ((kb0 + kb) & 3) + s + 128 * j);
-        nw[j] = mx_expand8(raw, mx_scale_f32(byte));
+        tw[j] = *reinterpret_cast<const uint8_t*>(st + osw + 2 * ((kb0 + kb) & 3) + s + 128 * j);
       }
     }
+  };
+  auto expand_w = [&](int j) {
+    if (FORM == kBf16) nw[j] = mx_expand8(raw[j], mx_scale_f32(tw[j]));
   };
   auto next_w = [&]() {
 #pragma unroll
@@ -293,9 +328,11 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
   };
   auto read_first = [&](int kb) {
     read_w(kb, 0);
-    next_w();
 #pragma unroll
     for (int i = 0; i < kFi; ++i) read_x(kb, 0, i);
+#pragma unroll
+    for (int j = 0; j < kFj; ++j) expand_w(j);
+    next_w();
   };
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
@@ -309,17 +346,26 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
     // reads were waited for before their products)
     wait_vmcnt<(kEarly ? S - 3 : 0) * kCopies>();
     asm volatile("s_barrier" ::: "memory");
-    const bool done = KS > 1 && kb >= kb1 - kb0;
-    if (!kEarly && !done) read_first(kb);
-    fetch(kb + S - 1);
-    if (done) continue;
+    const bool done = kb >= kb1 - kb0;
+    if (done) {
+      fetch(kb + S - 1);
+      continue;
+    }
+    if (!kEarly) read_first(kb);
+    if (!kSpread) fetch(kb + S - 1);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int kn = s ? kb + 1 : kb, sn = 1 - s;
       const bool more = kEarly || s == 0;
       if (more) read_w(kn, sn);
+      // in this order: left to itself the compiler puts the reads right before their use
 #pragma unroll
       for (int i = 0; i < kFi; ++i) {
+        if (more) {
+#pragma unroll
+          for (int j = 0; j < kFj; ++j)
+            if (i == (kFi > 1 ? 1 + j * (kFi - 1) / kFj : 0)) expand_w(j);
+        }
 #pragma unroll
         for (int j = 0; j < kFj; ++j) {
           if (FORM == kFour)
@@ -327,7 +373,13 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
           else
             acc[i][j] = mfma16(fw[j], fx[i], acc[i][j]);
         }
+        __builtin_amdgcn_sched_barrier(0);
         if (more) read_x(kn, sn, i);
+        if (kSpread && s == 0) {
+#pragma unroll
+          for (int p = 0; p < kCopies; ++p)
+            if (p * kFi / kCopies == i) copy(kb + S - 1, p);
+        }
       }
       if (more) next_w();
     }
@@ -412,6 +464,13 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
     int row = wi + 16 * i;                   // opaque: these rows' addresses only now
     asm volatile("" : "+s"(row));
     const int64_t t0 = tb + row;
+    if (a.part) {
+      float* part = a.part + split * a.n * a.ldp;
+      store(t0, part, a.ldp, false, [&](int j) { return acc[i][GATED ? 2 * j : j]; });
+      if constexpr (GATED)
+        store(t0, part + a.ldp / 2, a.ldp, false, [&](int j) { return acc[i][2 * j + 1]; });
+      continue;
+    }
     if constexpr (GATED) {
       store(t0, a.y.Y, a.y.ldy, true, [&](int j) {
         f32x4 v;
@@ -429,8 +488,57 @@ __global__ __launch_bounds__(WM* WN* KS * 64) void mx_gemm_kernel(GemmMx a, unsi
   }
 }
 
+// The parts of a sum added in their order, and what is made of them: four columns a thread.
+// (A row's columns in blockIdx.x, rows in blockIdx.y: at most kRowChunk.)
+__global__ __launch_bounds__(256) void mx_join_kernel(GemmMx a, int vec_y) {
+  const int64_t t = blockIdx.y;
+  const int64_t c = 4 * (int64_t(blockIdx.x) * 256 + threadIdx.x);
+  if (c >= a.m) return;
+  const bool gated = a.W[1];
+  const float* p = a.part + t * a.ldp + c;
+  f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f}, u = v;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    v += *reinterpret_cast<const f32x4*>(p + s * a.n * a.ldp);
+    if (gated) u += *reinterpret_cast<const f32x4*>(p + s * a.n * a.ldp + a.ldp / 2);
+  }
+  auto bf16 = [&](void* Y, int64_t ld, const f32x4& x) {
+    uint16_t* y = static_cast<uint16_t*>(Y) + t * ld + c;
+    if (vec_y && c + 4 <= a.m) {
+      *reinterpret_cast<uint2*>(y) =
+          make_uint2(uint32_t(f32_bf16(x[0])) | uint32_t(f32_bf16(x[1])) << 16,
+                     uint32_t(f32_bf16(x[2])) | uint32_t(f32_bf16(x[3])) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < a.m) y[i] = f32_bf16(x[i]);
+    }
+  };
+  if (gated) {
+    f32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mx_act(v[i], a.y.act) * u[i];
+    bf16(a.y.Y, a.y.ldy, y);
+    if (a.y.G) {
+      bf16(a.y.G, a.y.ldg, v);
+      bf16(a.y.U, a.y.ldg, u);
+    }
+  } else if (a.y.out_bf16) {
+    bf16(a.y.Y, a.y.ldy, v);
+  } else {
+    float* y = static_cast<float*>(a.y.Y) + t * a.y.ldy + c;
+    if (vec_y && c + 4 <= a.m) {
+      *reinterpret_cast<f32x4*>(y) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < a.m) y[i] = v[i];
+    }
+  }
+}
+
 template <int FORM, int TM, int TN, int WM, int WN, int KS, int S, bool GATED>
-gptq_status launch_tile(const GemmMx& a, hipStream_t st) {
+gptq_status launch_tile(GemmMx a, int splits, hipStream_t st) {
   constexpr int lds = KS * S * (FORM == kFour ? (TM + TN) * (kRow + kPer)
                                               : TM * kRow + TN * (32 + kPer));
   static_assert(lds <= 160 * 1024, "the ring fits the LDS");
@@ -441,28 +549,80 @@ gptq_status launch_tile(const GemmMx& a, hipStream_t st) {
   };
   const int vec_y = lines(a.y.Y, a.y.ldy * (a.y.out_bf16 ? 2 : 4)) &&
                     (!a.y.G || (lines(a.y.G, a.y.ldg * 2) && lines(a.y.U, a.y.ldg * 2)));
-  mx_gemm_kernel<FORM, TM, TN, WM, WN, KS, S, GATED><<<tiles, WM * WN * KS * 64, lds, st>>>(a, tj, tiles, vec_y);
+  a.splits = splits;
+  if (splits == 1) a.part = nullptr;
+  mx_gemm_kernel<FORM, TM, TN, WM, WN, KS, S, GATED>
+      <<<tiles * splits, WM * WN * KS * 64, lds, st>>>(a, tj, tiles, a.part ? 1 : vec_y);
   GPTQ_CHECK_LAUNCH();
+  if (splits > 1) {
+    mx_join_kernel<<<dim3(ceil_div(a.m, 1024), unsigned(a.n)), 256, 0, st>>>(a, vec_y);
+    GPTQ_CHECK_LAUNCH();
+  }
   return GPTQ_OK;
 }
 
-// Tiles by the time they take on 256 CUs: rounds of workgroups times a tile's
-// area over the rate measured for its shape (relative).
+// Tile and parts of the sum by the time they take (us, as measured): a CU's
+// workgroups, at most four at a time, turn once per block of k and share, in turn[c - 1] where c
+// of them are there; parts of the sum cost their bytes and a second launch.
+struct Shape {
+  int tm, tn, ks, resident;
+  double turn[4];
+};
+constexpr int kTiles = 5;
+constexpr Shape kShapes[2][kTiles] = {{{256, 256, 1, 1, {1.52}},
+                                       {128, 128, 2, 1, {1.13}},
+                                       {128, 128, 1, 2, {0.66, 1.08}},
+                                       {64, 64, 4, 1, {1.05}},
+                                       {64, 64, 1, 4, {0.42, 0.57, 0.73, 0.92}}},
+                                      {{256, 256, 1, 1, {1.8}},
+                                       {128, 128, 2, 1, {1.4}},
+                                       {128, 128, 1, 2, {0.9, 1.3}},
+                                       {64, 64, 4, 1, {1.3}},
+                                       {64, 64, 1, 4, {0.57, 0.69, 0.88, 1.08}}}};
+constexpr int kMaxSplits = 16;
+constexpr int64_t kPartFloats = int64_t(16) << 20;       // of all parts
+
+inline double time_of(const Shape& s, int64_t n, int64_t rows, int64_t kblocks, int splits) {
+  const int64_t wgs = int64_t(ceil_div(n, s.tm)) * ceil_div(rows, s.tn) * splits;
+  const double turns = double(ceil_div(kblocks, s.ks * splits)) + 2.0;
+  const int64_t most = (wgs + 255) / 256;    // of the fullest CU
+  const int64_t last = most % s.resident;
+  double time = turns * double(most / s.resident) * s.turn[s.resident - 1];
+  if (last) time += turns * s.turn[last - 1];
+  if (splits > 1) time += 3.0 + double(splits) * double(n * rows) * 8.0 / 4e6;
+  return time;
+}
+
+struct Choice {
+  int tile, splits;
+};
+inline Choice choose(int form, int64_t n, int64_t m, int64_t kblocks, bool gated) {
+  const int64_t rows = (gated ? 2 : 1) * round_up(m, 4);
+  const int64_t most = std::min<int64_t>(kMaxSplits, kPartFloats / (n * rows));
+  Choice c{0, 1};
+  double best = 1e30;
+  for (int i = 0; i < kTiles; ++i)
+    for (int p = 1; p == 1 || (p <= most && p * kShapes[form][i].ks * 2 <= kblocks); ++p) {
+      const double t = time_of(kShapes[form][i], n, rows, kblocks, p);
+      if (t < best) {
+        best = t;
+        c = Choice{i, p};
+      }
+    }
+  return c;
+}
+
 template <int FORM, bool GATED>
 gptq_status launch_form(const GemmMx& a, hipStream_t st) {
-  const int64_t rows = GATED ? 2 * a.m : a.m;
-  auto cost = [&](int tm, int tn, int per_cu, double rate) {
-    const int64_t tiles = int64_t(ceil_div(a.n, tm)) * ceil_div(rows, tn);
-    const int64_t rounds = (tiles + 256 * per_cu - 1) / (256 * per_cu);
-    const int64_t left = tiles - (rounds - 1) * 256 * per_cu;
-    return double((rounds - 1) * per_cu + (left + 255) / 256) * tm * tn / rate;
-  };
-  const double c256 = cost(256, 256, 1, 1.2), c128 = cost(128, 128, 1, 0.75), c64 = cost(64, 64, 2, 0.40);
-  const double best = std::min(c256, std::min(c128, c64));
+  const Choice c = choose(FORM, a.n, a.m, a.kblocks, GATED);
   constexpr int S = FORM == kFour ? 2 : 3;
-  if (best == c256) return launch_tile<FORM, 256, 256, 2, 4, 1, S, GATED>(a, st);
-  if (best == c128) return launch_tile<FORM, 128, 128, 2, 2, 2, S, GATED>(a, st);
-  return launch_tile<FORM, 64, 64, 2, 2, 4, S, GATED>(a, st);
+  switch (c.tile) {
+    case 0: return launch_tile<FORM, 256, 256, 2, 4, 1, S, GATED>(a, c.splits, st);
+    case 1: return launch_tile<FORM, 128, 128, 2, 2, 2, S, GATED>(a, c.splits, st);
+    case 2: return launch_tile<FORM, 128, 128, 2, 2, 1, S, GATED>(a, c.splits, st);
+    case 3: return launch_tile<FORM, 64, 64, 2, 2, 4, S, GATED>(a, c.splits, st);
+    default: return launch_tile<FORM, 64, 64, 2, 2, 1, S, GATED>(a, c.splits, st);
+  }
 }
 
 bool as_is(const void* X, int64_t ldx, int64_t d) {
@@ -470,7 +630,13 @@ bool as_is(const void* X, int64_t ldx, int64_t d) {
          ldx < (int64_t(1) << 22);
 }
 
+// Scales that 4-byte copies can take as they are stored.
+bool stored_scales(const Mx& w) {
+  return w.nb % 4 == 0 && reinterpret_cast<uintptr_t>(w.scales) % 4 == 0;
+}
+
 struct GemmWs {
+  float* part;               // of the sums over k
   uint8_t* xcodes;           // a chunk of rows
   uint8_t* xscale;
   uint8_t* wscale;
@@ -480,6 +646,16 @@ struct GemmWs {
 GemmWs carve(Carver& c, int64_t n, int64_t m, int64_t d, int form, bool gated) {
   const int64_t nc = std::min<int64_t>(n, kRowChunk), nbp = round_up(mx_blocks(d), kPer);
   GemmWs w{};
+  // a last, shorter chunk of rows may want more parts than a whole one
+  size_t floats = 0;
+  for (int64_t rows : {nc, n % kRowChunk}) {
+    if (rows == 0) continue;
+    const bool four = form != GPTQ_MX_BF16;
+    const int64_t kblocks = four ? nbp / kPer : (d + 63) / 64;
+    const int p = choose(four ? kFour : kBf16, rows, m, kblocks, gated).splits;
+    if (p > 1) floats = std::max(floats, size_t(p) * rows * (gated ? 2 : 1) * round_up(m, 4));
+  }
+  w.part = c.take<float>(floats);
   w.wscale = c.take<uint8_t>(size_t(gated ? 2 : 1) * nbp * round_up(m, 256));
   if (form == GPTQ_MX_BF16) {
     w.V2 = c.take<uint16_t>(size_t(nc) * round_up(d, 64));
@@ -510,7 +686,11 @@ gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const Mx
     g.n = nc;
     g.W[0] = w.codes;
     g.W[1] = up.codes;
-    g.ws = b.wscale;
+    g.part = b.part;
+    g.ldp = (gated ? 2 : 1) * round_up(m, 4);
+    g.s_rows = x.form == GPTQ_MX_BF16 && stored_scales(w) && (!gated || stored_scales(up));
+    g.S[0] = g.s_rows ? w.scales : b.wscale;
+    g.S[1] = g.s_rows ? up.scales : b.wscale + nbp * mpad;
     g.mpad = mpad;
     g.m = m;
     g.nb = int(nb);
@@ -557,7 +737,7 @@ gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const Mx
       }
       if (l.xcodes) l.blocks_x = ceil_div(nc * l.runs, 4);
     }
-    if (t0 == 0) l.blocks_w = ceil_div(mpad * (nbp / kPer), 256);
+    if (t0 == 0 && !g.s_rows) l.blocks_w = ceil_div(mpad * (nbp / kPer), 256);
     const unsigned grid = l.blocks_x + l.blocks_xs + l.blocks_w * (gated ? 2 : 1);
     if (grid) {
       mx_lay_kernel<<<grid, 256, 0, st>>>(l);
