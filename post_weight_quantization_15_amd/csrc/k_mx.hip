@@ -155,41 +155,48 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantizeArgs a) {
 // Layout in bf16 (exact) for the gradient's product
 // ---------------------------------------------------------------------------
 
-// Wt[c][j0 + j] = W[j][c] for 64 rows x 128 columns a workgroup, zeros for
-// rows past the matrix.  A thread takes the same eight columns of two
-// neighbouring rows and writes pairs to the turned tile in LDS (a column's
-// stride of 144 bytes puts a wave's two runs in different halves of the banks).
+// Wt[c][j0 + j] = W[j][c] for 64 rows x 256 columns a workgroup, zeros for
+// rows past the matrix.  A thread takes the same block of two neighbouring
+// rows and writes pairs to the turned tile in LDS, 32 lanes to 32 consecutive words of a
+// column; a wave's second block takes the other column of two first, whose words lie in other
+// banks.
 __global__ __launch_bounds__(256) void mx_turn_kernel(Mx w, Mx up, unsigned by_one, int64_t d,
                                                       uint16_t* __restrict__ Wt, int64_t ldt) {
-  __shared__ __attribute__((aligned(16))) uint32_t tile[128][36];
-  const int tid = threadIdx.x, pair = tid & 31;
+  __shared__ __attribute__((aligned(16))) uint32_t tile[256][36];
+  const int tid = threadIdx.x, pair = tid & 31, run = tid >> 5;
   const bool second = blockIdx.y >= by_one;
   const Mx& src = second ? up : w;
-  const int64_t c0 = int64_t(blockIdx.x) * 128, j0 = int64_t(blockIdx.y - (second ? by_one : 0)) * 64;
+  const int64_t c0 = int64_t(blockIdx.x) * 256, j0 = int64_t(blockIdx.y - (second ? by_one : 0)) * 64;
+  const int64_t b = c0 / kMxBlock + run;
+  u32x4 code[2];
+  float scale[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int run = (tid >> 5) + 8 * e;
-    const int64_t u = c0 / 8 + run;
-    u32x4 v[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t j = j0 + 2 * pair + h;
-      v[h] = u32x4{0u, 0u, 0u, 0u};
-      if (j < src.rows && u < 4 * src.nb)
-        v[h] = mx_expand8(reinterpret_cast<const uint32_t*>(src.codes)[j * 4 * src.nb + u],
-                          mx_scale_f32(src.scales[j * src.nb + (u >> 2)]));
+  for (int h = 0; h < 2; ++h) {
+    const int64_t j = j0 + 2 * pair + h;
+    code[h] = u32x4{0u, 0u, 0u, 0u};
+    scale[h] = 1.0f;
+    if (j < src.rows && b < src.nb) {
+      code[h] = *reinterpret_cast<const u32x4*>(src.codes + (j * src.nb + b) * 16);
+      scale[h] = mx_scale_f32(src.scales[j * src.nb + b]);
     }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const u32x4 lo = mx_expand8(code[0][e], scale[0]), hi = mx_expand8(code[1][e], scale[1]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      tile[8 * run + 2 * i][pair] = (v[0][i] & 0xFFFFu) | (v[1][i] << 16);
-      tile[8 * run + 2 * i + 1][pair] = (v[0][i] >> 16) | (v[1][i] & 0xFFFF0000u);
+      const uint32_t even = (lo[i] & 0xFFFFu) | (hi[i] << 16);
+      const uint32_t uneven = (lo[i] >> 16) | (hi[i] & 0xFFFF0000u);
+      const int c = 32 * run + 8 * e + 2 * i, odd = run & 1;
+      tile[c + odd][pair] = odd ? uneven : even;
+      tile[c + 1 - odd][pair] = odd ? even : uneven;
     }
   }
   __syncthreads();
   const int64_t at = int64_t(blockIdx.y) * 64;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int cl = (tid >> 3) + 32 * e, u = tid & 7;
+  for (int e = 0; e < 8; ++e) {
+    const int cl = run + 8 * (4 * e + (pair >> 3)), u = pair & 7;
     if (c0 + cl < d)
       *reinterpret_cast<u32x4*>(Wt + (c0 + cl) * ldt + at + 8 * u) =
           *reinterpret_cast<const u32x4*>(&tile[cl][4 * u]);
@@ -234,6 +241,7 @@ bool as_is(const uint16_t* V, int64_t ldv, int64_t len) {
 }
 
 struct TurnWs {
+  float* part;
   uint16_t* Wt;
   uint16_t* V2;
 };
@@ -241,15 +249,19 @@ struct TurnWs {
 TurnWs carve_turn(Carver& c, int64_t n, int64_t m, int64_t d, bool gated) {
   TurnWs w{};
   if (n == 0) return w;
-  const int64_t mp = round_up(m, 64);
-  w.Wt = c.take<uint16_t>(size_t(d) * mp * (gated ? 2 : 1));
+  const int64_t mp = round_up(m, 64), k = mp * (gated ? 2 : 1);
+  // a last, shorter chunk of rows may want more parts than a whole one
+  size_t floats = mx_dense_floats(std::min<int64_t>(n, kRowChunk), d, k);
+  if (n % kRowChunk) floats = std::max(floats, mx_dense_floats(n % kRowChunk, d, k));
+  w.part = c.take<float>(floats);
+  w.Wt = c.take<uint16_t>(size_t(d) * k);
   if (!gated) w.V2 = c.take<uint16_t>(size_t(std::min<int64_t>(n, kRowChunk)) * mp);
   return w;
 }
 
 gptq_status launch_turn(const Mx& w, const Mx& up, int64_t d, uint16_t* Wt, hipStream_t st) {
   const unsigned by = ceil_div(w.rows, 64), two = up.codes ? 2 : 1;
-  mx_turn_kernel<<<dim3(ceil_div(d, 128), by * two), 256, 0, st>>>(w, up, by, d, Wt,
+  mx_turn_kernel<<<dim3(ceil_div(d, 256), by * two), 256, 0, st>>>(w, up, by, d, Wt,
                                                                    int64_t(by) * 64 * two);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
@@ -299,26 +311,17 @@ gptq_status launch_mx_matmul_t(const uint16_t* dY, int64_t lddy, int64_t n, cons
   const int64_t mp = round_up(w.rows, 64);
   gptq_status s;
   if ((s = launch_turn(w, Mx{}, d, b.Wt, st)) != GPTQ_OK) return s;
-  GemmArgs g{};
-  g.m = d;
-  g.M = b.Wt;
-  g.ldm = mp;
-  g.kblocks = g.kwrap = int(mp / 64);
-  g.ldy = lddx;
-  g.out_bf16 = 1;
   const bool direct = as_is(dY, lddy, w.rows);
   for (int64_t t0 = 0; t0 < n; t0 += kRowChunk) {
     const int64_t nc = std::min<int64_t>(kRowChunk, n - t0);
-    g.V = dY + t0 * lddy;
-    g.ldv = lddy;
+    const uint16_t* V = dY + t0 * lddy;
     if (!direct) {
-      if ((s = launch_pad_rows(g.V, lddy, nc, w.rows, b.V2, mp, st)) != GPTQ_OK) return s;
-      g.V = b.V2;
-      g.ldv = mp;
+      if ((s = launch_pad_rows(V, lddy, nc, w.rows, b.V2, mp, st)) != GPTQ_OK) return s;
+      V = b.V2;
     }
-    g.n = nc;
-    g.Y = dX + t0 * lddx;
-    if ((s = launch_gemm(g, 0, st)) != GPTQ_OK) return s;
+    const MxOutput y{dX + t0 * lddx, lddx, 1, GPTQ_ACT_NONE, nullptr, nullptr, 0};
+    if ((s = launch_mx_dense(V, direct ? lddy : mp, nc, b.Wt, mp, d, mp, y, b.part, st)) != GPTQ_OK)
+      return s;
   }
   return GPTQ_OK;
 }
@@ -341,18 +344,13 @@ gptq_status launch_mx_gated_backward(const uint16_t* dY, int64_t lddy, int64_t n
   const TurnWs b = carve_turn(c, n, m, d, true);
   gptq_status s;
   if ((s = launch_turn(gate, up, d, b.Wt, st)) != GPTQ_OK) return s;
-  GemmArgs g{};
-  g.m = d;
-  g.M = b.Wt;
-  g.ldm = 2 * mp;
-  g.kblocks = g.kwrap = int(2 * mp / 64);
-  g.V = dGU;
-  g.ldv = 2 * mp;
-  g.n = n;
-  g.Y = dX;
-  g.ldy = lddx;
-  g.out_bf16 = 1;
-  return launch_gemm(g, 0, st);
+  for (int64_t t0 = 0; t0 < n; t0 += kRowChunk) {
+    const MxOutput y{dX + t0 * lddx, lddx, 1, GPTQ_ACT_NONE, nullptr, nullptr, 0};
+    if ((s = launch_mx_dense(dGU + t0 * 2 * mp, 2 * mp, std::min<int64_t>(kRowChunk, n - t0), b.Wt,
+                             2 * mp, d, 2 * mp, y, b.part, st)) != GPTQ_OK)
+      return s;
+  }
+  return GPTQ_OK;
 }
 
 }  // namespace gptq

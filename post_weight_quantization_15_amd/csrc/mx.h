@@ -66,6 +66,11 @@ size_t mx_gemm_ws_bytes(int64_t n, int64_t m, int64_t d, int form, bool gated);
 gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y, void* ws,
                            hipStream_t st);
 
+size_t mx_dense_floats(int64_t n, int64_t m, int64_t k);
+gptq_status launch_mx_dense(const uint16_t* V, int64_t ldv, int64_t n, const uint16_t* M,
+                            int64_t ldm, int64_t m, int64_t k, const MxOutput& y, float* part,
+                            hipStream_t st);
+
 #ifdef __HIPCC__
 namespace {
 
@@ -116,7 +121,8 @@ __device__ inline uint32_t mx_amax2(uint32_t m, uint32_t v) {
 }
 
 // acc += A B^T over 128 values of 16 rows each: a lane holds block lane / 16 of
-// its operands' row lane % 16, with the block's scale in byte 0.
+// its operands' row lane % 16, with the block's scale in byte B.
+template <int B>
 __device__ inline f32x4 mx_mfma(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb,
                                 const f32x4& c) {
   i32x8 va = {}, vb = {};
@@ -125,8 +131,8 @@ __device__ inline f32x4 mx_mfma(const u32x4& a, uint32_t sa, const u32x4& b, uin
     va[i] = static_cast<int>(a[i]);
     vb[i] = static_cast<int>(b[i]);
   }
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, 0, static_cast<int>(sa),
-                                                          0, static_cast<int>(sb));
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, B, static_cast<int>(sa),
+                                                          B, static_cast<int>(sb));
 }
 
 // The gate's activation and its slope.  The reciprocal is the hardware's (1 ulp).

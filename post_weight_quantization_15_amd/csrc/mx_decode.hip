@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kWaves * 64) void mx_decode_kernel(DecodeArgs a) {
         for (int j = 0; j < JT; ++j)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            acc[j][t] = mx_mfma(w[u][j], sc[u][j], x[t][0], sx[t], acc[j][t]);
+            acc[j][t] = mx_mfma<0>(w[u][j], sc[u][j], x[t][0], sx[t], acc[j][t]);
       }
     }
   }

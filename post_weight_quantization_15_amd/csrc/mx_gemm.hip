@@ -112,7 +112,8 @@ struct GemmMx {
   int64_t ldx, n;
   const uint8_t* xs;         // scales' layout (4-bit)
   int64_t npad;
-  const uint8_t* W[2];       // codes [m][16 nb]
+  const uint8_t* W[2];       // codes [m][16 nb], or (kDense) bf16 rows of ldw bytes
+  int64_t ldw;
   const uint8_t* S[2];       // their scales, as stored (s_rows) or in the layout
   int64_t mpad, m;
   int nb, kblocks, s_rows;
@@ -124,41 +125,50 @@ struct GemmMx {
   MxOutput y;
 };
 
-enum { kBf16 = 0, kFour = 1 };
+enum { kBf16 = 0, kFour = 1, kDense = 2 };
 
-// A 16-byte read passes in four parts of 16 lanes, of which the first takes
-// rows 0 .. 3 and 12 .. 15 of one quarter of the wave with rows 4 .. 11 of the next, whose
-// unit differs in bit 0.
 constexpr int kRow = 128;    // bytes of an activation row and block
-__device__ inline int unit_swap(int r) { return (r >> 1) & 7; }
+// A 16-byte read passes in four parts of 16 lanes, of which the first takes
+// rows 0 .. 3 and 12 .. 15 of one quarter of the wave with rows 4 .. 11 of the next.  Where the
+// next quarter's unit differs in bit 0 any turn by row pairs will do; where it differs in bit 1
+// (PAIR) row pairs 2 .. 5 have to lie in one half of the units, the others in the other one.
+template <bool PAIR>
+__device__ inline int unit_swap(int r) {
+  const int p = (r >> 1) & 7;
+  return PAIR ? (0x76321054 >> (4 * p)) & 7 : p;
+}
+template <bool PAIR>
 __device__ inline uint32_t unit_at(int r, int c) {
-  return static_cast<uint32_t>(r * kRow + ((c ^ unit_swap(r)) << 4));
+  return static_cast<uint32_t>(r * kRow + ((c ^ unit_swap<PAIR>(r)) << 4));
 }
 
 template <int FORM, int TM, int TN, int WM, int WN, int KS, int S, bool GATED>
 __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void mx_gemm_kernel(GemmMx a, unsigned tiles_j,
                                                                   unsigned tiles, int vec_y) {
   constexpr int kWaves = WM * WN;                        // of one share of k
+  constexpr bool kPair = FORM == kFour;                  // a lane's units: 2 q + s, else q + 4 s
+  constexpr int kFlip = kPair ? 16 : 64;                 // bytes that the other half's differ in
   constexpr int kFi = TM / WM / 16, kFj = TN / WN / 16;  // fragments of a wave
-  constexpr int kWRow = FORM == kFour ? kRow : 32;       // bytes of a weight row and block
+  constexpr int kWRow = FORM == kBf16 ? 32 : kRow;       // bytes of a weight row and block
   constexpr int kCopyRows = 1024 / kRow;                 // rows of a wave's copy
   constexpr int kLoadsX = TM / kCopyRows / kWaves;       // copies of a wave and block
   constexpr int kLanesX = TM * kRow / 16 / kWaves >= 64 ? 64 : TM * kRow / 16 / kWaves;
   constexpr int kUnitsW = TN * kWRow / 16 / kWaves;      // 16-byte units of a wave and block
   constexpr int kLoadsW = kUnitsW > 64 ? kUnitsW / 64 : 1, kLanesW = kUnitsW > 64 ? 64 : kUnitsW;
-  constexpr int kSRows = FORM == kFour ? TM + TN : TN;   // rows with scales
+  constexpr int kSRows = FORM == kFour ? TM + TN : FORM == kBf16 ? TN : 0;   // rows with scales
   // copied 16 bytes a lane (two rows), bf16: 4 (half a row), which the stored scales' alignment allows
   constexpr int kBytesS = FORM == kFour ? 16 : 4;
   constexpr int kLanesS = kSRows * kPer / kBytesS / kWaves;
-  static_assert(TM % (kCopyRows * kWaves) == 0 && kLanesX == 64 && kLanesS >= 1 && kLanesS <= 64 &&
+  static_assert(TM % (kCopyRows * kWaves) == 0 && kLanesX == 64 && kLanesS <= 64 &&
                     kUnitsW % kLanesW == 0 && kSRows * kPer % (kBytesS * kWaves) == 0,
                 "copies divide evenly");
   static_assert(!GATED || (TN / WN) % 32 == 0, "a wave has both factors");
   // copies one at a time behind the products of the first half block (two waves a SIMD: 423 us
   // where all at once take 443, 8192 x 4096 -> 8192; smaller tiles need them earlier)
   constexpr bool kSpread = FORM == kBf16 && TM * TN == 256 * 256;
-  constexpr bool kEarly = S >= 3;                        // the next block has landed, too
-  constexpr int kCopies = kLoadsX + kLoadsW + 1;
+  constexpr bool kEarly = FORM == kBf16;                 // the next block has landed, too
+  static_assert(S >= (kEarly ? 3 : 2), "stages");
+  constexpr int kCopies = kLoadsX + kLoadsW + (kSRows ? 1 : 0);
   constexpr int kOffW = TM * kRow, kOffS = kOffW + TN * kWRow;
   constexpr int kStage = kOffS + kSRows * kPer;
   constexpr int kRing = S * kStage;
@@ -189,13 +199,13 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
   // tile row r of the weights: its layer and row
   auto w_layer = [&](int r) { return GATED ? (r >> 4) & 1 : 0; };
   auto w_row = [&](int r) { return GATED ? (r >> 5) * 16 + (r & 15) : r; };
-  const int64_t ldw = int64_t(a.nb) * 16;
+  const int64_t ldw = FORM == kDense ? a.ldw : int64_t(a.nb) * 16;
   const char* xbase = a.X + tb * a.ldx;
   uint32_t offx[kLoadsX];
 #pragma unroll
   for (int i = 0; i < kLoadsX; ++i) {
     const int r = kCopyRows * (kLoadsX * wv + i) + lane / (kRow / 16);
-    const int c = (lane % (kRow / 16)) ^ unit_swap(r);
+    const int c = (lane % (kRow / 16)) ^ unit_swap<kPair>(r);
     offx[i] = static_cast<uint32_t>((min<int64_t>(tb + r, a.n - 1) - tb) * a.ldx + 16 * c);
   }
   // weights: units in the order of the stage.  4-bit: a copy's rows are of one layer; bf16: a
@@ -206,7 +216,7 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
   // the lane's unit of a block in copy i
   auto unit_w = [&](int i) {
     const int u = kUnitsW * wv + 64 * i + min(lane, kLanesW - 1), r = u / kUnits;
-    return (u % kUnits) ^ (FORM == kFour ? unit_swap(r) : (r >> 3) & 1);
+    return (u % kUnits) ^ (FORM == kBf16 ? (r >> 3) & 1 : unit_swap<kPair>(r));
   };
 #pragma unroll
   for (int i = 0; i < kLoadsW; ++i) {
@@ -216,10 +226,10 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
   }
   const char* wbase[2] = {reinterpret_cast<const char*>(a.W[0]) + jb * ldw,
                           reinterpret_cast<const char*>(a.W[1]) + jb * ldw};
-  const char* ps;
-  int64_t step_s;
+  const char* ps = nullptr;
+  int64_t step_s = 0;
   const int half_s = lane & 1;               // bf16: the lane's half of a row
-  {
+  if (FORM != kDense) {
     const int u = kLanesS * wv + min(lane, kLanesS - 1);
     int r = FORM == kFour ? 2 * u : u >> 1;
     if (FORM == kFour && r < TM) {
@@ -254,9 +264,9 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
       const int i = p - kLoadsX;
       // units past the row's last: that one again (the activations are 0 there)
       int over = 0;
-      if (kUnits * (k + 1) > a.nb) over = 16 * max(kUnits * k + unit_w(i) - (a.nb - 1), 0);
+      if (FORM != kDense && kUnits * (k + 1) > a.nb) over = 16 * max(kUnits * k + unit_w(i) - (a.nb - 1), 0);
       const char* from;
-      if (FORM == kFour) {
+      if (FORM != kBf16) {
         const char* base = wbase[w_layer((kUnitsW * wv + 64 * i) / kUnits)] + int64_t(k) * kWRow;
         uint32_t o = offw[i] - over;
         asm volatile("" : "+s"(base), "+v"(o));
@@ -267,7 +277,7 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
       if (kLanesW == 64 || lane < kLanesW)
         __builtin_amdgcn_global_load_lds((gvoid)from, (lvoid)(st + kOffW + 16 * (kUnitsW * wv + 64 * i)),
                                          16, 0, 0);
-    } else {
+    } else if (FORM != kDense) {
       const int step = FORM == kFour ? k : k >> 2;
       const char* from = ps + step * step_s;
       // past the stored row's last four: those again (the activations are 0 there)
@@ -283,11 +293,11 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
 #pragma unroll
     for (int p = 0; p < kCopies; ++p) copy(kb, p);
   };
-  const uint32_t ox = unit_at(wi + c16, q);
-  const uint32_t ow = kOffW + (FORM == kFour ? unit_at(wj + c16, q)
-                                             : uint32_t((wj + c16) * 32 + 4 * q + ((c16 & 8) << 1)));
-  const uint32_t osx = kOffS + (wi + c16) * kPer + q;      // and q + 4, the second half's
-  const uint32_t osw = kOffS + ((FORM == kFour ? TM : 0) + wj + c16) * kPer + (FORM == kFour ? q : 0);
+  const uint32_t ox = unit_at<kPair>(wi + c16, kPair ? 2 * q : q);
+  const uint32_t ow = kOffW + (FORM == kBf16 ? uint32_t((wj + c16) * 32 + 4 * q + ((c16 & 8) << 1))
+                                             : unit_at<kPair>(wj + c16, kPair ? 2 * q : q));
+  const uint32_t osx = kOffS + (wi + c16) * kPer + 2 * q;  // both halves' scales
+  const uint32_t osw = kOffS + ((FORM == kFour ? TM : 0) + wj + c16) * kPer + (FORM == kFour ? 2 * q : 0);
   f32x4 acc[kFi][kFj];
 #pragma unroll
   for (int i = 0; i < kFi; ++i)
@@ -298,17 +308,17 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
   uint32_t sx[kFi], sw[kFj], tw[kFj];        // 4-bit: scales
   auto read_x = [&](int kb, int s, int i) {
     const char* st = lds + (kb % S) * kStage;
-    fx[i] = *reinterpret_cast<const u32x4*>(st + (ox ^ (64 * s)) + 16 * kRow * i);
-    if (FORM == kFour) sx[i] = *reinterpret_cast<const uint8_t*>(st + osx + 4 * s + 16 * kPer * i);
+    fx[i] = *reinterpret_cast<const u32x4*>(st + (ox ^ (kFlip * s)) + 16 * kRow * i);
+    if (FORM == kFour && s == 0) sx[i] = *reinterpret_cast<const uint16_t*>(st + osx + 16 * kPer * i);
   };
   uint32_t raw[kFj];                         // bf16: the next step's weights as stored, and scales
   auto read_w = [&](int kb, int s) {
     const char* st = lds + (kb % S) * kStage;
 #pragma unroll
     for (int j = 0; j < kFj; ++j) {
-      if (FORM == kFour) {
-        nw[j] = *reinterpret_cast<const u32x4*>(st + (ow ^ (64 * s)) + 16 * kRow * j);
-        tw[j] = *reinterpret_cast<const uint8_t*>(st + osw + 4 * s + 16 * kPer * j);
+      if (FORM != kBf16) {
+        nw[j] = *reinterpret_cast<const u32x4*>(st + (ow ^ (kFlip * s)) + 16 * kRow * j);
+        if (FORM == kFour && s == 0) tw[j] = *reinterpret_cast<const uint16_t*>(st + osw + 16 * kPer * j);
       } else {
         raw[j] = *reinterpret_cast<const uint32_t*>(st + (ow ^ (16 * s)) + 512 * j);
         // the block's place in its 256 columns
@@ -351,37 +361,46 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
       fetch(kb + S - 1);
       continue;
     }
-    if (!kEarly) read_first(kb);
     if (!kSpread) fetch(kb + S - 1);
+    if constexpr (kEarly) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int kn = s ? kb + 1 : kb, sn = 1 - s;
-      const bool more = kEarly || s == 0;
-      if (more) read_w(kn, sn);
-      // in this order: left to itself the compiler puts the reads right before their use
+      for (int s = 0; s < 2; ++s) {
+        const int kn = s ? kb + 1 : kb, sn = 1 - s;
+        read_w(kn, sn);
+        // in this order: left to itself the compiler puts the reads right before their use
 #pragma unroll
-      for (int i = 0; i < kFi; ++i) {
-        if (more) {
+        for (int i = 0; i < kFi; ++i) {
 #pragma unroll
           for (int j = 0; j < kFj; ++j)
             if (i == (kFi > 1 ? 1 + j * (kFi - 1) / kFj : 0)) expand_w(j);
-        }
 #pragma unroll
-        for (int j = 0; j < kFj; ++j) {
-          if (FORM == kFour)
-            acc[i][j] = mx_mfma(fw[j], sw[j], fx[i], sx[i], acc[i][j]);
-          else
-            acc[i][j] = mfma16(fw[j], fx[i], acc[i][j]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) read_x(kn, sn, i);
-        if (kSpread && s == 0) {
+          for (int j = 0; j < kFj; ++j) acc[i][j] = mfma16(fw[j], fx[i], acc[i][j]);
+          __builtin_amdgcn_sched_barrier(0);
+          read_x(kn, sn, i);
+          if (kSpread && s == 0) {
 #pragma unroll
-          for (int p = 0; p < kCopies; ++p)
-            if (p * kFi / kCopies == i) copy(kb + S - 1, p);
+            for (int p = 0; p < kCopies; ++p)
+              if (p * kFi / kCopies == i) copy(kb + S - 1, p);
+          }
         }
+        next_w();
       }
-      if (more) next_w();
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        read_w(kb, s);
+        next_w();
+#pragma unroll
+        for (int i = 0; i < kFi; ++i) read_x(kb, s, i);
+#pragma unroll
+        for (int j = 0; j < kFj; ++j)
+#pragma unroll
+          for (int i = 0; i < kFi; ++i) {
+            if (FORM != kFour) acc[i][j] = mfma16(fw[j], fx[i], acc[i][j]);
+            else if (s == 0) acc[i][j] = mx_mfma<0>(fw[j], sw[j], fx[i], sx[i], acc[i][j]);
+            else acc[i][j] = mx_mfma<1>(fw[j], sw[j], fx[i], sx[i], acc[i][j]);
+          }
+      }
     }
   }
   wait_vmcnt<0>();
@@ -539,8 +558,9 @@ __global__ __launch_bounds__(256) void mx_join_kernel(GemmMx a, int vec_y) {
 
 template <int FORM, int TM, int TN, int WM, int WN, int KS, int S, bool GATED>
 gptq_status launch_tile(GemmMx a, int splits, hipStream_t st) {
-  constexpr int lds = KS * S * (FORM == kFour ? (TM + TN) * (kRow + kPer)
-                                              : TM * kRow + TN * (32 + kPer));
+  constexpr int lds = KS * S * (FORM == kFour   ? (TM + TN) * (kRow + kPer)
+                                : FORM == kBf16 ? TM * kRow + TN * (32 + kPer)
+                                                : (TM + TN) * kRow);
   static_assert(lds <= 160 * 1024, "the ring fits the LDS");
   const unsigned tj = ceil_div(a.m, GATED ? TN / 2 : TN);
   const unsigned tiles = tj * ceil_div(a.n, TM);
@@ -569,7 +589,7 @@ struct Shape {
   double turn[4];
 };
 constexpr int kTiles = 5;
-constexpr Shape kShapes[2][kTiles] = {{{256, 256, 1, 1, {1.52}},
+constexpr Shape kShapes[3][kTiles] = {{{256, 256, 1, 1, {1.52}},
                                        {128, 128, 2, 1, {1.13}},
                                        {128, 128, 1, 2, {0.66, 1.08}},
                                        {64, 64, 4, 1, {1.05}},
@@ -578,7 +598,12 @@ constexpr Shape kShapes[2][kTiles] = {{{256, 256, 1, 1, {1.52}},
                                        {128, 128, 2, 1, {1.4}},
                                        {128, 128, 1, 2, {0.9, 1.3}},
                                        {64, 64, 4, 1, {1.3}},
-                                       {64, 64, 1, 4, {0.57, 0.69, 0.88, 1.08}}}};
+                                       {64, 64, 1, 4, {0.57, 0.69, 0.88, 1.08}}},
+                                      {{256, 256, 1, 1, {1.5}},
+                                       {128, 128, 2, 1, {1.25}},
+                                       {128, 128, 1, 2, {0.75, 1.1}},
+                                       {64, 64, 4, 1, {1.2}},
+                                       {64, 64, 1, 4, {0.5, 0.6, 0.8, 1.0}}}};
 constexpr int kMaxSplits = 16;
 constexpr int64_t kPartFloats = int64_t(16) << 20;       // of all parts
 
@@ -615,7 +640,7 @@ inline Choice choose(int form, int64_t n, int64_t m, int64_t kblocks, bool gated
 template <int FORM, bool GATED>
 gptq_status launch_form(const GemmMx& a, hipStream_t st) {
   const Choice c = choose(FORM, a.n, a.m, a.kblocks, GATED);
-  constexpr int S = FORM == kFour ? 2 : 3;
+  constexpr int S = FORM == kBf16 ? 3 : 2;
   switch (c.tile) {
     case 0: return launch_tile<FORM, 256, 256, 2, 4, 1, S, GATED>(a, c.splits, st);
     case 1: return launch_tile<FORM, 128, 128, 2, 2, 2, S, GATED>(a, c.splits, st);
@@ -750,6 +775,29 @@ gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const Mx
     if (s != GPTQ_OK) return s;
   }
   return GPTQ_OK;
+}
+
+// Y = V M^T, both bf16: rows 16-byte aligned, k in blocks of 64, n at most kRowChunk.
+size_t mx_dense_floats(int64_t n, int64_t m, int64_t k) {
+  const int p = choose(kDense, n, m, k / 64, false).splits;
+  return p > 1 ? size_t(p) * n * round_up(m, 4) : 0;
+}
+
+gptq_status launch_mx_dense(const uint16_t* V, int64_t ldv, int64_t n, const uint16_t* M,
+                            int64_t ldm, int64_t m, int64_t k, const MxOutput& y, float* part,
+                            hipStream_t st) {
+  GemmMx g{};
+  g.X = reinterpret_cast<const char*>(V);
+  g.ldx = ldv * 2;
+  g.n = n;
+  g.W[0] = reinterpret_cast<const uint8_t*>(M);
+  g.ldw = ldm * 2;
+  g.m = m;
+  g.kblocks = int(k / 64);
+  g.part = part;
+  g.ldp = round_up(m, 4);
+  g.y = y;
+  return launch_form<kDense, false>(g, st);
 }
 
 }  // namespace gptq
