@@ -288,13 +288,13 @@ gptq_status launch_mx_quantize(const void* X, gptq_dtype dt, int64_t n, int64_t 
 }
 
 size_t mx_matmul_ws_bytes(int64_t n, int64_t m, int64_t d, int form, bool gated) {
-  return n <= kMxDecodeRows ? 0 : mx_gemm_ws_bytes(n, m, d, form, gated);
+  return mx_decode_takes(n, m, d, form, gated) ? 0 : mx_gemm_ws_bytes(n, m, d, form, gated);
 }
 
 gptq_status launch_mx_matmul(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y,
                              void* ws, hipStream_t st) {
-  return x.n <= kMxDecodeRows ? launch_mx_decode(x, w, up, y, st)
-                              : launch_mx_gemm(x, w, up, y, ws, st);
+  return mx_decode_takes(x.n, w.rows, x.d, x.form, up.codes) ? launch_mx_decode(x, w, up, y, st)
+                                                             : launch_mx_gemm(x, w, up, y, ws, st);
 }
 
 size_t mx_matmul_t_ws_bytes(int64_t n, int64_t m, int64_t d, bool gated) {

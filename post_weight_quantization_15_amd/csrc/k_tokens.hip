@@ -213,9 +213,19 @@ struct TokenArgs {
   uint64_t* part_top;                        // [n][parts][k]
 };
 
-// What the row's sums say; one thread.
+// The row's token's logit (0 without a token); asked for at the start, for two
+// loads one behind the other.
 template <int DT>
-__device__ inline void finish_row(const TokenArgs& a, int64_t row, double ref, double s, double t) {
+__device__ inline float token_logit(const TokenArgs& a, int64_t row, bool& given) {
+  const int id = a.token ? a.token[row] : -1;
+  given = id >= 0 && id < a.vocab;
+  if (!given) return 0.0f;
+  return to_f32<DT>(static_cast<const typename Cells<DT>::type*>(a.logits)[row * a.ldl + id]);
+}
+
+// What the row's sums say; one thread.
+__device__ inline void finish_row(const TokenArgs& a, int64_t row, double ref, double s, double t,
+                                  bool given, float x) {
   double lse, rest, h;
   if (s == 0.0) {                            // nothing but -inf
     lse = rest = -INFINITY;
@@ -225,15 +235,8 @@ __device__ inline void finish_row(const TokenArgs& a, int64_t row, double ref, d
     lse = ref * a.inv_temp + rest;
     h = rest - kLn2 * (t / s);
   }
-  if (a.logp) {
-    const int id = a.token ? a.token[row] : -1;
-    double lp = 0.0;
-    if (id >= 0 && id < a.vocab) {
-      const float x = to_f32<DT>(static_cast<const typename Cells<DT>::type*>(a.logits)[row * a.ldl + id]);
-      lp = s == 0.0 ? h : (double(x) - ref) * a.inv_temp - rest;
-    }
-    a.logp[row] = static_cast<float>(lp);
-  }
+  if (a.logp)
+    a.logp[row] = given ? static_cast<float>(s == 0.0 ? h : (double(x) - ref) * a.inv_temp - rest) : 0.0f;
   if (a.entropy) a.entropy[row] = static_cast<float>(h);
   if (a.lse) a.lse[row] = static_cast<float>(lse);
   if (a.stats) {
@@ -307,7 +310,12 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
   };
 #pragma unroll
   for (int s = 0; s < kAhead; ++s) load(ring[s], s);
-  if (tid == 0) cnt = 0;
+  bool given = false;
+  float token_x = 0.0f;
+  if (tid == 0) {
+    cnt = 0;
+    if (a.parts == 1) token_x = token_logit<DT>(a, row, given);
+  }
   float ez = -INFINITY;
   if (edge >= 0) ez = to_f32<DT>(src[edge]);
   __syncthreads();
@@ -496,7 +504,8 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
         __syncthreads();
       }
       have = now;
-      if (now > a.k) {
+      // (few are put in order as they are, below)
+      if (now > (again || step + 1 < steps ? a.k : max(a.k, kThreads))) {
         const uint64_t least = kth_entry(buf, now, a.k, sc);
         keep_from(buf, now, least, sc);
         have = a.k;
@@ -525,7 +534,7 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
     join_sums(r, s, t, c);
     if (lane == 0) {
       if (a.parts == 1) {
-        finish_row<DT>(a, row, r, s, t);
+        finish_row(a, row, r, s, t, given, token_x);
       } else {
         double* o = a.part_sums + (row * a.parts + part) * 3;
         o[0] = r;
@@ -553,17 +562,29 @@ __global__ __launch_bounds__(kThreads) void tokens_join_kernel(TokenArgs a) {
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   const uint64_t* in = a.part_top + row * a.parts * a.k;
-  if (tid == 0) cnt = 0;
+  bool given = false;
+  float token_x = 0.0f;
+  double r = kLowest, s = 0.0, t = 0.0;      // a part's sums in a lane: at most 64 parts
+  if (tid == 0) {
+    cnt = 0;
+    token_x = token_logit<DT>(a, row, given);
+  }
+  if (tid < a.parts) {
+    const double* p = a.part_sums + (row * a.parts + tid) * 3;
+    r = p[0];
+    s = p[1];
+    t = p[2];
+  }
   uint64_t bar = 0u;
   if (a.k) {
-    // as for a part's first cells: for all parts, a quarter and one
-    uint32_t best = 0u;
-    for (int p = a.parts; p > 0; p = p > 4 ? p >> 2 : p > 1 ? 1 : 0) {
-      const int lane = tid & 63, want = (a.k + p - 1) / p;
-      const uint32_t pick = reached_by(lane < a.parts ? order_in(in[lane * a.k + want - 1]) : 0u, p);
-      best = pick > best ? pick : best;
-    }
-    bar = uint64_t(best) << 18;
+    // as for a part's first cells: for all parts and for a quarter of them
+    const int lane = tid & 63, few = max(a.parts / 4, 1);
+    const uint64_t* mine = in + min(lane, a.parts - 1) * a.k;
+    const uint32_t all = order_in(mine[(a.k + a.parts - 1) / a.parts - 1]);
+    const uint32_t some = order_in(mine[(a.k + few - 1) / few - 1]);
+    const uint32_t x = reached_by(lane < a.parts ? all : 0u, a.parts);
+    const uint32_t y = reached_by(lane < a.parts ? some : 0u, few);
+    bar = uint64_t(max(x, y)) << 18;
   }
   __syncthreads();
   if (a.k) {
@@ -574,7 +595,7 @@ __global__ __launch_bounds__(kThreads) void tokens_join_kernel(TokenArgs a) {
     __syncthreads();
     int have = cnt;
     __syncthreads();
-    if (have > kByRank || have > a.k) {
+    if (have > max(a.k, kThreads)) {
       const uint64_t least = kth_entry(buf, have, a.k, sc);
       keep_from(buf, have, least, sc);
       have = a.k;
@@ -582,12 +603,9 @@ __global__ __launch_bounds__(kThreads) void tokens_join_kernel(TokenArgs a) {
     sort_by_rank(buf, have);
     write_top(a, row, buf, have);
   }
-  if (tid < 64) {                            // at most 64 parts
-    const double* p = a.part_sums + (row * a.parts + tid) * 3;
-    const bool in = tid < a.parts;
-    double r = in ? p[0] : double(kLowest), s = in ? p[1] : 0.0, t = in ? p[2] : 0.0;
+  if (tid < 64) {
     join_sums(r, s, t, static_cast<float>(a.inv_temp) * kLog2e);
-    if (tid == 0) finish_row<DT>(a, row, r, s, t);
+    if (tid == 0) finish_row(a, row, r, s, t, given, token_x);
   }
 }
 

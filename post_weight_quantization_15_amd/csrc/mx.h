@@ -56,13 +56,15 @@ gptq_status launch_mx_gated_backward(const uint16_t* dY, int64_t lddy, int64_t n
                                      uint16_t* dX, int64_t lddx, uint16_t* dGU, void* ws,
                                      hipStream_t st);
 
-// Few rows (mx_decode.hip): no workspace.
-constexpr int64_t kMxDecodeRows = 64;
+// Few rows (mx_decode.hip): no workspace.  Up to 16 rows, and up to 64 where it takes less time
+// than tiles.
+bool mx_decode_takes(int64_t n, int64_t m, int64_t d, int form, bool gated);
 gptq_status launch_mx_decode(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y,
                              hipStream_t st);
 
 // Many rows (mx_gemm.hip).
 size_t mx_gemm_ws_bytes(int64_t n, int64_t m, int64_t d, int form, bool gated);
+double mx_gemm_time(int64_t n, int64_t m, int64_t d, int form, bool gated);   // us, estimated
 gptq_status launch_mx_gemm(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y, void* ws,
                            hipStream_t st);
 

@@ -195,6 +195,18 @@ gptq_status launch_form(const DecodeArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// Every 16 output columns read all activations again, which takes over from 16
+// rows on (7.5 TB/s from the L2s, as measured: 64 rows of 4096 into 11008 take 54 us here, 28 in
+// tiles; of 4096 into 1024 columns 7 and 9).
+bool mx_decode_takes(int64_t n, int64_t m, int64_t d, int form, bool gated) {
+  if (n <= 16) return true;
+  if (n > 64) return false;
+  const double row = form == GPTQ_MX_CODES ? d * 0.5 : d * 2.0;
+  const double bytes = double(ceil_div(m, 16)) * double(round_up(n, 16)) * row +
+                       double(m) * double(d) * (gated ? 1.06 : 0.53);
+  return 3.0 + bytes / 7.5e6 < 2.5 + mx_gemm_time(n, m, d, form, gated);
+}
+
 gptq_status launch_mx_decode(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y,
                              hipStream_t st) {
   if (x.n == 0) return GPTQ_OK;

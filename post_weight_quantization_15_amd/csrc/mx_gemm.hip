@@ -620,19 +620,16 @@ inline double time_of(const Shape& s, int64_t n, int64_t rows, int64_t kblocks, 
 
 struct Choice {
   int tile, splits;
+  double time;
 };
 inline Choice choose(int form, int64_t n, int64_t m, int64_t kblocks, bool gated) {
   const int64_t rows = (gated ? 2 : 1) * round_up(m, 4);
   const int64_t most = std::min<int64_t>(kMaxSplits, kPartFloats / (n * rows));
-  Choice c{0, 1};
-  double best = 1e30;
+  Choice c{0, 1, 1e30};
   for (int i = 0; i < kTiles; ++i)
     for (int p = 1; p == 1 || (p <= most && p * kShapes[form][i].ks * 2 <= kblocks); ++p) {
       const double t = time_of(kShapes[form][i], n, rows, kblocks, p);
-      if (t < best) {
-        best = t;
-        c = Choice{i, p};
-      }
+      if (t < c.time) c = Choice{i, p, t};
     }
   return c;
 }
@@ -692,6 +689,11 @@ GemmWs carve(Carver& c, int64_t n, int64_t m, int64_t d, int form, bool gated) {
 }
 
 }  // namespace
+
+double mx_gemm_time(int64_t n, int64_t m, int64_t d, int form, bool gated) {
+  if (form == GPTQ_MX_BF16) return choose(kBf16, n, m, (d + 63) / 64, gated).time;
+  return choose(kFour, n, m, ceil_div(mx_blocks(d), kPer), gated).time + 4.0;   // and the layout
+}
 
 size_t mx_gemm_ws_bytes(int64_t n, int64_t m, int64_t d, int form, bool gated) {
   Carver c(nullptr);
