@@ -10,6 +10,8 @@
 // + v of product i, in both operands).  Activations to be rounded are rounded
 // on the way: a lane holds a whole block, so its scale needs no exchange.  The
 // waves' sums meet in LDS in the order of k.
+#include <algorithm>
+
 #include "mx.h"
 
 namespace gptq {
@@ -175,6 +177,167 @@ __global__ __launch_bounds__(kWaves * 64) void mx_decode_kernel(DecodeArgs a) {
   }
 }
 
+// Up to 16 activation rows, where the weights' stream is the whole of it: one workgroup a CU
+// goes through row tiles, the next loads under way beside the products, the sums in two sets
+// of LDS in turn.  KEEP: a wave's share of the activations (at most kSlabs slabs) stays in
+// registers.
+template <int FORM, bool GATED, bool KEEP>
+__global__ __launch_bounds__(kWaves * 64, 2) void mx_stream_kernel(DecodeArgs a, int tiles) {
+  constexpr int JT = GATED ? 2 : 1;
+  __shared__ f32x4 sums[2][kWaves][JT][64];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  const int nb = static_cast<int>(a.w.nb), slabs = (nb + 3) / 4;
+  const int s0 = slabs * wv / kWaves, s1 = slabs * (wv + 1) / kWaves;
+  const int64_t row = min<int64_t>(r, a.x.n - 1);
+  const char* xp = static_cast<const char*>(a.x.X) + (FORM == GPTQ_MX_CODES ? row * nb * 16 : row * a.x.ldx * 2);
+  const uint8_t* xs = FORM == GPTQ_MX_CODES ? a.x.scales + row * nb : nullptr;
+  constexpr int kX = FORM == GPTQ_MX_BF16 ? 4 : 1;       // operands of a slab
+  // the activations of one slab (zeros past the share's end), as operands
+  auto load_x = [&](int s, u32x4 (&x)[kX], uint32_t& sx) {
+    const int b = 4 * s + q;
+    sx = 127u;
+    if (FORM == GPTQ_MX_CODES) {
+      x[0] = u32x4{0u, 0u, 0u, 0u};
+      if (s < s1 && b < nb) {
+        x[0] = *reinterpret_cast<const u32x4*>(xp + 16 * b);
+        sx = xs[b];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kX; ++i) x[i] = u32x4{0u, 0u, 0u, 0u};
+      if (s >= s1) return;
+      u32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = load8(reinterpret_cast<const uint16_t*>(xp), 32 * int64_t(b) + 8 * i, a.x.d, a.vec);
+      if (FORM == GPTQ_MX_ROUND) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = mx_amax2(m, v[i][e]);
+        sx = mx_scale_byte(max(m & 0xFFFFu, m >> 16) << 16);
+        const float scale = mx_scale_f32(sx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[0][i] = mx_round8(v[i], scale);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kX; ++i) x[i] = v[i];
+      }
+    }
+  };
+  // the weights of kSlabs slabs of a tile (past the share's end or the row's: zeros times 1)
+  auto load_w = [&](int tile, int s, u32x4 (&w)[kSlabs][JT], uint32_t (&sc)[kSlabs][JT]) {
+    const int64_t j = min(int64_t(tile) * 16 + r, a.w.rows - 1) * nb;
+#pragma unroll
+    for (int u = 0; u < kSlabs; ++u) {
+      const int b = 4 * (s + u) + q;
+      const bool in = s + u < s1 && b < nb;
+#pragma unroll
+      for (int l = 0; l < JT; ++l) {
+        const Mx& m = l ? a.up : a.w;
+        w[u][l] = u32x4{0u, 0u, 0u, 0u};
+        sc[u][l] = 127u;
+        if (in) {
+          w[u][l] = *reinterpret_cast<const u32x4*>(m.codes + (j + b) * 16);
+          sc[u][l] = m.scales[j + b];
+        }
+      }
+    }
+  };
+  u32x4 w[kSlabs][JT], nw[kSlabs][JT];
+  uint32_t sc[kSlabs][JT], nsc[kSlabs][JT];
+  int tile = blockIdx.x;
+  load_w(tile, s0, w, sc);
+  u32x4 x[KEEP ? kSlabs : 1][kX];
+  uint32_t sx[KEEP ? kSlabs : 1];
+  if (KEEP) {
+#pragma unroll
+    for (int u = 0; u < (KEEP ? kSlabs : 1); ++u) load_x(s0 + u, x[u], sx[u]);
+  }
+  for (int turn = 0; tile < tiles; ++turn) {
+    f32x4 acc[JT];
+#pragma unroll
+    for (int l = 0; l < JT; ++l) acc[l] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int next = tile + static_cast<int>(gridDim.x);
+    for (int s = s0; s < s1; s += kSlabs) {
+      const bool over = s + kSlabs >= s1;
+      if (!over || next < tiles) load_w(over ? next : tile, over ? s0 : s + kSlabs, nw, nsc);
+#pragma unroll
+      for (int u = 0; u < kSlabs; ++u) {
+        if (s + u >= s1) break;
+        if (!KEEP) load_x(s + u, x[0], sx[0]);
+        const int k = KEEP ? u : 0;
+#pragma unroll
+        for (int l = 0; l < JT; ++l) {
+          if (FORM == GPTQ_MX_BF16) {
+            const float scale = mx_scale_f32(sc[u][l]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[l] = mfma16(mx_expand8(w[u][l][i], scale), x[k][i % kX], acc[l]);
+          } else {
+            acc[l] = mx_mfma<0>(w[u][l], sc[u][l], x[k][0], sx[k], acc[l]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kSlabs; ++u)
+#pragma unroll
+        for (int l = 0; l < JT; ++l) {
+          w[u][l] = nw[u][l];
+          sc[u][l] = nsc[u][l];
+        }
+    }
+#pragma unroll
+    for (int l = 0; l < JT; ++l) sums[turn & 1][wv][l][lane] = acc[l];
+    __syncthreads();
+    // one wave, another one each turn; lane 16 q + r holds columns 4 q .. + 3 of row r
+    if (wv == turn % kWaves) {
+      f32x4 v[JT];
+#pragma unroll
+      for (int l = 0; l < JT; ++l) {
+        v[l] = sums[turn & 1][0][l][lane];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) v[l] += sums[turn & 1][k][l][lane];
+      }
+      const int64_t j = int64_t(tile) * 16 + 4 * q;
+      if (r < a.x.n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (j + e >= a.w.rows) break;
+          const int64_t at = r * a.y.ldy + j + e;
+          if (GATED) {
+            static_cast<uint16_t*>(a.y.Y)[at] = f32_bf16(mx_act(v[0][e], a.y.act) * v[JT - 1][e]);
+            if (a.y.G) {
+              a.y.G[r * a.y.ldg + j + e] = f32_bf16(v[0][e]);
+              a.y.U[r * a.y.ldg + j + e] = f32_bf16(v[JT - 1][e]);
+            }
+          } else if (a.y.out_bf16) {
+            static_cast<uint16_t*>(a.y.Y)[at] = f32_bf16(v[0][e]);
+          } else {
+            static_cast<float*>(a.y.Y)[at] = v[0][e];
+          }
+        }
+      }
+    }
+    tile = next;
+  }
+}
+
+template <int FORM, bool GATED>
+gptq_status launch_stream(const DecodeArgs& a, hipStream_t st) {
+  const int tiles = static_cast<int>(ceil_div(a.w.rows, 16));
+  const unsigned grid = static_cast<unsigned>(std::min(tiles, 256));
+  // every wave's share: at most kSlabs slabs
+  if ((a.w.nb + 3) / 4 <= kSlabs * kWaves)
+    mx_stream_kernel<FORM, GATED, true><<<grid, kWaves * 64, 0, st>>>(a, tiles);
+  else
+    mx_stream_kernel<FORM, GATED, false><<<grid, kWaves * 64, 0, st>>>(a, tiles);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
 template <int FORM, int NT>
 gptq_status launch_rows(const DecodeArgs& a, hipStream_t st) {
   const int64_t m = a.w.rows;
@@ -188,7 +351,8 @@ gptq_status launch_rows(const DecodeArgs& a, hipStream_t st) {
 
 template <int FORM>
 gptq_status launch_form(const DecodeArgs& a, hipStream_t st) {
-  if (a.x.n <= 16) return launch_rows<FORM, 1>(a, st);
+  if (a.x.n <= 16)
+    return a.up.codes ? launch_stream<FORM, true>(a, st) : launch_stream<FORM, false>(a, st);
   if (a.x.n <= 32) return launch_rows<FORM, 2>(a, st);
   return launch_rows<FORM, 4>(a, st);
 }

@@ -403,3 +403,83 @@ def test_offsets_beyond_32_bits(dev):
         v = f64(X[r:r + 1])
         want = v @ w.T
         check(Y[r:r + 1], want, sum_bound(d, np.abs(v) @ np.abs(w).T) * (1 + UB) + UB * np.abs(want), str(r))
+
+
+# ---------------------------------------------------------------------------
+# every tile and way of dividing the sum, chunks of rows
+# ---------------------------------------------------------------------------
+
+def exact(v, w):
+    """v w^T and |v| |w|^T in 64 bits, on the device."""
+    v, w = torch.from_numpy(v).cuda(), torch.from_numpy(w).cuda()
+    return (v @ w.T).cpu().numpy(), (v.abs() @ w.abs().T).cpu().numpy()
+
+
+@pytest.mark.parametrize("form", ["bf16", "round", "codes"])
+@pytest.mark.parametrize("n,d,m", [(70, 4096, 1100), (203, 11008, 512), (1000, 4096, 2048), (300, 4096, 4100),
+                                   (2100, 512, 4096), (4200, 256, 4100), (2048, 300, 8192), (640, 2080, 2048),
+                                   (16500, 96, 80), (33000, 40, 33)])
+def test_sizes_of_layers(dev, form, n, d, m):
+    rng = np.random.default_rng([n, d, m, 7])
+    (Wg, wg), (Wu, wu) = layer(rng, m, d, dev), layer(rng, m, d, dev)
+    x, kw, v = as_input(rows(rng, n, d, 2.0 / np.sqrt(d)).to(dev), form)
+    g, mg = exact(v, wg)
+    u, mu = exact(v, wu)
+    bg, bu = sum_bound(d, mg), sum_bound(d, mu)
+    check(gq.gptq_mx_matmul(x, *Wg, **kw), g, bg, "product")
+    Y, G, Up = gq.gptq_mx_gated(x, *Wg, *Wu, want_parts=True, **kw)
+    check(G, g, bg + UB * (np.abs(g) + bg), "G")
+    check(Up, u, bu + UB * (np.abs(u) + bu), "U")
+    y = orc.mx_gate(g, "silu") * u
+    e = 1.1 * bg * (np.abs(u) + bu) + np.abs(orc.mx_gate(g, "silu")) * bu + 10 * U * np.abs(y)
+    check(Y, y, e + UB * (np.abs(y) + e) + 1e-38, "Y")
+
+
+@pytest.mark.parametrize("n,d,m", [(70, 1100, 4096), (203, 512, 11008), (1000, 2048, 4096), (300, 4100, 4096),
+                                   (2100, 4096, 512), (4200, 4100, 256), (2048, 8192, 300), (16500, 80, 96)])
+def test_gradients_of_sizes_of_layers(dev, n, d, m):
+    rng = np.random.default_rng([n, d, m, 8])
+    (Wg, wg), (Wu, wu) = layer(rng, m, d, dev), layer(rng, m, d, dev)
+    dY, G, Up = (rows(rng, n, m).to(dev) for _ in range(3))
+    want, mag = exact(f64(dY), np.ascontiguousarray(wg.T))
+    check(gq.gptq_mx_matmul_t(dY, *Wg, d), want, sum_bound(m, mag) * (1 + UB) + UB * np.abs(want), "dX")
+    dX, dG, dU = gq.gptq_mx_gated_backward(dY, G, Up, *Wg, *Wu, d)
+    a, ma = exact(f64(dG), np.ascontiguousarray(wg.T))
+    b, mb = exact(f64(dU), np.ascontiguousarray(wu.T))
+    check(dX, a + b, sum_bound(2 * m, ma + mb) * (1 + UB) + UB * np.abs(a + b), "gated dX")
+
+
+@pytest.mark.parametrize("n", [1, 16, 40, 300])
+def test_calls_on_two_streams_at_once(dev, n):
+    """Calls share nothing but their inputs: with a workspace each, two streams at
+    a time give what one gives."""
+    rng = np.random.default_rng([n, 12])
+    Wg, _ = layer(rng, 2048, 1024, dev)
+    Wu, _ = layer(rng, 2048, 1024, dev)
+    Xs = [rows(rng, n, 1024).to(dev) for _ in range(2)]
+    want = [(gq.gptq_mx_gated(X, *Wg, *Wu), gq.gptq_mx_matmul(X, *Wg, quantize_x=True)) for X in Xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = []
+        for s, X in zip(streams, Xs):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append((gq.gptq_mx_gated(X, *Wg, *Wu), gq.gptq_mx_matmul(X, *Wg, quantize_x=True)))
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_rows_behind_the_last_are_left_alone(dev):
+    """Outputs with rows behind the last activation row, for every kernel's row tiles."""
+    rng = np.random.default_rng(13)
+    m, d = 320, 512
+    W, _ = layer(rng, m, d, dev)
+    for n in (1, 15, 17, 63, 65, 130, 257, 700):
+        X = rows(rng, n, d).to(dev)
+        for kw in ({}, dict(quantize_x=True)):
+            want = gq.gptq_mx_matmul(X, *W, **kw)
+            out = torch.full((n + 64, m), 5.0, device=dev)
+            gq.gptq_mx_matmul(X, *W, Y=out[:n], **kw)
+            assert torch.equal(out[:n], want) and bool((out[n:] == 5).all())
