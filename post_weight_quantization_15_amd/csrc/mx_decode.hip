@@ -10,6 +10,12 @@
 // + v of product i, in both operands).  Activations to be rounded are rounded
 // on the way: a lane holds a whole block, so its scale needs no exchange.  The
 // waves' sums meet in LDS in the order of k.
+//
+// Up to 16 rows mx_stream_kernel: a workgroup stays on its CU and goes through tiles, which keeps
+// its weights' loads in flight across them and the activations in registers.  Measured, kernel
+// alone, 4096 columns: into 11008 one row 12.4 us (1.9 TB/s), 16 rows 15.5; gated 18.9 and 21.4
+// (2.3 TB/s; a workgroup a tile took 25); into 4096 5.9 and 8.3.  The bytes at a large copy's rate
+// would take half of that; the first loads' and the last sums' latencies are the rest.
 #include <algorithm>
 
 #include "mx.h"
@@ -27,23 +33,22 @@ struct DecodeArgs {
 constexpr int kWaves = 8;
 constexpr int kSlabs = 4;                    // slabs whose loads are under way at once
 
-// FORM: gptq_mx_input; NT: activation rows / 16; JT: 16-row tiles of a wave
-// (GATED: one of each layer).
-template <int FORM, int NT, int JT, bool GATED>
+// Up to 16 NT rows, a workgroup for each 16 output columns.  FORM: gptq_mx_input.
+template <int FORM, int NT, bool GATED>
 __global__ __launch_bounds__(kWaves * 64) void mx_decode_kernel(DecodeArgs a) {
+  constexpr int JT = GATED ? 2 : 1;                      // layers
   __shared__ f32x4 sums[kWaves][JT * NT][64];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15;
-  constexpr int kRows = GATED ? 16 : 16 * JT;            // output columns of the workgroup
-  const int64_t j0 = int64_t(blockIdx.x) * kRows;
+  const int64_t j0 = int64_t(blockIdx.x) * 16;
   const int nb = static_cast<int>(a.w.nb), slabs = (nb + 3) / 4;
   const int s0 = slabs * wv / kWaves, s1 = slabs * (wv + 1) / kWaves;
   const uint8_t* wc[JT];
   const uint8_t* wsc[JT];
 #pragma unroll
   for (int j = 0; j < JT; ++j) {
-    const Mx& w = GATED && j ? a.up : a.w;
-    const int64_t row = min(j0 + (GATED ? 0 : 16 * j) + r, w.rows - 1);
+    const Mx& w = j ? a.up : a.w;
+    const int64_t row = min(j0 + r, w.rows - 1);
     wc[j] = w.codes + row * nb * 16;
     wsc[j] = w.scales + row * nb;
   }
@@ -147,13 +152,13 @@ __global__ __launch_bounds__(kWaves * 64) void mx_decode_kernel(DecodeArgs a) {
     for (int t = 0; t < NT; ++t) sums[wv][j * NT + t][lane] = acc[j][t];
   __syncthreads();
   // lane 16 q + r holds columns 4 q .. + 3 of activation row r
-  for (int p = wv; p < (GATED ? NT : JT * NT); p += kWaves) {
+  for (int p = wv; p < NT; p += kWaves) {
     f32x4 v = sums[0][p][lane];
 #pragma unroll
     for (int k = 1; k < kWaves; ++k) v += sums[k][p][lane];
-    const int64_t t = 16 * (p % NT) + r, j = j0 + 16 * (p / NT) + 4 * q;
+    const int64_t t = 16 * p + r, j = j0 + 4 * q;
     if (t >= a.x.n) continue;
-    if (GATED) {
+    if constexpr (GATED) {
       f32x4 u = sums[0][NT + p][lane];
 #pragma unroll
       for (int k = 1; k < kWaves; ++k) u += sums[k][NT + p][lane];
@@ -180,7 +185,7 @@ __global__ __launch_bounds__(kWaves * 64) void mx_decode_kernel(DecodeArgs a) {
 // Up to 16 activation rows, where the weights' stream is the whole of it: one workgroup a CU
 // goes through row tiles, the next loads under way beside the products, the sums in two sets
 // of LDS in turn.  KEEP: a wave's share of the activations (at most kSlabs slabs) stays in
-// registers.
+// registers (4096 columns; longer rows read them again for every tile).
 template <int FORM, bool GATED, bool KEEP>
 __global__ __launch_bounds__(kWaves * 64, 2) void mx_stream_kernel(DecodeArgs a, int tiles) {
   constexpr int JT = GATED ? 2 : 1;
@@ -342,9 +347,9 @@ template <int FORM, int NT>
 gptq_status launch_rows(const DecodeArgs& a, hipStream_t st) {
   const int64_t m = a.w.rows;
   if (a.up.codes)
-    mx_decode_kernel<FORM, NT, 2, true><<<ceil_div(m, 16), kWaves * 64, 0, st>>>(a);
+    mx_decode_kernel<FORM, NT, true><<<ceil_div(m, 16), kWaves * 64, 0, st>>>(a);
   else
-    mx_decode_kernel<FORM, NT, 1, false><<<ceil_div(m, 16), kWaves * 64, 0, st>>>(a);
+    mx_decode_kernel<FORM, NT, false><<<ceil_div(m, 16), kWaves * 64, 0, st>>>(a);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
@@ -360,13 +365,13 @@ gptq_status launch_form(const DecodeArgs& a, hipStream_t st) {
 }  // namespace
 
 // Every 16 output columns read all activations again, which takes over from 16
-// rows on (7.5 TB/s from the L2s, as measured: 64 rows of 4096 into 11008 take 54 us here, 28 in
-// tiles; of 4096 into 1024 columns 7 and 9).
+// rows on (7.5 TB/s from the L2s, as measured: 64 rows of 4096 into 11008 take 54 us here, 24 in
+// tiles; of 1024 into 1024 columns 7 and 9).  The same for both 4-bit forms, whose results are the
+// same bits.
 bool mx_decode_takes(int64_t n, int64_t m, int64_t d, int form, bool gated) {
   if (n <= 16) return true;
   if (n > 64) return false;
-  const double row = form == GPTQ_MX_CODES ? d * 0.5 : d * 2.0;
-  const double bytes = double(ceil_div(m, 16)) * double(round_up(n, 16)) * row +
+  const double bytes = double(ceil_div(m, 16)) * double(round_up(n, 16)) * double(d) * 2.0 +
                        double(m) * double(d) * (gated ? 1.06 : 0.53);
   return 3.0 + bytes / 7.5e6 < 2.5 + mx_gemm_time(n, m, d, form, gated);
 }

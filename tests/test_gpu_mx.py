@@ -165,13 +165,14 @@ def test_product(dev, form, n, d, m):
         check(Y, want, sum_bound(d, mag) * (1 + UB) + (UB * np.abs(want) if dtype == BF else 0), form)
 
 
-@pytest.mark.parametrize("n", [1, 20, 100, 700])
-def test_forms_agree_and_runs_repeat(dev, n):
+@pytest.mark.parametrize("n", [1, 20, 33, 64, 100, 700])
+@pytest.mark.parametrize("d,m", [(1056, 520), (512, 4096), (4096, 768)])
+def test_forms_agree_and_runs_repeat(dev, n, d, m):
     """Rounding within the call is the call on the codes, bit for bit, and
     results are the same bits from run to run."""
     rng = np.random.default_rng(n)
-    W, _ = layer(rng, 520, 1056, dev)
-    X = rows(rng, n, 1056).to(dev)
+    W, _ = layer(rng, m, d, dev)
+    X = rows(rng, n, d).to(dev)
     q = gq.gptq_mx_quantize(X)
     a = gq.gptq_mx_matmul(X, *W, quantize_x=True)
     assert torch.equal(a, gq.gptq_mx_matmul(q["codes"], *W, x_scales=q["scales"]))
