@@ -446,7 +446,8 @@ gptq_status gptq_distill_backward(const void* logits, gptq_dtype dtype, int64_t 
  * numbers the rest of top_idx is -1, of top_logits -inf.
  * Cells are exponentiated in fp32, summed in fp32 for 32 cells and in fp64
  * beyond.  Results are the same bits from run to run.  Rows whose logits rise
- * along the vocabulary take up to some ten times as long for their largest.
+ * all along the vocabulary take up to some fifteen times as long for their
+ * largest.
  * ws: at least gptq_token_logprobs_workspace_bytes(n, vocab, k) bytes, 16-byte
  *   aligned (else WORKSPACE).
  * Errors: INVALID_ARG (bad sizes, dtype, k, temperature outside 1e-30 .. 1e30,

@@ -193,6 +193,25 @@ def test_masks_and_what_is_not_finite(dev, dtype, n, vocab):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("k", [3, 40, 300])
+def test_numbers_beside_signalling_nan_are_found(dev, dtype, k):
+    """Every kind of NaN is left out, none of its neighbours."""
+    ids = torch.from_numpy(np.random.default_rng(k).permutation(20000)).to(torch.float32) / 16
+    z = torch.stack([ids.to(TYPES[dtype])] * 4)
+    as_int = torch.int32 if dtype == "f32" else torch.int16
+    nan = {"f32": (0x7F800001, 0x7FC00000), "bf16": (0x7F81, 0x7FC0), "f16": (0x7C01, 0x7E00)}[dtype]
+    for r, bits in enumerate(nan):
+        z.view(as_int)[1 + r, 1::2] = bits
+    z[3] = z[1]
+    z[3, 2000:] = -float("inf")
+    got = gq.gptq_token_logprobs(z.to(dev), None, k=k)
+    _, _, _, top, idx = orc.token_stats(f64(z), [-1] * 4, k, 1.0)
+    assert (got["top_idx"].cpu().numpy() == idx).all()
+    assert (f64(got["top_logits"]) == top).all()
+    assert torch.isnan(got["lse"][1:]).all() and torch.isfinite(got["lse"][0])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("T", [1e-30, 1e-3, 1e3, 1e30])
 def test_far_temperatures_and_logits(dev, dtype, T):
     rng = np.random.default_rng(5)
