@@ -91,21 +91,32 @@ __global__ __launch_bounds__(256) void mx_lay_kernel(LayArgs a) {
 // rows; k goes by in blocks of 128 bytes of an activation row (256 4-bit or 64 bf16
 // values) through a ring of S stages in LDS, copied by global_load_lds (no
 // registers), one barrier per block.  KS shares of k, each with its own waves and
-// ring, where tiles are few and small.
-// A wave reads the operands of its next half block into the registers that the
-// products of this one have freed.  With three stages, at the barrier of block kb block
-// kb + 1 has landed too, and no product waits behind a barrier for LDS; three stages of
-// 4-bit operands do not fit beside tiles of 256 x 256 (stages of half the length do: with
-// twice the barriers they take 231 us where these take 209, 8192 rows of 4096 into 11008).
+// ring, where tiles are few and small; `splits` more by workgroups of their own, whose sums a
+// second launch adds in their order.
+//   kFour    both operands in 4 bits: a lane reads 16 bytes of each and a scale byte a
+//            block, and the scaled matrix instruction takes them as they are
+//   kBf16    bf16 activations; weights pass through LDS in 4 bits (a quarter of the
+//            copies and reads) and become bf16, exactly, in registers
+//   kDense   both operands bf16, for the gradient through a turned layer
 // In LDS a row has its 16-byte units at c ^ unit_swap(r): copies and fragment reads (16
-// rows, one unit each) pass without bank conflicts.  Lane 16 q + r reads unit q +
-// 4 s of its row in half s of a block: 32 4-bit values, or 8 bf16 ones.  With bf16 a
-// block of a weight row is 32 bytes, of which the lane takes word q + 4 s; rows with bit 3
-// set have their halves swapped, which spreads a read over the banks.  Weights are
-// the matrix instruction's first operand: a lane then holds four consecutive columns
-// of one activation row.
+// rows, one unit each) pass without bank conflicts.  In half s of a block lane 16 q + r reads
+// unit 2 q + s of its row with kFour (so that its two scale bytes are neighbours), unit q + 4 s
+// otherwise.  With kBf16 a block of a weight row is 32 bytes, of which the lane takes word q + 4 s;
+// rows with bit 3 set have their halves swapped, which spreads a read over the banks.  Weights
+// are the matrix instruction's first operand: a lane then holds four consecutive columns of one
+// activation row.
 // GATED: 16 rows of the gate's layer and 16 of the other in turn, so that a lane
 // holds both factors of a result.
+//
+// What bounds it.  kBf16: the matrix unit (8192 rows of 4096 into 11008: 610 us, 1210 TFLOP/s,
+// 85 % of what a large library product in bf16 reaches on the card).  With three stages block kb
+// + 1 has landed at the barrier of block kb, and a wave reads the operands of its next half block
+// into the registers that the products of this one have freed, so no product waits behind a
+// barrier for LDS; the conversions run beside the matrix unit.  kFour: LDS and the barrier: a
+// block's products take a third of the bf16 ones' time and its reads as long as theirs (218 us on
+// codes, 3390 TFLOP/s, where the instruction alone runs at 7700).  Two stages, as three do not fit beside
+// tiles of 256 x 256; stages of half the length, of which three fit, were no faster with twice
+// the barriers, and waves in two groups that take turns at LDS and the matrix unit were slower.
 // ---------------------------------------------------------------------------
 struct GemmMx {
   const char* X;             // rows of ldx bytes: bf16, or padded codes
@@ -166,7 +177,7 @@ __global__ __launch_bounds__(WM* WN* KS * 64, TM * TN >= 128 * 128 ? 2 : 4) void
   // copies one at a time behind the products of the first half block (two waves a SIMD: 423 us
   // where all at once take 443, 8192 x 4096 -> 8192; smaller tiles need them earlier)
   constexpr bool kSpread = FORM == kBf16 && TM * TN == 256 * 256;
-  constexpr bool kEarly = FORM == kBf16;                 // the next block has landed, too
+  constexpr bool kEarly = FORM == kBf16;                 // the next block has landed at a barrier, too
   static_assert(S >= (kEarly ? 3 : 2), "stages");
   constexpr int kCopies = kLoadsX + kLoadsW + (kSRows ? 1 : 0);
   constexpr int kOffW = TM * kRow, kOffS = kOffW + TN * kWRow;
@@ -581,9 +592,14 @@ gptq_status launch_tile(GemmMx a, int splits, hipStream_t st) {
   return GPTQ_OK;
 }
 
-// Tile and parts of the sum by the time they take (us, as measured): a CU's
-// workgroups, at most four at a time, turn once per block of k and share, in turn[c - 1] where c
-// of them are there; parts of the sum cost their bytes and a second launch.
+// Tile and parts of the sum by the time they take (us): a CU's workgroups, at most `resident` at a
+// time, turn once per block of k and share, in turn[c - 1] where c of them are there (measured for
+// each form and tile, with products whose tiles fill the card evenly); parts of the sum cost
+// their bytes, written and read at 4 TB/s, and a second launch.  Bf16 rows of 4096 into 4096, us:
+//   100 rows   21 in 64 x 64 with 4 shares and 2 parts (24 without parts), 24 in 128 x 128 with 4
+//              parts, 32 in 256 x 256 with 8
+//   1024 rows  49 in 128 x 128 with 2 shares, 53 with one, 57 in 256 x 256 with 4 parts, 69 in 64 x 64
+//   8192 rows  227 in 256 x 256, 289 in 128 x 128, 467 in 64 x 64
 struct Shape {
   int tm, tn, ks, resident;
   double turn[4];
