@@ -161,8 +161,8 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantizeArgs a) {
 // rows past the matrix.  A thread takes the same block of two neighbouring
 // rows and writes pairs to the turned tile in LDS, 32 lanes to 32 consecutive words of a
 // column; a wave's second block takes the other column of two first, whose words lie in other
-// banks.  Bound by the writing: 4096 x 11008 values in 26 us (4.3 TB/s with the codes), a gated pair of them in 51;
-// a product of 4096 rows behind it takes ten times that.
+// banks.  Bound by the writing: 4096 x 11008 values in 28 us (4 TB/s with the codes), a gated
+// pair of them in 49; a product of 4096 rows behind it takes ten times that.
 __global__ __launch_bounds__(256) void mx_turn_kernel(Mx w, Mx up, unsigned by_one, int64_t d,
                                                       uint16_t* __restrict__ Wt, int64_t ldt) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[256][36];

@@ -123,13 +123,13 @@ __global__ __launch_bounds__(256) void mx_lay_kernel(LayArgs a) {
 // GATED: 16 rows of the gate's layer and 16 of the other in turn, so that a lane
 // holds both factors of a result.
 //
-// What bounds it.  kBf16: the matrix unit (8192 rows of 4096 into 11008: 610 us, 1210 TFLOP/s,
-// 85 % of what a large library product in bf16 reaches on the card).  With three stages block kb
+// What bounds it.  kBf16: the matrix unit (8192 rows of 4096 into 11008: 600 us, 1230 TFLOP/s,
+// four fifths of what a large library product in bf16 reaches on the card).  With three stages block kb
 // + 1 has landed at the barrier of block kb, and a wave reads the operands of its next half block
 // into the registers that the products of this one have freed, so no product waits behind a
 // barrier for LDS; the conversions run beside the matrix unit.  kFour: LDS and the barrier: a
-// block's products take a third of the bf16 ones' time and its reads as long as theirs (218 us on
-// codes, 3390 TFLOP/s, where the instruction alone runs at 7700).  Two stages, as three do not fit beside
+// block's products take a third of the bf16 ones' time and its reads as long as theirs (212 us on
+// codes, 3480 TFLOP/s, where the instruction alone runs at 7700).  Two stages, as three do not fit beside
 // tiles of 256 x 256; stages of half the length, of which three fit, were no faster with twice
 // the barriers, and waves in two groups that take turns at LDS and the matrix unit were slower.
 // ---------------------------------------------------------------------------
