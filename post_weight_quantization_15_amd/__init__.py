@@ -539,6 +539,14 @@ def _enough(ws, need, dev):
     return ws
 
 
+def _scratch(ws, need, dev):
+    """A workspace (none where none is needed), its address and its size."""
+    if ws is None and not need:
+        return None, None, 0
+    ws = _enough(ws, need, dev)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _launch(dev, where, fn, *args):
     """Calls a library function with the stream of `dev` last, `dev` being the
     current device for the launch."""
@@ -755,7 +763,7 @@ def gptq_token_logprobs(logits: torch.Tensor, tokens=None, k: int = 0, temperatu
     if tokens is not None:
         _like(tokens, "tokens", torch.int32, (n,), dev)
     lib = _lib()
-    ws = _enough(ws, lib.gptq_token_logprobs_workspace_bytes(n, vocab, k), dev)
+    ws, at_ws, ws_bytes = _scratch(ws, lib.gptq_token_logprobs_workspace_bytes(n, vocab, k), dev)
     out = torch.empty(6 * n, dtype=_F32, device=dev)
     logp, entropy, lse, stats = out[:n], out[n:2 * n], out[2 * n:3 * n], out[3 * n:].view(n, 3)
     top = torch.empty(n, k, dtype=_F32, device=dev) if k > 0 else None
@@ -765,7 +773,7 @@ def gptq_token_logprobs(logits: torch.Tensor, tokens=None, k: int = 0, temperatu
             _LOGITS[logits.dtype], n, vocab, ldl, None if tokens is None else tokens.data_ptr(),
             temperature, k, None if tokens is None else at, at + 4 * n, at + 8 * n, at + 12 * n,
             None if top is None else top.data_ptr(), None if idx is None else idx.data_ptr(),
-            ws.data_ptr(), ws.numel() * ws.element_size())
+            at_ws, ws_bytes)
     return dict(logp=None if tokens is None else logp, entropy=entropy, lse=lse, stats=stats,
                 top_logits=top, top_idx=idx)
 
@@ -892,12 +900,11 @@ def gptq_mx_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     if out_dtype is not _F32 and out_dtype is not _BF16:
         raise TypeError(f"Y must be float32 or bfloat16, got {out_dtype}")
     lib = _lib()
-    ws = _enough(ws, lib.gptq_mx_matmul_workspace_bytes(n, m, d, form), dev)
+    ws, at_ws, ws_bytes = _scratch(ws, lib.gptq_mx_matmul_workspace_bytes(n, m, d, form), dev)
     Y = _out(Y, "Y", out_dtype, (n, m), dev)
     _launch(dev, "gptq_mx_matmul", lib.gptq_mx_matmul, X.data_ptr(), form, xs, n, d, ldx,
             codes.data_ptr(), scales.data_ptr(), m, Y.data_ptr(),
-            GPTQ_F32 if out_dtype is _F32 else GPTQ_BF16, m, ws.data_ptr(),
-            ws.numel() * ws.element_size())
+            GPTQ_F32 if out_dtype is _F32 else GPTQ_BF16, m, at_ws, ws_bytes)
     return Y
 
 
@@ -943,7 +950,7 @@ def gptq_mx_gated(X: torch.Tensor, gate_codes: torch.Tensor, gate_scales: torch.
     if _check_mx(up_codes, up_scales, "up", blocks, dev) != m:
         raise ValueError("gate and up must have the same shape")
     lib = _lib()
-    ws = _enough(ws, lib.gptq_mx_gated_workspace_bytes(n, m, d, form), dev)
+    ws, at_ws, ws_bytes = _scratch(ws, lib.gptq_mx_gated_workspace_bytes(n, m, d, form), dev)
     Y = _out(Y, "Y", _BF16, (n, m), dev)
     G = U = None
     if want_parts:
@@ -952,7 +959,7 @@ def gptq_mx_gated(X: torch.Tensor, gate_codes: torch.Tensor, gate_scales: torch.
     _launch(dev, "gptq_mx_gated", lib.gptq_mx_gated, X.data_ptr(), form, xs, n, d, ldx,
             gate_codes.data_ptr(), gate_scales.data_ptr(), up_codes.data_ptr(), up_scales.data_ptr(),
             m, act, Y.data_ptr(), m, None if G is None else G.data_ptr(),
-            None if U is None else U.data_ptr(), m, ws.data_ptr(), ws.numel() * ws.element_size())
+            None if U is None else U.data_ptr(), m, at_ws, ws_bytes)
     return (Y, G, U) if want_parts else Y
 
 
