@@ -764,18 +764,18 @@ def gptq_token_logprobs(logits: torch.Tensor, tokens=None, k: int = 0, temperatu
         _like(tokens, "tokens", torch.int32, (n,), dev)
     lib = _lib()
     ws, at_ws, ws_bytes = _scratch(ws, lib.gptq_token_logprobs_workspace_bytes(n, vocab, k), dev)
-    out = torch.empty(6 * n, dtype=_F32, device=dev)
-    logp, entropy, lse, stats = out[:n], out[n:2 * n], out[2 * n:3 * n], out[3 * n:].view(n, 3)
+    # (new tensors cost the host half of what views of one cost)
+    logp = None if tokens is None else torch.empty(n, dtype=_F32, device=dev)
+    entropy, lse = torch.empty(n, dtype=_F32, device=dev), torch.empty(n, dtype=_F32, device=dev)
+    stats = torch.empty(n, 3, dtype=_F32, device=dev)
     top = torch.empty(n, k, dtype=_F32, device=dev) if k > 0 else None
     idx = torch.empty(n, k, dtype=torch.int32, device=dev) if k > 0 else None
-    at = out.data_ptr()
     _launch(dev, "gptq_token_logprobs", lib.gptq_token_logprobs, logits.data_ptr(),
             _LOGITS[logits.dtype], n, vocab, ldl, None if tokens is None else tokens.data_ptr(),
-            temperature, k, None if tokens is None else at, at + 4 * n, at + 8 * n, at + 12 * n,
-            None if top is None else top.data_ptr(), None if idx is None else idx.data_ptr(),
-            at_ws, ws_bytes)
-    return dict(logp=None if tokens is None else logp, entropy=entropy, lse=lse, stats=stats,
-                top_logits=top, top_idx=idx)
+            temperature, k, None if logp is None else logp.data_ptr(), entropy.data_ptr(),
+            lse.data_ptr(), stats.data_ptr(), None if top is None else top.data_ptr(),
+            None if idx is None else idx.data_ptr(), at_ws, ws_bytes)
+    return dict(logp=logp, entropy=entropy, lse=lse, stats=stats, top_logits=top, top_idx=idx)
 
 
 def gptq_token_logprobs_backward(logits: torch.Tensor, stats: torch.Tensor, tokens=None,

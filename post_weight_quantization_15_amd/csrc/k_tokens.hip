@@ -20,8 +20,8 @@
 // per 16 bytes; a row that rises all along selects at each look (1024 rows of 128000 fp32
 // values: 1500 us where the same values in disorder take 114).  Measured, bf16
 // rows: 4096 of 128000 take 232 us without alternatives (4.5 TB/s of one reading), 272 with
-// k = 64, 435 with 256, 619 with 512; one row of 128000, in 62 parts of its own workgroups
-// and joined by a second launch, 19 us with k = 20, of which the launches' kernels are 9
+// k = 64, 435 with 256, 619 with 512; one row of 128000, in 63 parts of its own workgroups
+// and joined by a second launch, 18 us with k = 20, of which the launches' kernels are 9
 // and 8: two readings' latency, a selection and the joining one.
 #include <type_traits>
 
