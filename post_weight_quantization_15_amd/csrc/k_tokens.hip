@@ -16,7 +16,8 @@
 // reach.  What passes is kept in LDS as (value, lower id first) in one 64-bit number, all
 // different; where many are there, the k-th of them, found digit by digit, is
 // the new bar.  A cell later in the row has to exceed it: an equal one has the higher
-// id.  In a row without order some k ln(vocab) cells pass, so the selection is a comparison
+// id (so the cells behind the last whole vector become candidates with the last step, though
+// they are read first).  In a row without order some k ln(vocab) cells pass, so the selection is a comparison
 // per 16 bytes; a row that rises all along selects at each look (1024 rows of 128000 fp32
 // values: 1500 us where the same values in disorder take 114).  Measured, bf16
 // rows: 4096 of 128000 take 232 us without alternatives (4.5 TB/s of one reading), 272 with
@@ -324,9 +325,9 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
   float ez = -INFINITY;
   if (edge >= 0) ez = to_f32<DT>(src[edge]);
   __syncthreads();
-  int have = 0;                              // candidates: the edges, to begin with
+  int have = 0;                              // candidates: the cells before the vectors, to begin with
   if (a.k) {
-    const bool some = edge >= 0 && ez == ez;
+    const bool some = tid < head && ez == ez;
     if (some) buf[atomicAdd(&cnt, 1)] = entry_of(ez, first + edge);
     have = __syncthreads_count(some);
   }
@@ -353,6 +354,14 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
         x = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(word >> (16 * (e & 1)))));
       const int p = atomicAdd(&cnt, 1);
       if (p < a.cap) buf[p] = entry_of(x, first + head + at * E + e);
+    }
+  };
+  // the cells behind the vectors: after all lower ids, so that a bar just above the k-th
+  // candidate drops no cell of that value with a lower id
+  auto push_tail = [&]() {
+    if (edge >= last && ez >= bar) {
+      const int p = atomicAdd(&cnt, 1);
+      if (p < a.cap) buf[p] = entry_of(ez, first + edge);
     }
   };
   int from = 0;                              // first step since the last look
@@ -482,6 +491,7 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
       if (in) push(cur[i], at);
     }
     if (!look) continue;
+    if (step + 1 == steps) push_tail();
     __syncthreads();
     const int found = cnt;
     __syncthreads();
@@ -505,6 +515,7 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
             if (at < nvec) push(*reinterpret_cast<const u32x4*>(body + int64_t(at) * E), at);
           }
         }
+        if (u == 2 * steps - 1) push_tail();
         __syncthreads();
         now = cnt;
         __syncthreads();

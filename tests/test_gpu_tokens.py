@@ -354,3 +354,50 @@ def test_a_teacher_for_the_distillation_loss(dev):
     R = float(Z.max() - Z.min()) / T
     e = (4 * (R + 28) + 190) * U + 2 * U * float(t["lse"].abs().max())
     assert float(loss.abs().max()) <= T * T * 2 * e
+
+
+# ---------------------------------------------------------------------------
+# equal logits over the whole row, ends of rows among them
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n,vocab,k", [(600, 24003, 300), (600, 24003, 256), (600, 24003, 40), (600, 24003, 2),
+                                       (520, 10007, 300), (17, 32771, 300), (1, 262143, 300), (1, 131071, 512)])
+@pytest.mark.parametrize("late", [0.45, 0.86, 0.97])
+def test_equal_logits_at_the_end_of_a_row_come_last(dev, dtype, n, vocab, k, late):
+    """k - 1 logits lie above; the last place goes to the lowest id of those at 1.5,
+    among which are the row's (a part's) last cells.  700 cells at 1 pass the first
+    bar, which sends the candidates through a selection before the row's end.  Rows of
+    an odd length take all alignments."""
+    row = np.zeros(vocab, np.float32)
+    a = int(vocab * 0.35)
+    row[a:a + 700] = 1.0
+    row[a + 700:a + 700 + k - 1] = 2.0
+    row[vocab - 7:] = 1.5
+    row[:9] = 1.5                                     # and its first ones, which come before all
+    at = max(int(vocab * late), a + 700 + k)
+    row[at] = 1.5
+    for first in (True, False):
+        if not first:
+            row[:9] = 0.0
+        Z = torch.from_numpy(row).to(dev).to(TYPES[dtype]).expand(n, vocab).contiguous()
+        got = gq.gptq_token_logprobs(Z, k=k)
+        want = np.append(np.arange(a + 700, a + 700 + k - 1), 0 if first else at)
+        assert (got["top_idx"].cpu().numpy() == want).all()
+        assert (f64(got["top_logits"]) == row[want]).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("k", [5, 100, 256, 257, 512])
+@pytest.mark.parametrize("n,vocab", [(1, 20011), (12, 9001), (520, 9001)])
+def test_few_different_logits(dev, dtype, k, n, vocab):
+    """Rows of a few values in disorder: most places are decided by the id."""
+    rng = np.random.default_rng([n, vocab, k])
+    levels = np.sort(rng.choice(np.arange(-8, 8) / 4, size=5, replace=False))
+    share = np.array([0.9, 0.0985, 0.001, 0.0003, 0.0002])
+    z = rng.choice(levels, p=share, size=(min(n, 8), vocab))
+    rows = torch.arange(n, device=dev) % len(z)       # again at other alignments
+    got = gq.gptq_token_logprobs(torch.from_numpy(z).to(dev).to(TYPES[dtype])[rows], k=k)
+    want = np.argsort(-z, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(got["top_idx"].cpu().numpy(), want[rows.cpu().numpy()])
+    assert np.array_equal(f64(got["top_logits"]), np.take_along_axis(z, want, 1)[rows.cpu().numpy()])
