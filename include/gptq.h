@@ -435,7 +435,7 @@ gptq_status gptq_distill_backward(const void* logits, gptq_dtype dtype, int64_t 
  * tokens: int32 [n]; an id outside [0, vocab) asks for none (logp 0); may be
  *   NULL where logp is.
  * logp, entropy, lse: fp32 [n], each may be NULL.  stats: fp32 [n, 3] or NULL,
- *   for the gradient: a logit r of the row, the log of sum exp((x - r) / T),
+ *   for the gradient: the row's largest logit r, the log of sum exp((x - r) / T),
  *   and the entropy.
  * top_logits fp32 [n, k] (the logits themselves, not over T), top_idx int32
  *   [n, k]: 0 <= k <= 512, k <= vocab; may be NULL where k = 0.
@@ -444,8 +444,10 @@ gptq_status gptq_distill_backward(const void* logits, gptq_dtype dtype, int64_t 
  * (lse: -inf); a row of nothing but the type's lowest value is a row of equal
  * logits.  NaN is never among the largest; where fewer than k logits are
  * numbers the rest of top_idx is -1, of top_logits -inf.
- * Cells are exponentiated in fp32, summed in fp32 for 32 cells and in fp64
- * beyond.  Results are the same bits from run to run.  Rows whose logits rise
+ * Cells are exponentiated in fp32 relative to the largest, summed in fp32 for 32
+ * cells and in fp64 beyond, the largest itself in fp64: logp is never above 0, entropy never
+ * below, and both keep their digits where one token has nearly all the
+ * probability.  Results are the same bits from run to run.  Rows whose logits rise
  * all along the vocabulary take up to some fifteen times as long for their
  * largest.
  * ws: at least gptq_token_logprobs_workspace_bytes(n, vocab, k) bytes, 16-byte

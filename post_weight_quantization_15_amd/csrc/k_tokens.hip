@@ -3,12 +3,15 @@
 // their ids; and the gradient of the first two.
 //
 // With z = x / T, one pass over the row: s = sum 2^(c (x - r)) and t = sum c (x
-// - r) 2^(c (x - r)), c = log2(e) / T, r a reference that a wave takes from its
-// own first cells and moves only for a cell far above it; then
+// - r) 2^(c (x - r)), c = log2(e) / T, r the largest cell that the wave has seen,
+// in the end the row's; then
 //   lse = r / T + ln s,  log p = (x_v - r) / T - ln s,
-//   entropy = ln s - ln2 t / s
-// (all terms of one sign, so nothing cancels).  Cells are exponentiated in fp32
-// and summed in fp32 for 32 cells of a thread, in fp64 beyond.
+//   entropy = ln s - ln2 t / s.
+// No term is positive in t, none negative in s, and the largest cell is 1 in s, so nothing
+// cancels.  Cells are exponentiated in fp32 and summed in fp32 for 32 cells of a thread,
+// in fp64 beyond; a cell that becomes the largest is counted apart, as its 1 would leave
+// a confident row's other cells no bits in an fp32 sum.  In a row without order a wave's largest
+// rises some ln(vocab / 512) times.
 //
 // The largest k: cells pass a bar that only rises.  The first bar comes from the
 // lanes' maxima over the cells at hand (a step's and those whose loads are ahead of it):
@@ -262,11 +265,17 @@ __device__ inline void write_top(const TokenArgs& a, int64_t row, const uint64_t
 }
 
 // Sums relative to a reference moved to one that is higher by `up` (in powers of
-// two); 2^-up from the fp32 exponential of its fraction (2 u).
+// two).  2^-up by the exponential's series for the fraction, |y| <= ln2 / 2, to 2e-10 (a row that
+// rises all along moves its sums at every step); constant factors, not terms, as those
+// would occupy registers throughout.
 __device__ inline void move_sums(double& s, double& t, double up) {
   up = up < 1000.0 ? up : 1000.0;
-  const int n = static_cast<int>(up);
-  const double f = ldexp(static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(n - up))), -n);
+  const int n = static_cast<int>(up + 0.5);
+  const double y = (n - up) * kLn2;
+  double f = 1.0;
+#pragma unroll
+  for (int k = 8; k > 0; --k) f = fma(y * (1.0 / k), f, 1.0);
+  f = ldexp(f, -n);
   t = f * (t - up * s);
   s *= f;
 }
@@ -300,7 +309,6 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
   // the cells before and after the whole vectors, one a thread
   const int edge = tid < head ? tid : tid >= E && tid - E < V - last ? last + tid - E : -1;
   const float c = static_cast<float>(a.inv_temp) * kLog2e;
-  const float margin = 40.0f / c;
   const int steps = max(1, (nvec + kSteps - 1) / kSteps);
   const T* body = src + head;
 
@@ -366,9 +374,15 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
   };
   int from = 0;                              // first step since the last look
   float ps = 0.0f, pt = 0.0f;                // of kLook steps
-  auto add_cell = [&](float x) {
+  int ones = 0;                              // cells equal to a reference that is new
+  auto add_cell = [&](float x, auto fresh) {
     float d = (x - ref) * c;
-    const float e = __builtin_amdgcn_exp2f(d);
+    float e = __builtin_amdgcn_exp2f(d);
+    if constexpr (decltype(fresh)::value) {
+      const bool one = d == 0.0f;            // (+inf: NaN, which goes into the sum)
+      ones += one;
+      e = one ? 0.0f : e;
+    }
     d = max3(d, -1000.0f, -1000.0f);         // 0 times -inf
     ps += e;
     pt = fmaf(e, d, pt);
@@ -397,22 +411,35 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
       top[i] = m;
       gm = max3(gm, m, step == 0 ? ez : m);
     }
-    if (__any(gm > ref + margin)) {
-      const float up = wave_all(gm, [](float x, float y) { return fmaxf(x, y); });
+    // ---- sums
+    auto add_step = [&](auto fresh) {
+      if (step == 0 && edge >= 0) add_cell(ez, fresh);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (at0 + i * kThreads < nvec) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) add_cell(cell_of<DT>(cur[i], e), fresh);
+        }
+      }
+    };
+    uint64_t above = __ballot(gm > ref);
+    if (above) {
+      // the wave's largest, a lane that has more at a time (in a row that rises the last one has it)
+      float up = ref;
+      do {
+        up = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gm), 63 - __builtin_clzll(above)));
+        above = __ballot(gm > up);
+      } while (above);
       s += ps;
       t += pt;
       ps = pt = 0.0f;
       if (step) move_sums(s, t, double(c) * (double(up) - double(ref)));
       ref = up;
-    }
-    // ---- sums
-    if (step == 0 && edge >= 0) add_cell(ez);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (at0 + i * kThreads < nvec) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) add_cell(cell_of<DT>(cur[i], e));
-      }
+      ones = 0;
+      add_step(std::true_type{});
+      s += ones;
+    } else {
+      add_step(std::false_type{});
     }
     // (without a first bar a step fills the candidates)
     const bool look = step % kLook == kLook - 1 || step + 1 == steps || (step == 0 && a.k > kThreads);

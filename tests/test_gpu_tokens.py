@@ -401,3 +401,115 @@ def test_few_different_logits(dev, dtype, k, n, vocab):
     want = np.argsort(-z, axis=1, kind="stable")[:, :k]
     assert np.array_equal(got["top_idx"].cpu().numpy(), want[rows.cpu().numpy()])
     assert np.array_equal(f64(got["top_logits"]), np.take_along_axis(z, want, 1)[rows.cpu().numpy()])
+
+
+# ---------------------------------------------------------------------------
+# confident rows
+# ---------------------------------------------------------------------------
+# Relative to the row's largest logit all terms have one sign.  With D = (max - x) / T
+# of a cell, its exponential is off by (5 D + 2) u of itself (difference, factor and
+# product: 5 u of the exponent; the exponential: 2 u), 32 of them are summed in fp32
+# (33 u), the rest in fp64.  So with tau = the sum without the largest cell and
+# eta = (5 R + 35) u, R the largest D that counts:
+#   logp     -log1p(tau) and what the token lies below: eta tau / (1 + tau)
+#   entropy  log1p(tau) + sum e D / (1 + tau): the same of the first, 2 eta + 8 u of the second
+# and the results' own rounding and fp64's 2^-50.
+
+def confident(rng, n, vocab, dtype, gap, T, at):
+    """Noise, and one token `gap` T above the rest at cell `at`."""
+    z = 1.5 * rng.normal(size=(n, vocab))
+    z[:, at] = z.max(1) + gap * T
+    return torch.from_numpy(z.astype(np.float32)).to(TYPES[dtype])
+
+
+def confident_values(z, T):
+    """tau, sum e D, D, the largest cell's id of rows [n, vocab]."""
+    best = z.argmax(1)
+    D = (z.max(1, keepdims=True) - z) / T
+    e = np.exp(-D)
+    np.put_along_axis(e, best[:, None], 0.0, 1)
+    return e.sum(1), (e * D).sum(1), D, best
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n,vocab,k", [(1, 20000, 512), (1, 100001, 300), (3, 60000, 100), (520, 7001, 0), (520, 7001, 30)])
+@pytest.mark.parametrize("gap,T", [(0.2, 1.0), (3.0, 1.0), (10.0, 1.0), (20.0, 0.7), (20.0, 2.0), (27.0, 1.0)])
+@pytest.mark.parametrize("place", [0.6, 0.98])
+def test_confident_rows(dev, dtype, n, vocab, k, gap, T, place):
+    """One token far above the rest, behind its wave's first cells."""
+    rng = np.random.default_rng([n, vocab, int(100 * gap)])
+    Z = confident(rng, min(n, 8), vocab, dtype, gap, T, int(place * vocab) + 5)
+    T32 = np.float64(np.float32(T))
+    tau, mean, D, best = confident_values(f64(Z), T32)
+    pick = np.arange(n) % len(Z)                      # the same rows at other alignments
+    zd = Z.to(dev)[torch.from_numpy(pick).to(dev)]
+    got = gq.gptq_token_logprobs(zd, i32(dev, best[pick]), k=k, temperature=T)
+    logp, entropy, lse = (f64(got[key]) for key in ("logp", "entropy", "lse"))
+    assert (logp <= 0).all() and (entropy >= 0).all()
+    eta = (5 * np.minimum(D.max(1), 120) + 35) * U
+    off = eta * tau / (1 + tau) + 2.0 ** -50
+    want = -np.log1p(tau)
+    assert (np.abs(logp - want[pick]) <= (off + U * np.abs(want))[pick]).all()
+    H = np.log1p(tau) + mean / (1 + tau)
+    off_h = off + (2 * eta + 8 * U) * mean / (1 + tau)
+    assert (np.abs(entropy - H[pick]) <= (off_h + U * H)[pick]).all()
+    full = f64(Z).max(1) / T32 + np.log1p(tau)
+    assert (np.abs(lse - full[pick]) <= (off + U * np.abs(full))[pick]).all()
+    if k == 0:                                        # another token
+        other = (best + 7) % vocab
+        lp = f64(gq.gptq_token_logprobs(zd, i32(dev, other[pick]), temperature=T)["logp"])
+        want = want - D[np.arange(len(Z)), other]
+        assert (np.abs(lp - want[pick]) <= (off + U * np.abs(want))[pick]).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n", [1, 5])
+@pytest.mark.parametrize("gap,T", [(3.0, 1.0), (10.0, 1.0), (20.0, 0.7), (27.0, 1.0)])
+def test_gradient_of_confident_rows(dev, dtype, n, gap, T):
+    """From the forward call's own statistics.  q = 2^(d c - rest c') is off by (5 D + 4
+    rest + 2) u of itself and what rest is off by, log q alike; 12 u for the products and
+    sums around them; at the token one subtraction of two numbers up to g."""
+    rng = np.random.default_rng([n, int(100 * gap)])
+    vocab = 20000                                     # with k = 512: three steps of 2048 cells a part
+    Z = confident(rng, n, vocab, dtype, gap, T, 14500)
+    T32 = np.float64(np.float32(T))
+    tau, mean, D, best = confident_values(f64(Z), T32)
+    zd, tok = Z.to(dev), i32(dev, best)
+    stats = gq.gptq_token_logprobs(zd, tok, k=512, temperature=T)["stats"]
+    eta = (5 * np.minimum(D.max(1), 120) + 35) * U
+    off = (eta * tau / (1 + tau) + 2.0 ** -50)[:, None]
+    H = (np.log1p(tau) + mean / (1 + tau))[:, None]
+    off_h = off + ((2 * eta + 8 * U) * mean / (1 + tau))[:, None] + U * H
+    rest = np.log1p(tau)[:, None]
+    lq = -D - rest
+    q = np.exp(lq)
+    one, tenth = np.full((n, 1), 0.75, np.float32), np.full((n, 1), 0.125, np.float32)
+    for g, h in ((one, 0 * tenth), (0 * one, tenth), (one, tenth)):
+        d = f64(gq.gptq_token_logprobs_backward(zd, stats, tok, torch.from_numpy(g[:, 0]).to(dev),
+                                                torch.from_numpy(h[:, 0]).to(dev), temperature=T))
+        want = -q * (g + h * (lq + H))
+        room = q * (g + h * (np.abs(lq) + H)) * ((5 * D + 4 * rest + 14) * U + off)
+        room += q * h * ((5 * D + 4 * rest) * U + off + off_h)
+        want[np.arange(n), best] += g[:, 0]
+        room[np.arange(n), best] += 2 * U * g[:, 0]
+        assert (np.abs(d - want / T32) <= room / T32 + half_step(Z.dtype, want / T32) + 1e-30).all()
+        if not h.any():
+            assert (d[np.arange(n), best] >= 0).all()
+    assert np.array_equal(f64(stats[:, 0]), f64(Z).max(1))
+
+
+@pytest.mark.parametrize("n,vocab,k", [(1, 262144, 512), (1, 262144, 0), (520, 40001, 0)])
+@pytest.mark.parametrize("rise", [1e-6, 1e-4, 1e-2])
+def test_rows_that_rise_slowly(dev, n, vocab, k, rise):
+    """The largest cell is a new one at every step: the sums move each time, and no
+    error gathers."""
+    row = torch.arange(vocab, dtype=torch.float32) * rise
+    Z = row.to(dev).expand(n, vocab).contiguous()
+    got = gq.gptq_token_logprobs(Z, i32(dev, [vocab // 2] * n), k=k)
+    z = f64(row)[None]
+    logp, entropy, lse, _, idx = orc.token_stats(z, [vocab // 2], k, 1.0)
+    eta = (5 * min(float(z.max() - z.min()), 120.0) + 35) * U
+    for key, want, bound in (("logp", logp, eta), ("lse", lse, eta), ("entropy", entropy, 2 * (eta + 8 * U) * entropy + eta)):
+        assert (np.abs(f64(got[key]) - want) <= bound + U * np.abs(want)).all(), key
+    if k:
+        assert (got["top_idx"].cpu().numpy() == idx).all()
