@@ -347,6 +347,28 @@ def test_gated_gradient_is_the_forward_difference(dev):
     assert abs(lhs - rhs) <= 1.01 * off
 
 
+@pytest.mark.parametrize("act", ["silu", "relu", "none"])
+@pytest.mark.parametrize("n,d,m", [(3, 96, 700), (130, 320, 300), (777, 130, 1100)])
+def test_gated_gradient_is_the_formulas(dev, act, n, d, m):
+    """dX against the formula, whose dG and dU are never rounded.  The call rounds both to
+    bf16 on their way into the product, each term by at most c = 2^-8 of itself with a sign
+    of its own: the sum of them leaves 7 sqrt(sum c^2) with a probability of 2 exp(-49 / 2).
+    Over all results that and the results' own rounding are at most 2^-8 / sqrt(3) of them
+    each in the mean square: 2^-8 sqrt(2 / 3) together."""
+    rng = np.random.default_rng([n, d, m, 14])
+    Wg, wg = layer(rng, m, d, dev)
+    Wu, wu = layer(rng, m, d, dev)
+    dY, G, Up = (rows(rng, n, m).to(dev) for _ in range(3))
+    dX, _, _ = gq.gptq_mx_gated_backward(dY, G, Up, *Wg, *Wu, d, activation=act)
+    want, dg, du = orc.mx_gated_backward(f64(dY), f64(G), f64(Up), wg, wu, act)
+    once = UB * np.sqrt(dg ** 2 @ wg ** 2 + du ** 2 @ wu ** 2)
+    size = np.abs(f64(dY) * f64(Up)) * (1.1 + (np.abs(f64(G)) if act == "silu" else 0))
+    mag = np.abs(dg) @ np.abs(wg) + np.abs(du) @ np.abs(wu)
+    rest = sum_bound(2 * m, mag) + 12 * U * (size @ np.abs(wg) + np.abs(du) @ np.abs(wu))
+    check(dX, want, (7 * once + rest) * (1 + UB) + UB * np.abs(want), "dX")
+    assert np.linalg.norm(f64(dX) - want) <= UB * np.sqrt(2.0 / 3.0) * np.linalg.norm(want) * 1.01
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, devices
 # ---------------------------------------------------------------------------
