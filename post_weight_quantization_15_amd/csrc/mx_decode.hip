@@ -367,12 +367,13 @@ gptq_status launch_form(const DecodeArgs& a, hipStream_t st) {
 // Every 16 output columns read all activations again, which takes over from 16
 // rows on (7.5 TB/s from the L2s, as measured: 64 rows of 4096 into 11008 take 54 us here, 24 in
 // tiles; of 1024 into 1024 columns 7 and 9).  The same for both 4-bit forms, whose results are the
-// same bits.
+// same bits: by blocks, as codes tell no more of their width.
 bool mx_decode_takes(int64_t n, int64_t m, int64_t d, int form, bool gated) {
   if (n <= 16) return true;
   if (n > 64) return false;
-  const double bytes = double(ceil_div(m, 16)) * double(round_up(n, 16)) * double(d) * 2.0 +
-                       double(m) * double(d) * (gated ? 1.06 : 0.53);
+  const double cols = double(form == GPTQ_MX_BF16 ? d : mx_blocks(d) * kMxBlock);
+  const double bytes = double(ceil_div(m, 16)) * double(round_up(n, 16)) * cols * 2.0 +
+                       double(m) * cols * (gated ? 1.06 : 0.53);
   return 3.0 + bytes / 7.5e6 < 2.5 + mx_gemm_time(n, m, d, form, gated);
 }
 

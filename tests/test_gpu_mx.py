@@ -181,6 +181,22 @@ def test_forms_agree_and_runs_repeat(dev, n, d, m):
     assert torch.equal(b, gq.gptq_mx_matmul(X, *W))
 
 
+@pytest.mark.parametrize("n,m,d", [(36, 3125, 3828), (56, 4860, 1453), (62, 9723, 559), (64, 1900, 5643),
+                                   (5, 300, 1000), (300, 520, 1061)])
+def test_forms_agree_where_the_last_block_is_short(dev, n, m, d):
+    """Sizes where a block more or less would choose another kernel; scales so far apart that
+    sums are not exact."""
+    rng = np.random.default_rng([n, m, d])
+    (Wg, _), (Wu, _) = layer(rng, m, d, dev, 100, 130), layer(rng, m, d, dev, 100, 130)
+    X = rows(rng, n, d, 0.1).to(dev)
+    q = gq.gptq_mx_quantize(X)
+    codes = dict(x_scales=q["scales"])
+    assert torch.equal(gq.gptq_mx_matmul(X, *Wg, quantize_x=True), gq.gptq_mx_matmul(q["codes"], *Wg, **codes))
+    a = gq.gptq_mx_gated(X, *Wg, *Wu, quantize_x=True, want_parts=True)
+    b = gq.gptq_mx_gated(q["codes"], *Wg, *Wu, want_parts=True, **codes)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 @pytest.mark.parametrize("form", ["bf16", "round"])
 @pytest.mark.parametrize("n", [3, 40, 150])
 def test_product_strides(dev, form, n):

@@ -3,6 +3,7 @@ every bad argument is turned away before the GPU is touched (no compute runs
 here)."""
 
 import math
+import random
 
 import pytest
 import torch
@@ -192,3 +193,16 @@ def test_binding_checks_shapes():
             gq._check_mx(*bad, "layer", 2, dev)
     with pytest.raises(TypeError):
         gq._check_mx(c.int(), s, "layer", 2, dev)
+
+
+def test_both_four_bit_forms_choose_alike(lib):
+    """Activations rounded in the call and given as codes (whose width is known in blocks
+    only) take the same kernel: few rows, without a workspace, or tiles."""
+    shapes = [(36, 3125, 3828), (56, 4860, 1453), (62, 9723, 559), (18, 7719, 1633), (64, 1900, 5643)]
+    rng = random.Random(3)
+    shapes += [(rng.randint(17, 64), int(math.exp(rng.uniform(3, 9.4))), int(math.exp(rng.uniform(3.5, 9.4))))
+               for _ in range(4000)]
+    for n, m, d in shapes:
+        wide = 32 * -(-d // 32)
+        for need in (lib.gptq_mx_matmul_workspace_bytes, lib.gptq_mx_gated_workspace_bytes):
+            assert need(n, m, d, 1) == need(n, m, wide, 2) == need(n, m, d, 2), (n, m, d)
