@@ -831,7 +831,9 @@ def _mx_input(X, x_scales, quantize_x, blocks):
             raise ValueError("X as codes needs x_scales, and is quantized already")
         dev = _gpu_device(X)
         n = _check_mx(X, x_scales, "X", blocks, dev)
-        return _MX_CODES, 0, x_scales.data_ptr(), n, 32 * blocks, dev
+        # the fewest columns with these blocks, which alone count here: the widest layers end
+        # inside their last one
+        return _MX_CODES, 0, x_scales.data_ptr(), n, 32 * blocks - 31, dev
     if x_scales is not None:
         raise ValueError("x_scales belongs to X as codes (uint8)")
     ldx = _gpu_rows(X, "X")

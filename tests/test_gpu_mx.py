@@ -263,6 +263,34 @@ def test_scales_over_the_whole_range(dev, form, n):
     check(Y, v @ w.T, sum_bound(d, np.abs(v) @ np.abs(w).T))
 
 
+@pytest.mark.parametrize("n,d", [(2, 65505), (30, 65535), (70, 65505)])
+def test_widest_layers(dev, n, d):
+    """The most columns that are allowed, whose last block is not a whole one: every form of
+    the activations, the gated block and the gradient."""
+    rng = np.random.default_rng([n, d])
+    m = 17
+    (Wg, wg), (Wu, _) = layer(rng, m, d, dev), layer(rng, m, d, dev)
+    X = rows(rng, n, d, 2.0 / np.sqrt(d)).to(dev)
+    q = gq.gptq_mx_quantize(X, want_hat=True)
+    for x, kw, v in ((X, {}, f64(X)), (X, dict(quantize_x=True), f64(q["hat"])),
+                     (q["codes"], dict(x_scales=q["scales"]), f64(q["hat"]))):
+        want, bound = v @ wg.T, sum_bound(d, np.abs(v) @ np.abs(wg).T)
+        check(gq.gptq_mx_matmul(x, *Wg, **kw), want, bound)
+        A, G, _ = gq.gptq_mx_gated(x, *Wg, *Wu, want_parts=True, **kw)
+        assert A.shape == (n, m)
+        check(G, want, bound * (1 + UB) + UB * np.abs(want))
+    dY = rows(rng, n, m).to(dev)
+    v = f64(dY)
+    check(gq.gptq_mx_matmul_t(dY, *Wg, d), v @ wg, sum_bound(m, np.abs(v) @ np.abs(wg)) * (1 + UB) + UB * np.abs(v @ wg))
+    # a block more is refused in every form
+    codes, scales = (torch.zeros(n, k, dtype=torch.uint8, device=dev) for k in (16 * 2049, 2049))
+    W, x = (codes, scales), torch.zeros(n, 65537, dtype=BF, device=dev)
+    for call in (lambda: gq.gptq_mx_matmul(x, *W), lambda: gq.gptq_mx_matmul(codes, *W, x_scales=scales),
+                 lambda: gq.gptq_mx_gated(codes, *W, *W, x_scales=scales)):
+        with pytest.raises(gq.GPTQError):
+            call()
+
+
 # ---------------------------------------------------------------------------
 # gradient, gated block
 # ---------------------------------------------------------------------------
