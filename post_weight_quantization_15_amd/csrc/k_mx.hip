@@ -105,8 +105,8 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantizeArgs a) {
     }
   }
   const int64_t block = int64_t(row) * a.nb + c / kMxBlock;
-  if (a.codes) reinterpret_cast<uint32_t*>(a.codes)[4 * block + (lane & 3)] = word;
-  if (a.scales && (lane & 3) == 0) a.scales[block] = static_cast<uint8_t>(byte);
+  reinterpret_cast<uint32_t*>(a.codes)[4 * block + (lane & 3)] = word;
+  if ((lane & 3) == 0) a.scales[block] = static_cast<uint8_t>(byte);
   if (!a.hat) return;
   const int64_t left = a.d - c;
   const int64_t at = int64_t(row) * a.ldh + c;
@@ -310,7 +310,6 @@ size_t mx_matmul_t_ws_bytes(int64_t n, int64_t m, int64_t d, bool gated) {
 
 gptq_status launch_mx_matmul_t(const uint16_t* dY, int64_t lddy, int64_t n, const Mx& w, int64_t d,
                                uint16_t* dX, int64_t lddx, void* ws, hipStream_t st) {
-  if (n == 0) return GPTQ_OK;
   Carver c(ws);
   const TurnWs b = carve_turn(c, n, w.rows, d, false);
   const int64_t mp = round_up(w.rows, 64);
@@ -336,7 +335,6 @@ gptq_status launch_mx_gated_backward(const uint16_t* dY, int64_t lddy, int64_t n
                                      const Mx& gate, const Mx& up, int64_t d, int act,
                                      uint16_t* dX, int64_t lddx, uint16_t* dGU, void* ws,
                                      hipStream_t st) {
-  if (n == 0) return GPTQ_OK;
   const int64_t m = gate.rows, mp = round_up(m, 64);
   const bool vec = lddy % 8 == 0 && ldg % 8 == 0 && reinterpret_cast<uintptr_t>(dY) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(G) % 16 == 0 &&

@@ -792,7 +792,6 @@ gptq_status launch_tokens(const void* logits, gptq_dtype dt, int64_t n, int64_t 
                           const int32_t* token, float temp, int64_t k, float* logp, float* entropy,
                           float* lse, float* stats, float* top, int32_t* idx, void* ws,
                           hipStream_t st) {
-  if (n == 0) return GPTQ_OK;
   Carver c(ws);
   const TokenWs w = carve_tokens(c, n, vocab, k);
   TokenArgs a{logits, ldl, int(vocab), int(k), parts_of(n, vocab, k), 0, k > kThreads ? 2 * kCap : kCap,
@@ -811,7 +810,6 @@ gptq_status launch_tokens_grad(const void* logits, gptq_dtype dt, int64_t n, int
                                int64_t ldl, const float* stats, const int32_t* token, float temp,
                                const float* grad_logp, const float* grad_entropy, void* dlogits,
                                int64_t ldd, hipStream_t st) {
-  if (n == 0) return GPTQ_OK;
   TokenGradArgs a{logits, n, ldl, int(vocab), int(ceil_div(vocab, 8 * kGradThreads * kGradVecs)),
                   1.0 / double(temp), stats, token, grad_logp, grad_entropy, dlogits, ldd};
   const dim3 grid = flat_grid(n * a.pieces);

@@ -379,7 +379,6 @@ bool mx_decode_takes(int64_t n, int64_t m, int64_t d, int form, bool gated) {
 
 gptq_status launch_mx_decode(const MxInput& x, const Mx& w, const Mx& up, const MxOutput& y,
                              hipStream_t st) {
-  if (x.n == 0) return GPTQ_OK;
   const DecodeArgs a{x, w, up, y, x.ldx % 8 == 0 && reinterpret_cast<uintptr_t>(x.X) % 16 == 0};
   switch (x.form) {
     case GPTQ_MX_BF16: return launch_form<GPTQ_MX_BF16>(a, st);
