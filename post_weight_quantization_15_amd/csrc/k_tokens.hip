@@ -191,18 +191,24 @@ __device__ inline void sort_by_rank(uint64_t* buf, int count) {
   __syncthreads();
 }
 
-// A lane has the (k / p)-th largest (rounded up) of its own list, as an order number.  What p of
-// the lists reach, k numbers of all lists reach: the p-th largest lane's.  The last six bits make
-// way for the lane's number, which makes lanes different, and come back as zeros (a lower bound).
-__device__ inline uint32_t reached_by(uint32_t order, int p) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t key = (order & ~63u) | static_cast<uint32_t>(lane);
-  int rank = 0;
+// The wave's order numbers ranked.  The last six bits make way for the lane's number, which makes
+// lanes different, and come back as zeros (a lower bound).
+struct Ranked {
+  uint32_t key;
+  int rank;                                  // lanes above
+};
+__device__ inline Ranked rank_lanes(uint32_t order) {
+  Ranked r{(order & ~63u) | (threadIdx.x & 63u), 0};
 #pragma unroll 8
   for (int l = 0; l < 64; ++l)
-    rank += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), l)) > key;
+    r.rank += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(r.key), l)) > r.key;
+  return r;
+}
+// What p lanes reach: the p-th largest lane's, 1 <= p <= 64.  Where a lane has the (k / p)-th
+// largest (rounded up) of its own list, k numbers of all lists reach it.
+__device__ inline uint32_t reached_by(const Ranked& r, int p) {
   return static_cast<uint32_t>(__builtin_amdgcn_readlane(
-             static_cast<int>(key), __builtin_ctzll(__ballot(rank == p - 1)))) & ~63u;
+             static_cast<int>(r.key), __builtin_ctzll(__ballot(r.rank == p - 1)))) & ~63u;
 }
 
 struct TokenArgs {
@@ -465,19 +471,11 @@ __global__ __launch_bounds__(kThreads, 6) void tokens_kernel(TokenArgs a) {
             for (int e = 0; e < E; e += 2)
               most = max3(most, cell_of<DT>(ring[u][i], e), cell_of<DT>(ring[u][i], e + 1));
           }
-      // last six bits in place of the lane's number, which makes them different
-      const uint32_t key = (order_of(most) & ~63u) | static_cast<uint32_t>(lane);
-      int rank = 0;
-#pragma unroll 8
-      for (int l = 0; l < 64; ++l)
-        rank += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), l)) > key;
+      const Ranked lanes = rank_lanes(order_of(most));
 #pragma unroll
       for (int g = 0; g < kBars; ++g) {
         const int want = (a.k + (1 << g) - 1) >> g;
-        uint32_t pick = 0u;
-        if (want <= 64)
-          pick = static_cast<uint32_t>(__builtin_amdgcn_readlane(
-                     static_cast<int>(key), __builtin_ctzll(__ballot(rank == want - 1)))) & ~63u;
+        const uint32_t pick = want <= 64 ? reached_by(lanes, want) : 0u;
         if (lane == 0) bars[g][wv] = pick;
       }
       __syncthreads();
@@ -626,8 +624,8 @@ __global__ __launch_bounds__(kThreads) void tokens_join_kernel(TokenArgs a) {
     const uint64_t* mine = in + min(lane, a.parts - 1) * a.k;
     const uint32_t all = order_in(mine[(a.k + a.parts - 1) / a.parts - 1]);
     const uint32_t some = order_in(mine[(a.k + few - 1) / few - 1]);
-    const uint32_t x = reached_by(lane < a.parts ? all : 0u, a.parts);
-    const uint32_t y = reached_by(lane < a.parts ? some : 0u, few);
+    const uint32_t x = reached_by(rank_lanes(lane < a.parts ? all : 0u), a.parts);
+    const uint32_t y = reached_by(rank_lanes(lane < a.parts ? some : 0u), few);
     bar = uint64_t(max(x, y)) << 18;
   }
   __syncthreads();
