@@ -13,8 +13,8 @@ namespace {
 // block's largest magnitude goes round by two exchanges.  A wave takes runs of
 // 512 values.  All of it exact but the rounding itself, which the hardware's
 // conversion does (nearest even, saturating).  One reading and one writing: bound by
-// bytes (11008 x 4096 bf16 with the rounded values too, 70 us: 5.4 TB/s, as part of it
-// stays in the last cache; small ones by the launch).
+// bytes (11008 x 4096 with the rounded values too: fp32 70 us, 5.5 TB/s, bf16 33 us, 6.2 TB/s, as part
+// of it stays in the last cache; small ones by the launch).
 // ---------------------------------------------------------------------------
 struct QuantizeArgs {
   const void* X;
@@ -210,8 +210,10 @@ __global__ __launch_bounds__(256) void mx_turn_kernel(Mx w, Mx up, unsigned by_o
 // The gated block's elementwise gradient
 // ---------------------------------------------------------------------------
 // dGU[t][j] = dY U act'(G), dGU[t][mp + j] = dY act(G); zeros in the padding.  Computed in fp32
-// and rounded to bf16 once, as the next product's operands and the layers' weight gradients take
-// them.  Bound by bytes.
+// and rounded to bf16 once, for the next product as for the layers' weight gradients, so that
+// both see the same factors.  dX is off by 0.0023 of itself for that (mean square), 0.0017 of which
+// is its own rounding; two bf16 parts of each factor would leave that alone at twice the product's
+// operations.  Bound by bytes.
 __global__ __launch_bounds__(256) void mx_gate_grad_kernel(const uint16_t* __restrict__ dY,
                                                            int64_t lddy,
                                                            const uint16_t* __restrict__ G,

@@ -11,7 +11,7 @@
 // cancels.  Cells are exponentiated in fp32 and summed in fp32 for 32 cells of a thread,
 // in fp64 beyond; a cell that becomes the largest is counted apart, as its 1 would leave
 // a confident row's other cells no bits in an fp32 sum.  In a row without order a wave's largest
-// rises some ln(vocab / 512) times.
+// rises in some ln(vocab / 2048) steps (all moves together take 1 to 3 % of the time).
 //
 // The largest k: cells pass a bar that only rises.  The first bar comes from the
 // lanes' maxima over the cells at hand (a step's and those whose loads are ahead of it):
@@ -20,13 +20,13 @@
 // different; where many are there, the k-th of them, found digit by digit, is
 // the new bar.  A cell later in the row has to exceed it: an equal one has the higher
 // id (so the cells behind the last whole vector become candidates with the last step, though
-// they are read first).  In a row without order some k ln(vocab) cells pass, so the selection is a comparison
-// per 16 bytes; a row that rises all along selects at each look (1024 rows of 128000 fp32
-// values: 1500 us where the same values in disorder take 114).  Measured, bf16
-// rows: 4096 of 128000 take 232 us without alternatives (4.5 TB/s of one reading), 272 with
-// k = 64, 435 with 256, 619 with 512; one row of 128000, in 63 parts of its own workgroups
-// and joined by a second launch, 18 us with k = 20, of which the launches' kernels are 9
-// and 8: two readings' latency, a selection and the joining one.
+// they are read first).  In a row without order some k ln(vocab) cells pass, so the selection
+// is a comparison per 16 bytes; a row that rises all along selects at each look (k = 64, 1024
+// rows of 128000 fp32 values: 1460 us, in disorder 117; 4096 of bf16: 6260 and 285).  Measured,
+// bf16 rows: 4096 of 128000 take 197 us without alternatives (5.3 TB/s of one reading, part of it
+// from the last cache), 285 with k = 64, 443 with 256, 638 with 512; one row of 128000, in 63
+// parts of its own workgroups and joined by a second launch, 17 to 19 us with k = 20, of which the
+// launches' kernels are 9 and 8: two readings' latency, a selection and the joining one.
 #include <type_traits>
 
 #include "lora.h"
@@ -66,7 +66,7 @@ __device__ inline float cell_of(const u32x4& v, int i) {
   return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w >> (16 * (i & 1)))));
 }
 
-// The larger of three, numbers before NaN.
+// The larger of three, numbers before quiet NaN (a signalling NaN may make the result NaN).
 __device__ inline float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
