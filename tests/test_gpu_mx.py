@@ -186,9 +186,11 @@ def test_forms_agree_and_runs_repeat(dev, n, d, m):
 def test_forms_agree_where_the_last_block_is_short(dev, n, m, d):
     """Sizes where a block more or less would choose another kernel; scales so far apart that
     sums are not exact."""
-    rng = np.random.default_rng([n, m, d])
-    (Wg, _), (Wu, _) = layer(rng, m, d, dev, 100, 130), layer(rng, m, d, dev, 100, 130)
-    X = rows(rng, n, d, 0.1).to(dev)
+    g = torch.Generator(device=dev).manual_seed(n)
+    nb = -(-d // 32)
+    Wg, Wu = ((torch.randint(0, 256, (m, 16 * nb), generator=g, device=dev, dtype=torch.uint8),
+               torch.randint(100, 130, (m, nb), generator=g, device=dev, dtype=torch.uint8)) for _ in range(2))
+    X = torch.randn(n, d, generator=g, device=dev).to(BF)
     q = gq.gptq_mx_quantize(X)
     codes = dict(x_scales=q["scales"])
     assert torch.equal(gq.gptq_mx_matmul(X, *Wg, quantize_x=True), gq.gptq_mx_matmul(q["codes"], *Wg, **codes))
